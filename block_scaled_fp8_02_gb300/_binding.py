@@ -33,7 +33,8 @@ EXPORTS = ("bfp8_group_quant", "bfp8_group_quant_ex", "bfp8_scale_ceil_ue8m0", "
            "bfp8_status_string", "bfp8_device_status", "bfp8_selftest_bounded_wait",
            "bfp8_version", "bfp8_gemm_noalloc", "bfp8_gemm_grouped",
            "bfp8_gemm_grouped_workspace_size", "bfp8_gemm_fused", "bfp8_gemm_fused_workspace_size",
-           "bfp8_linear", "bfp8_linear_workspace_size")
+           "bfp8_linear", "bfp8_linear_workspace_size", "bfp8_rmsnorm_quant", "bfp8_kv_cache_write",
+           "bfp8_kv_cache_read", "bfp8_paged_attention", "bfp8_paged_attention_workspace_size")
 
 
 class BFP8Error(RuntimeError):
@@ -55,6 +56,26 @@ class PlanInfo(ctypes.Structure):
                 ("dp_tiles", ctypes.c_int64), ("sk_units", ctypes.c_int64),
                 ("relayout", ctypes.c_int), ("workspace_bytes", ctypes.c_size_t),
                 ("cluster", ctypes.c_int), ("gemv", ctypes.c_int), ("pair", ctypes.c_int)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+                ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("reserved", ctypes.c_int),
+                ("stride_page", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64), ("scale_stride_page", ctypes.c_int64),
+                ("scale_stride_head", ctypes.c_int64)]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("total_q", ctypes.c_int64), ("num_heads", ctypes.c_int), ("batch", ctypes.c_int),
+                ("q_stride_token", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+                ("out_stride_token", ctypes.c_int64), ("out_stride_head", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+                ("max_pages", ctypes.c_int), ("max_q_len", ctypes.c_int), ("max_kv_len", ctypes.c_int64),
+                ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("softmax_scale", ctypes.c_float),
+                ("causal", ctypes.c_int), ("window", ctypes.c_int), ("reserved", ctypes.c_int)]
 
 
 _lock = threading.Lock()
@@ -125,6 +146,19 @@ def lib():
             L.bfp8_gemm_grouped_workspace_size.argtypes = [i64, i64, i64, i32,
                                                            ctypes.POINTER(GemmOptions), i32,
                                                            ctypes.POINTER(sz)]
+            L.bfp8_rmsnorm_quant.restype = i32
+            L.bfp8_rmsnorm_quant.argtypes = [P, i32, i64, P, i64, P, i64, P, i32, ctypes.c_float, i64, i64,
+                                             P, i64, i32, i32, P, i64, P, i64, P]
+            L.bfp8_kv_cache_write.restype = i32
+            L.bfp8_kv_cache_write.argtypes = [P, P, i32, i64, i64, i64, i64, P, i64, i32,
+                                              ctypes.POINTER(KVCacheDesc), P]
+            L.bfp8_kv_cache_read.restype = i32
+            L.bfp8_kv_cache_read.argtypes = [ctypes.POINTER(KVCacheDesc), P, i64, i32, P, i64, P, i64, P]
+            L.bfp8_paged_attention.restype = i32
+            L.bfp8_paged_attention.argtypes = [ctypes.POINTER(AttentionArgs), ctypes.POINTER(KVCacheDesc),
+                                               P, sz, P]
+            L.bfp8_paged_attention_workspace_size.restype = i32
+            L.bfp8_paged_attention_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
             _lib = L
     return _lib
 
@@ -500,3 +534,187 @@ def linear(x: torch.Tensor, B: torch.Tensor, Bs: torch.Tensor, out: torch.Tensor
     # the quantisation kernel writes neither B nor Bs: the GEMM may start
     # streaming the weights while it runs
     return bfp8_gemm(q, B, s, Bs, out=out, options={"prefetch_weights": 1}, stream=stream)
+
+
+_IN_DTYPE = {torch.bfloat16: BFP8_IN_BF16, torch.float32: BFP8_IN_F32}
+
+
+def _rows(t: torch.Tensor, name: str, M: int, K: int, dtype) -> int:
+    """Row stride of a [M, K] tensor with unit inner stride."""
+    if t.shape != (M, K) or t.dtype != dtype or (K > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape ({M}, {K}) with unit inner stride")
+    return t.stride(0) if M > 1 else K
+
+
+def bfp8_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None, residual: torch.Tensor | None = None,
+                       residual_out: torch.Tensor | None = None, eps: float = 1e-6,
+                       col_major: bool = True, ue8m0: bool = False, want_y: bool = False,
+                       quantise: bool = True, stream=None):
+    """Residual addition, RMS norm and 1 x 128 group quantisation of x [M, K] (bf16 or fp32) in one pass.
+
+    h = x + residual goes to residual_out (default: residual itself, in place); y = h * rsqrt(mean(h^2) +
+    eps) * weight.  Returns (q, s), the codes and scales of y as bfp8_group_quant returns them; with
+    want_y, (q, s, y) with y in bf16; without quantise q and s are None."""
+    if x.dim() != 2 or x.dtype not in _IN_DTYPE:
+        raise ValueError("x must be a 2-D bfloat16 or float32 tensor")
+    M, K = x.shape
+    ld_x = _rows(x, "x", M, K, x.dtype)
+    r_ptr = ro_ptr = w_ptr = y_ptr = q_ptr = s_ptr = None
+    ld_r = ld_ro = ld_q = ld_s = K
+    if residual is not None:
+        ld_r = _rows(residual, "residual", M, K, x.dtype)
+        r_ptr = residual.data_ptr()
+        if residual_out is None:
+            residual_out = residual
+    if residual_out is not None:
+        ld_ro = ld_r if residual_out is residual else _rows(residual_out, "residual_out", M, K, x.dtype)
+        ro_ptr = residual_out.data_ptr()
+    w_dtype = BFP8_IN_BF16
+    if weight is not None:
+        if weight.dtype not in _IN_DTYPE or weight.shape != (K,) or not weight.is_contiguous():
+            raise ValueError(f"weight must be a contiguous bfloat16 or float32 tensor of shape ({K},)")
+        w_dtype, w_ptr = _IN_DTYPE[weight.dtype], weight.data_ptr()
+    q = s = y = None
+    if quantise:
+        G = (K + 127) // 128
+        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+        if col_major:
+            ld_s = (M + 3) // 4 * 4
+            st = torch.empty((G, ld_s), dtype=torch.float32, device=x.device)
+            s = st[:, :M].t()
+        else:
+            ld_s = G
+            s = st = torch.empty((M, G), dtype=torch.float32, device=x.device)
+        q_ptr, s_ptr = q.data_ptr(), st.data_ptr()
+    if want_y:
+        y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+        y_ptr = y.data_ptr()
+    rc = lib().bfp8_rmsnorm_quant(x.data_ptr(), _IN_DTYPE[x.dtype], ld_x, r_ptr, ld_r, ro_ptr, ld_ro, w_ptr,
+                                  w_dtype, eps, M, K, y_ptr, K, int(col_major),
+                                  SCALE_UE8M0 if ue8m0 else SCALE_FP32, q_ptr, ld_q, s_ptr, ld_s,
+                                  _stream_ptr(stream))
+    _check(rc, "bfp8_rmsnorm_quant")
+    return (q, s, y) if want_y else (q, s)
+
+
+class KVCache:
+    """A paged e4m3 cache: codes k, v [pages, kv_heads, page_size, head_dim] (float8_e4m3fn, any strides with
+    unit inner stride) and fp32 scales k_scale, v_scale [pages, kv_heads, page_size] (unit inner stride).
+    The tensors stay the caller's; slot = page * page_size + offset."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "_desc")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        shape, st, ss = k.shape, k.stride(), k_scale.stride()
+        if len(shape) != 4 or v.shape != shape or k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+            raise ValueError("k and v must be [pages, kv_heads, page_size, head_dim], the scales [pages, kv_heads, page_size]")
+        if k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
+            raise ValueError("k and v must be float8_e4m3fn")
+        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+            raise ValueError("k_scale and v_scale must be float32")
+        if st[3] != 1 or ss[2] != 1 or v.stride() != st or v_scale.stride() != ss:
+            raise ValueError("k and v (and the two scale tensors) must have the same strides, the inner one 1")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        P, H, page, D = shape
+        self._desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, page, H, D, 0,
+                                 st[0], st[1] if H > 1 else max(st[1], page * D), st[2], ss[0],
+                                 ss[1] if H > 1 else max(ss[1], page))
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, page_size: int, head_dim: int, device) -> "KVCache":
+        """A zero-filled cache of its own."""
+        def codes():
+            return torch.zeros((pages, kv_heads, page_size, head_dim), dtype=torch.uint8,
+                               device=device).view(torch.float8_e4m3fn)
+
+        def scales():
+            return torch.zeros((pages, kv_heads, page_size), dtype=torch.float32, device=device)
+        return cls(codes(), codes(), scales(), scales())
+
+    @property
+    def shape(self):
+        return self.k.shape
+
+
+def _check_slots(slots: torch.Tensor, T: int | None = None) -> int:
+    if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous 1-D int64 tensor")
+    if T is not None and slots.shape[0] != T:
+        raise ValueError(f"slots has {slots.shape[0]} entries for {T} tokens")
+    return slots.shape[0]
+
+
+def bfp8_kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots: torch.Tensor,
+                        ue8m0: bool = False, stream=None) -> None:
+    """Quantise new keys and values k, v [T, kv_heads, head_dim] (bf16 or fp32; token and head strides free)
+    into the cache at slots [T] (int64; negative: skipped), one fp32 scale per (token, head)."""
+    _, H, _, D = cache.k.shape
+    if k.dim() != 3 or k.shape[1:] != (H, D) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [T, {H}, {D}]")
+    if k.dtype not in _IN_DTYPE or v.dtype != k.dtype:
+        raise ValueError("k and v must both be bfloat16 or float32")
+    if k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("k and v must have unit inner stride")
+    T = _check_slots(slots, k.shape[0])
+    _check(lib().bfp8_kv_cache_write(k.data_ptr(), v.data_ptr(), _IN_DTYPE[k.dtype], k.stride(0), k.stride(1),
+                                     v.stride(0), v.stride(1), slots.data_ptr(), T,
+                                     SCALE_UE8M0 if ue8m0 else SCALE_FP32, ctypes.byref(cache._desc),
+                                     _stream_ptr(stream)), "bfp8_kv_cache_write")
+
+
+def bfp8_kv_cache_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, stream=None):
+    """The keys and values of slots [T] (int64; negative: zeros) as (k, v) [T, kv_heads, head_dim] in bf16 or fp32."""
+    if dtype not in _IN_DTYPE:
+        raise ValueError("dtype must be bfloat16 or float32")
+    T = _check_slots(slots)
+    _, H, _, D = cache.k.shape
+    k = torch.empty((T, H, D), dtype=dtype, device=slots.device)
+    v = torch.empty((T, H, D), dtype=dtype, device=slots.device)
+    _check(lib().bfp8_kv_cache_read(ctypes.byref(cache._desc), slots.data_ptr(), T, _IN_DTYPE[dtype], k.data_ptr(),
+                                    H * D, v.data_ptr(), H * D, _stream_ptr(stream)), "bfp8_kv_cache_read")
+    return k, v
+
+
+def bfp8_paged_attention_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int, max_q_len: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().bfp8_paged_attention_workspace_size(num_heads, num_kv_heads, head_dim, max_q_len, ctypes.byref(n)),
+           "bfp8_paged_attention_workspace_size")
+    return int(n.value)
+
+
+def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
+                         kv_lens: torch.Tensor, max_q_len: int, max_kv_len: int, scale: float | None = None,
+                         causal: bool = True, window: int = 0, return_lse: bool = False,
+                         out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Attention of the newest tokens q [total_q, heads, head_dim] (bf16) of each sequence over its context in the
+    paged cache: sequence b's rows are cu_q[b] .. cu_q[b+1] (int32 [batch + 1]), its context kv_lens[b] tokens
+    (int32 [batch], the new ones included) on the pages block_table[b] (int32 [batch, max_pages]).  max_q_len and
+    max_kv_len bound the lengths; scale defaults to head_dim ** -0.5.  Returns out (bf16, like q), or (out, lse)
+    with lse fp32 [total_q, heads]."""
+    P, H, page, D = cache.k.shape
+    if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
+        raise ValueError(f"q must be bfloat16 [total_q, heads, {D}] with unit inner stride")
+    T, Hq, _ = q.shape
+    B = kv_lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != B or (B > 0 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be [{B}, max_pages] with unit inner stride")
+    if kv_lens.dim() != 1 or cu_q.shape != (B + 1,) or not kv_lens.is_contiguous() or not cu_q.is_contiguous():
+        raise ValueError("kv_lens must be a contiguous [batch] tensor and cu_q a contiguous [batch + 1] one")
+    if block_table.dtype != torch.int32 or cu_q.dtype != torch.int32 or kv_lens.dtype != torch.int32:
+        raise ValueError("block_table, cu_q and kv_lens must be int32")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.stride(2) != 1:
+        raise ValueError("out must be bfloat16, shaped like q, with unit inner stride")
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    if workspace is None:
+        workspace = workspace_for(bfp8_paged_attention_workspace_size(Hq, H, D, max_q_len), q.device, stream)
+    a = AttentionArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else None, T, Hq, B, q.stride(0),
+                      q.stride(1), out.stride(0), out.stride(1), block_table.data_ptr(),
+                      block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1], max_q_len,
+                      max_kv_len, cu_q.data_ptr(), kv_lens.data_ptr(), D ** -0.5 if scale is None else scale,
+                      int(causal), window, 0)
+    _check(lib().bfp8_paged_attention(ctypes.byref(a), ctypes.byref(cache._desc), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
+           "bfp8_paged_attention")
+    return (out, lse) if return_lse else out

@@ -52,6 +52,17 @@ bfp8_status set_last_error(bfp8_status st, const char* msg) {
   return st;
 }
 
+bfp8_status set_last_errorf(bfp8_status st, const char* fmt, ...) {
+  if (st == BFP8_OK) return ok();
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  t_last_error = buf;
+  return st;
+}
+
 namespace {
 
 constexpr int kMaxCluster = 8;   // portable cluster size
@@ -213,6 +224,41 @@ bfp8_status encode_output(CUtensorMap* map, void* ptr, int64_t rows, int64_t col
                 (int)r, (long long)rows, (long long)cols);
   return BFP8_OK;
 }
+
+}  // namespace
+
+bfp8_status device_for_call(int* sms, int** err) {
+  DevInfo d;
+  const bfp8_status st = current_device(&d, nullptr);
+  if (st != BFP8_OK) return st;
+  *sms = d.sms;
+  *err = d.err;
+  return BFP8_OK;
+}
+
+bfp8_status encode_bytes_tiled(CUtensorMap* map, const void* ptr, int rank, const uint64_t* dims,
+                               const uint64_t* strides, const uint32_t* box, int swizzle_bytes) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  bfp8_status st = get_encoder(&enc);
+  if (st != BFP8_OK) return st;
+  cuuint64_t d[5], t[4];
+  cuuint32_t b[5], e[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    e[i] = 1u;
+    if (i + 1 < rank) t[i] = strides[i];
+  }
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
+                   const_cast<void*>(ptr), d, t, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(BFP8_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a rank-%d byte tensor", (int)r, rank);
+  return BFP8_OK;
+}
+
+namespace {
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

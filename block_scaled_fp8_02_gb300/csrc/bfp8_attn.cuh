@@ -1,0 +1,62 @@
+// bfp8_attn.cuh -- what the attention kernels share: their arguments and the
+// lengths of a sequence as they stand on the device.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "bfp8_kvcache.cuh"
+
+namespace bfp8 {
+
+struct AttnArgs {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* lse;                   // or nullptr
+  int64_t q_st, q_sh, o_st, o_sh;
+  const int32_t* table;
+  int64_t ld_table;
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  int64_t total_q;
+  int64_t max_kv;               // bound of kv_lens: host bound and table width
+  int32_t heads, group;         // query heads, query heads a kv head
+  int32_t batch;
+  int32_t max_q;
+  int32_t causal;
+  int32_t window;
+  float scale;
+  CacheView c;
+  int* err;
+};
+
+// Sequence b: its rows of q and its context, clamped to the bounds, so that no
+// length can lead out of a buffer.
+struct SeqLens {
+  int64_t row0;
+  int32_t q_len;
+  int32_t kv_len;
+};
+__device__ __forceinline__ SeqLens seq_lens(const AttnArgs& a, int b) {
+  SeqLens s;
+  int64_t c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
+  c0 = c0 < 0 ? 0 : c0 > a.total_q ? a.total_q : c0;
+  c1 = c1 < c0 ? c0 : c1 > a.total_q ? a.total_q : c1;
+  s.row0 = c0;
+  s.q_len = static_cast<int32_t>(c1 - c0 < a.max_q ? c1 - c0 : a.max_q);
+  const int64_t n = a.kv_lens[b];
+  s.kv_len = static_cast<int32_t>(n < 0 ? 0 : n < a.max_kv ? n : a.max_kv);
+  return s;
+}
+
+// Tokens [lo, hi) that the new token at position p sees.
+__device__ __forceinline__ void seen_range(const AttnArgs& a, int32_t kv_len, int32_t p, int32_t& lo,
+                                           int32_t& hi) {
+  hi = a.causal ? p + 1 : kv_len;
+  lo = a.window > 0 ? p - a.window + 1 : 0;
+  if (lo < 0) lo = 0;
+  if (hi > kv_len) hi = kv_len;
+}
+
+}  // namespace bfp8

@@ -13,6 +13,7 @@ enum : int {
   kDevTimeoutEpilogue = 3,
   kDevTimeoutTail = 4,
   kDevBadGroupedLayout = 5,   // grouped_layout not non-decreasing multiples of 128
+  kDevBadCacheIndex = 6,      // a slot or page number outside the cache
 };
 
 __device__ __forceinline__ void report_failure(int* err, int code) {

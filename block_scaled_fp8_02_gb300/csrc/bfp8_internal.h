@@ -17,6 +17,17 @@ namespace bfp8 {
 // Records `msg` as the calling thread's bfp8_last_error() and returns st.
 bfp8_status set_last_error(bfp8_status st, const char* msg);
 
+// The same with a printf-style reason; BFP8_OK clears the reason.
+bfp8_status set_last_errorf(bfp8_status st, const char* fmt, ...);
+// The current device if it is one the library runs on: its SM count and the
+// address of its failure word.
+bfp8_status device_for_call(int* sms, int** err);
+// The driver's tensor-map encoder (tiled, 128- or 64-byte swizzle by
+// `swizzle_bytes`, zero fill): `rank` dims of bytes, strides of dims 1.. in
+// bytes.
+bfp8_status encode_bytes_tiled(CUtensorMap* map, const void* ptr, int rank, const uint64_t* dims,
+                               const uint64_t* strides, const uint32_t* box, int swizzle_bytes);
+
 struct GemmArgs;
 
 // Per-token group quantisation launcher (bfp8_quant.cu); ue8m0: scales

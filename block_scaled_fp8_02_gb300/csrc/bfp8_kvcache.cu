@@ -1,0 +1,314 @@
+// bfp8_kvcache.cu -- the paged e4m3 key/value cache: quantising new tokens into
+// it and reading tokens back (sm_103a).
+//
+//   write: s = max(amax_d |x|, 1e-10) / 448, code = e4m3(x / s) per (token, head)
+//   read:  x' = code * s, one rounding
+//
+// Both are streams of rows of head_dim elements, (token, k or v, head) in that
+// order so that neighbouring lanes read neighbouring heads of a token.  Bound
+// by memory: write 2 bytes in and 1 + 4 / head_dim out an element (bf16), read
+// the other way round.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "bfp8_devstatus.cuh"
+#include "bfp8_internal.h"
+#include "bfp8_kvcache.cuh"
+#include "bfp8_ptx.cuh"
+#include "bfp8_vec8.cuh"
+
+namespace bfp8 {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kRowsInFlight = 4;      // warp steps whose loads are issued together
+
+struct WriteArgs {
+  const void* k;
+  const void* v;
+  int64_t k_st, k_sh, v_st, v_sh;     // element strides
+  const int64_t* slots;
+  uint32_t rows;                      // T * 2 * H
+  int32_t vec;
+  CacheView c;
+  int* err;
+};
+
+template <bool kF32, bool kUe8m0, int D>
+__global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_constant__ WriteArgs a) {
+  using T = typename std::conditional<kF32, float, uint16_t>::type;
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, li = lane % LPR;
+  const uint32_t warp0 = blockIdx.x * kWarps + (threadIdx.x >> 5), nw = gridDim.x * kWarps;
+  const uint32_t H = a.c.heads;
+  const int64_t nslots = a.c.num_pages * a.c.page_size;
+  griddep_launch_dependents();
+  griddep_wait();
+  for (uint32_t w = warp0; static_cast<uint64_t>(w) * RPW < a.rows; w += nw * kRowsInFlight) {
+    float x[kRowsInFlight][8];
+    int64_t slot[kRowsInFlight];
+    uint32_t head[kRowsInFlight];
+    bool is_v[kRowsInFlight];
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      const uint64_t row = (static_cast<uint64_t>(w) + static_cast<uint64_t>(u) * nw) * RPW + sub;
+      slot[u] = -1;
+      const bool ok = row < a.rows;
+      const uint32_t r = ok ? static_cast<uint32_t>(row) : 0u;
+      const uint32_t pair = r / H, t = pair >> 1;
+      head[u] = r - pair * H;
+      is_v[u] = pair & 1;
+      if (ok) slot[u] = __ldg(a.slots + t);
+      const T* src = is_v[u] ? static_cast<const T*>(a.v) + t * a.v_st + head[u] * a.v_sh
+                             : static_cast<const T*>(a.k) + t * a.k_st + head[u] * a.k_sh;
+      load8<kF32>(src + li * 8, a.vec, ok ? 8 : 0, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      float scale;
+      uint32_t lo, hi;
+      quant8<LPR, kUe8m0>(x[u], scale, lo, hi);
+      if (slot[u] < 0) continue;
+      if (slot[u] >= nslots) {
+        report_failure(a.err, kDevBadCacheIndex);
+        continue;
+      }
+      const int64_t page = slot[u] >> a.c.page_shift, o = slot[u] & (a.c.page_size - 1);
+      uint8_t* q = (is_v[u] ? a.c.v : a.c.k) + page * a.c.st_page + head[u] * a.c.st_head + o * a.c.st_tok;
+      *reinterpret_cast<uint2*>(q + li * 8) = make_uint2(lo, hi);
+      if (li == 0) (is_v[u] ? a.c.vs : a.c.ks)[page * a.c.ss_page + head[u] * a.c.ss_head + o] = scale;
+    }
+  }
+}
+
+struct ReadArgs {
+  void* k;                            // or nullptr
+  void* v;                            // or nullptr
+  int64_t k_st, v_st;                 // element strides of tokens
+  const int64_t* slots;
+  uint32_t rows;                      // T * nkv * H
+  uint32_t nkv;                       // 1: only one of k and v
+  int32_t vec;
+  CacheView c;
+  int* err;
+};
+
+template <bool kF32, int D>
+__global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_constant__ ReadArgs a) {
+  using T = typename std::conditional<kF32, float, __nv_bfloat16>::type;
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, li = lane % LPR;
+  const uint32_t warp0 = blockIdx.x * kWarps + (threadIdx.x >> 5), nw = gridDim.x * kWarps;
+  const uint32_t H = a.c.heads;
+  const int64_t nslots = a.c.num_pages * a.c.page_size;
+  griddep_launch_dependents();
+  griddep_wait();
+  for (uint32_t w = warp0; static_cast<uint64_t>(w) * RPW < a.rows; w += nw * kRowsInFlight) {
+    uint2 q[kRowsInFlight];
+    float s[kRowsInFlight];
+    T* dst[kRowsInFlight];
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      const uint64_t row = (static_cast<uint64_t>(w) + static_cast<uint64_t>(u) * nw) * RPW + sub;
+      dst[u] = nullptr;
+      q[u] = make_uint2(0u, 0u);
+      s[u] = 0.f;
+      if (row >= a.rows) continue;
+      const uint32_t r = static_cast<uint32_t>(row), pair = r / H, h = r - pair * H;
+      const uint32_t t = a.nkv == 2 ? pair >> 1 : pair;
+      const bool is_v = a.nkv == 2 ? (pair & 1) : a.k == nullptr;
+      dst[u] = static_cast<T*>(is_v ? a.v : a.k) + t * (is_v ? a.v_st : a.k_st) + h * D + li * 8;
+      const int64_t slot = __ldg(a.slots + t);
+      if (slot >= nslots) {
+        report_failure(a.err, kDevBadCacheIndex);
+      } else if (slot >= 0) {
+        const int64_t page = slot >> a.c.page_shift, o = slot & (a.c.page_size - 1);
+        q[u] = __ldg(reinterpret_cast<const uint2*>((is_v ? a.c.v : a.c.k) + page * a.c.st_page +
+                                                    h * a.c.st_head + o * a.c.st_tok + li * 8));
+        s[u] = __ldg((is_v ? a.c.vs : a.c.ks) + page * a.c.ss_page + h * a.c.ss_head + o);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      if (dst[u] == nullptr) continue;
+      float v[8], lo[4], hi[4];
+      e4m3x4_to_f32(q[u].x, lo);
+      e4m3x4_to_f32(q[u].y, hi);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = __fmul_rn(lo[e], s[u]);
+        v[4 + e] = __fmul_rn(hi[e], s[u]);
+      }
+      store8<kF32>(dst[u], a.vec, 8, v);
+    }
+  }
+}
+
+template <typename F, typename A>
+cudaError_t launch_rows(F* f, const A& a, uint64_t rows, int rpw, int num_sms, cudaStream_t stream) {
+  // 8 blocks of 8 warps a SM; each warp walks kRowsInFlight steps at a time
+  const uint64_t steps = (rows + rpw - 1) / rpw;
+  uint64_t blocks = (steps + kWarps - 1) / kWarps;
+  const uint64_t cap = static_cast<uint64_t>(num_sms) * 8;
+  if (blocks > cap) blocks = cap;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, a);
+}
+
+inline bool off_align(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+template <typename... V>
+bfp8_status bad(const char* fmt, V... v) {
+  return set_last_errorf(BFP8_ERR_INVALID_ARG, fmt, v...);
+}
+
+// Rows of one launch: the kernels index them in 32 bits with room for a step.
+constexpr int64_t kMaxRows = int64_t{1} << 31;
+
+}  // namespace
+
+bfp8_status check_cache(const bfp8_kv_cache* c, CacheView* view) {
+  if (!c) return bad("cache is null");
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale)
+    return bad("cache: null pointer (k=%p v=%p k_scale=%p v_scale=%p)", c->k, c->v, (void*)c->k_scale,
+               (void*)c->v_scale);
+  int shift = 4;
+  while (shift < 8 && (1 << shift) != c->page_size) ++shift;
+  if ((1 << shift) != c->page_size)
+    return bad("cache: page_size = %d (expected 16, 32, 64, 128 or 256)", c->page_size);
+  if (c->head_dim != 64 && c->head_dim != 128) return bad("cache: head_dim = %d (expected 64 or 128)", c->head_dim);
+  if (c->num_kv_heads < 1 || c->num_kv_heads > 65535)
+    return bad("cache: num_kv_heads = %d (expected 1 .. 65535)", c->num_kv_heads);
+  if (c->num_pages < 1 || c->num_pages >= (int64_t{1} << 31))
+    return bad("cache: num_pages = %lld", (long long)c->num_pages);
+  constexpr int64_t kMaxStride = int64_t{1} << 39;      // what a tensor map can hold
+  for (int64_t s : {c->stride_page, c->stride_head, c->stride_token})
+    if (s < c->head_dim || s >= kMaxStride) return bad("cache: code stride %lld (expected >= head_dim)", (long long)s);
+  for (int64_t s : {c->scale_stride_page, c->scale_stride_head})
+    if (s < c->page_size || s >= kMaxStride)
+      return bad("cache: scale stride %lld (expected >= page_size)", (long long)s);
+  if (c->stride_page % 16 || c->stride_head % 16 || c->stride_token % 16 || c->scale_stride_page % 4 ||
+      c->scale_stride_head % 4)
+    return set_last_errorf(BFP8_ERR_ALIGNMENT, "cache: strides must be multiples of 16 bytes");
+  if (off_align(c->k, 16) || off_align(c->v, 16) || off_align(c->k_scale, 16) || off_align(c->v_scale, 16))
+    return set_last_errorf(BFP8_ERR_ALIGNMENT, "cache: pointers must be 16-byte aligned");
+  view->k = static_cast<uint8_t*>(c->k);
+  view->v = static_cast<uint8_t*>(c->v);
+  view->ks = c->k_scale;
+  view->vs = c->v_scale;
+  view->num_pages = c->num_pages;
+  view->st_page = c->stride_page;
+  view->st_head = c->stride_head;
+  view->st_tok = c->stride_token;
+  view->ss_page = c->scale_stride_page;
+  view->ss_head = c->scale_stride_head;
+  view->page_size = c->page_size;
+  view->page_shift = shift;
+  view->heads = c->num_kv_heads;
+  view->dim = c->head_dim;
+  return BFP8_OK;
+}
+
+}  // namespace bfp8
+
+using namespace bfp8;
+
+extern "C" bfp8_status bfp8_kv_cache_write(const void* k, const void* v, int in_dtype,
+                                           int64_t k_stride_token, int64_t k_stride_head,
+                                           int64_t v_stride_token, int64_t v_stride_head,
+                                           const int64_t* slots, int64_t T, int scale_fmt,
+                                           const bfp8_kv_cache* cache, void* stream) {
+  WriteArgs a{};
+  bfp8_status st = check_cache(cache, &a.c);
+  if (st != BFP8_OK) return st;
+  if (in_dtype != BFP8_IN_BF16 && in_dtype != BFP8_IN_F32)
+    return bad("in_dtype = %d (expected BFP8_IN_BF16 or BFP8_IN_F32)", in_dtype);
+  if (scale_fmt != BFP8_SCALE_FP32 && scale_fmt != BFP8_SCALE_UE8M0)
+    return bad("scale_fmt = %d (expected BFP8_SCALE_FP32 or BFP8_SCALE_UE8M0)", scale_fmt);
+  if (T < 0) return bad("T = %lld", (long long)T);
+  if (T == 0) return set_last_error(BFP8_OK, "");
+  if (!k || !v || !slots) return bad("null pointer (k=%p v=%p slots=%p)", k, v, (const void*)slots);
+  for (int64_t s : {k_stride_token, k_stride_head, v_stride_token, v_stride_head})
+    if (s < 0) return bad("k and v strides must not be negative (got %lld)", (long long)s);
+  const int es = in_dtype == BFP8_IN_F32 ? 4 : 2;
+  if (off_align(k, es) || off_align(v, es) || off_align(slots, 8))
+    return set_last_errorf(BFP8_ERR_ALIGNMENT, "k, v or slots is not aligned to its element size");
+  if (T >= kMaxRows / (2 * a.c.heads))
+    return set_last_errorf(BFP8_ERR_UNSUPPORTED, "T x heads too large for one launch");
+  int sms = 0;
+  if ((st = device_for_call(&sms, &a.err)) != BFP8_OK) return st;
+  a.k = k;
+  a.v = v;
+  a.k_st = k_stride_token;
+  a.k_sh = k_stride_head;
+  a.v_st = v_stride_token;
+  a.v_sh = v_stride_head;
+  a.slots = slots;
+  a.rows = static_cast<uint32_t>(T * 2 * a.c.heads);
+  a.vec = !off_align(k, 16) && !off_align(v, 16) && k_stride_token * es % 16 == 0 &&
+          k_stride_head * es % 16 == 0 && v_stride_token * es % 16 == 0 && v_stride_head * es % 16 == 0;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const bool f32 = in_dtype == BFP8_IN_F32, ue = scale_fmt == BFP8_SCALE_UE8M0;
+  auto go = [&](auto f128, auto f64) {
+    return a.c.dim == 128 ? launch_rows(f128, a, a.rows, 2, sms, cs) : launch_rows(f64, a, a.rows, 4, sms, cs);
+  };
+  const cudaError_t e =
+      f32 ? (ue ? go(kv_write_kernel<true, true, 128>, kv_write_kernel<true, true, 64>)
+                : go(kv_write_kernel<true, false, 128>, kv_write_kernel<true, false, 64>))
+          : (ue ? go(kv_write_kernel<false, true, 128>, kv_write_kernel<false, true, 64>)
+                : go(kv_write_kernel<false, false, 128>, kv_write_kernel<false, false, 64>));
+  if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "cache write launch: %s", cudaGetErrorString(e));
+  return set_last_error(BFP8_OK, "");
+}
+
+extern "C" bfp8_status bfp8_kv_cache_read(const bfp8_kv_cache* cache, const int64_t* slots, int64_t T,
+                                          int out_dtype, void* k_out, int64_t k_stride_token,
+                                          void* v_out, int64_t v_stride_token, void* stream) {
+  ReadArgs a{};
+  bfp8_status st = check_cache(cache, &a.c);
+  if (st != BFP8_OK) return st;
+  if (out_dtype != BFP8_IN_BF16 && out_dtype != BFP8_IN_F32)
+    return bad("out_dtype = %d (expected BFP8_IN_BF16 or BFP8_IN_F32)", out_dtype);
+  if (T < 0) return bad("T = %lld", (long long)T);
+  if (T == 0) return set_last_error(BFP8_OK, "");
+  if (!slots) return bad("slots is null");
+  if (!k_out && !v_out) return bad("k_out and v_out are null");
+  const int64_t width = static_cast<int64_t>(a.c.heads) * a.c.dim;
+  if ((k_out && k_stride_token < width) || (v_out && v_stride_token < width))
+    return bad("token strides must be >= num_kv_heads * head_dim");
+  const int es = out_dtype == BFP8_IN_F32 ? 4 : 2;
+  if (off_align(k_out, es) || off_align(v_out, es) || off_align(slots, 8))
+    return set_last_errorf(BFP8_ERR_ALIGNMENT, "k_out, v_out or slots is not aligned to its element size");
+  if (T >= kMaxRows / (2 * a.c.heads))
+    return set_last_errorf(BFP8_ERR_UNSUPPORTED, "T x heads too large for one launch");
+  int sms = 0;
+  if ((st = device_for_call(&sms, &a.err)) != BFP8_OK) return st;
+  a.k = k_out;
+  a.v = v_out;
+  a.k_st = k_stride_token;
+  a.v_st = v_stride_token;
+  a.slots = slots;
+  a.nkv = k_out && v_out ? 2 : 1;
+  a.rows = static_cast<uint32_t>(T * a.nkv * a.c.heads);
+  a.vec = !off_align(k_out, 16) && !off_align(v_out, 16) && (!k_out || k_stride_token * es % 16 == 0) &&
+          (!v_out || v_stride_token * es % 16 == 0);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  auto go = [&](auto f128, auto f64) {
+    return a.c.dim == 128 ? launch_rows(f128, a, a.rows, 2, sms, cs) : launch_rows(f64, a, a.rows, 4, sms, cs);
+  };
+  const cudaError_t e = out_dtype == BFP8_IN_F32 ? go(kv_read_kernel<true, 128>, kv_read_kernel<true, 64>)
+                                                 : go(kv_read_kernel<false, 128>, kv_read_kernel<false, 64>);
+  if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "cache read launch: %s", cudaGetErrorString(e));
+  return set_last_error(BFP8_OK, "");
+}

@@ -423,6 +423,161 @@ bfp8_status bfp8_gemm_noalloc(const void* A, const void* B, const float* As, int
                               int64_t K, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Around the linear layers: norm, paged 8-bit cache, attention              */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * bfp8_rmsnorm_quant -- the root-mean-square norm before a linear layer, with
+ * the residual's addition before it and the layer's input quantisation after
+ * it, in one pass.  For every row m:
+ *   h[k]  = x[m, k] + residual[m, k]                 (residual NULL: h = x)
+ *   residual_out[m, k] = h[k] in x's type            (residual_out NULL: not written)
+ *   y[k]  = h[k] * rsqrt(sum_k h[k]^2 / K + eps) * weight[k]
+ *   y_out[m, k] = bf16(y[k])                         (y_out NULL: not written)
+ *   q[m, k], s[m, g]: the 1 x 128 group quantisation of the unrounded y
+ *                     (as bfp8_group_quant_ex)       (q and s NULL: not written)
+ * All of it in fp32; each output is rounded once (h is not rounded to x's type
+ * before the norm, nor y to bf16 before the quantisation).
+ *   x             [M, K] bf16 or fp32 (in_dtype), row stride ld_x elements.
+ *   residual      [M, K] of x's type, row stride ld_r, or NULL.
+ *   residual_out  [M, K] of x's type, row stride ld_ro, or NULL; may be
+ *                 `residual` or `x` itself (same stride), else no overlap.
+ *   weight        [K] bf16 or fp32 (weight_dtype), or NULL (ones).
+ *   y_out         bf16 [M, K], row stride ld_y, or NULL.
+ *   q, ld_q, s, ld_s, col_major, scale_fmt   as for bfp8_group_quant_ex.
+ * Any M >= 0 and 1 <= K <= 2^20 (M == 0 launches nothing).  No alignment
+ * beyond the element size is required; K % 8 == 0 with 16-byte aligned rows
+ * takes the vectorised path.  Errors: BFP8_ERR_INVALID_ARG when there is
+ * nothing to write (residual_out, y_out and q all NULL), q and s are not both
+ * given, eps is negative or not finite, or a stride is too small.
+ */
+bfp8_status bfp8_rmsnorm_quant(const void* x, int in_dtype, int64_t ld_x, const void* residual,
+                               int64_t ld_r, void* residual_out, int64_t ld_ro,
+                               const void* weight, int weight_dtype, float eps, int64_t M,
+                               int64_t K, void* y_out, int64_t ld_y, int col_major, int scale_fmt,
+                               void* q, int64_t ld_q, float* s, int64_t ld_s, void* stream);
+
+/*
+ * A paged cache of keys and values in e4m3, one fp32 scale per (token, kv
+ * head): value = code * scale.  Token `o` of page `p`, kv head `h`:
+ *   codes  k + p * stride_page + h * stride_head + o * stride_token, head_dim bytes
+ *   scale  k_scale[p * scale_stride_page + h * scale_stride_head + o]
+ * and the same offsets in v and v_scale.  A slot is p * page_size + o.
+ * page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; code strides in bytes
+ * and multiples of 16 (stride_token >= head_dim); scale strides in floats and
+ * multiples of 4; all four pointers 16-byte aligned.  Both [page, head, token,
+ * dim] and [page, token, head, dim] orders of the codes, and keys and values
+ * interleaved by page, are strides of this form.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t num_pages;
+  int page_size;
+  int num_kv_heads;
+  int head_dim;
+  int reserved;
+  int64_t stride_page, stride_head, stride_token;
+  int64_t scale_stride_page, scale_stride_head;
+} bfp8_kv_cache;
+
+/*
+ * bfp8_kv_cache_write -- quantises T new tokens' keys and values into the
+ * cache: for every token t and kv head h, scale = max(amax, 1e-10) / 448 over
+ * the head's elements (rounded up to a power of two for BFP8_SCALE_UE8M0) and
+ * codes = e4m3(x / scale), the arithmetic of bfp8_group_quant_ex with the head
+ * as the group.
+ *   k, v   [T, num_kv_heads, head_dim] bf16 or fp32 (in_dtype) with token and
+ *          head strides >= 0 in elements (e.g. columns of a fused projection's
+ *          output); element strides 1.
+ *   slots  device int64 [T]: where token t goes; a negative slot skips the
+ *          token.  Slots of one call are distinct.  A slot past the last page
+ *          writes nothing and records BFP8_DEV_BAD_CACHE_INDEX.
+ * T == 0 launches nothing.
+ */
+bfp8_status bfp8_kv_cache_write(const void* k, const void* v, int in_dtype, int64_t k_stride_token,
+                                int64_t k_stride_head, int64_t v_stride_token,
+                                int64_t v_stride_head, const int64_t* slots, int64_t T,
+                                int scale_fmt, const bfp8_kv_cache* cache, void* stream);
+
+/*
+ * bfp8_kv_cache_read -- k_out[t, h, :] = code * scale of slot slots[t], rounded
+ * once to out_dtype (bf16 or fp32), and v_out likewise; [T, num_kv_heads,
+ * head_dim] with token strides in elements and heads contiguous.  k_out or
+ * v_out may be NULL (not both).  A negative slot gives zeros; a slot past the
+ * last page gives zeros and records BFP8_DEV_BAD_CACHE_INDEX.
+ */
+bfp8_status bfp8_kv_cache_read(const bfp8_kv_cache* cache, const int64_t* slots, int64_t T,
+                               int out_dtype, void* k_out, int64_t k_stride_token, void* v_out,
+                               int64_t v_stride_token, void* stream);
+
+/*
+ * bfp8_paged_attention -- attention of each sequence's newest tokens over its
+ * whole context in the paged cache (which already holds the new tokens).
+ * Sequence b has q_len = cu_q[b+1] - cu_q[b] new tokens, rows cu_q[b] .. of q,
+ * and a context of kv_lens[b] tokens; token j of it is at page
+ * block_table[b * ld_table + j / page_size], offset j % page_size.  New token
+ * i stands at position p = kv_lens[b] - q_len + i and sees the tokens
+ *   0 <= j <= p                     (causal = 1; causal = 0: 0 <= j < kv_lens[b])
+ *   j > p - window                  (window > 0; 0: no window)
+ * Query head h reads kv head h / (num_heads / num_kv_heads).
+ *   S_j   = softmax_scale * q . k_j,   w = softmax(S over the tokens seen)
+ *   out   = sum_j w_j v_j,   lse = log sum_j exp(S_j)   (natural logarithm)
+ * A row that sees no token (q_len > kv_lens[b], an empty context) gets out = 0
+ * and lse = -infinity.  Softmax and sums are fp32; the products run on the
+ * tensor cores from the exact bf16 queries and e4m3 codes, with the weights
+ * rounded to fp16 (11 bits) for the second product.
+ *   q, out   bf16 [total_q, num_heads, head_dim] with token and head strides
+ *            in elements (element stride 1; 16-byte aligned pointers and
+ *            strides that are multiples of 8).
+ *   lse      fp32 [total_q, num_heads] contiguous, or NULL.
+ *   block_table  device int32 [batch, max_pages], row stride ld_table.
+ *   cu_q     device int32 [batch + 1], non-decreasing, cu_q[0] >= 0,
+ *            cu_q[batch] <= total_q.  Rows outside every sequence are not written.
+ *   kv_lens  device int32 [batch].
+ *   max_q_len, max_kv_len   host upper bounds of the lengths (they size the
+ *            launch; the lengths themselves stay on the device, so that a
+ *            captured graph serves other lengths within the bounds).
+ *   workspace  as for bfp8_gemm (zero-filled once, left ready by every call;
+ *            one buffer may serve both), at least
+ *            bfp8_paged_attention_workspace_size bytes, 256-byte aligned.
+ * Page numbers outside the cache, and lengths outside the bounds, give
+ * unspecified outputs for their sequence, never a fault; page numbers are also
+ * recorded as BFP8_DEV_BAD_CACHE_INDEX.  Results are deterministic.
+ * batch == 0 or total_q == 0 launches nothing.
+ */
+typedef struct {
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t total_q;
+  int num_heads;
+  int batch;
+  int64_t q_stride_token, q_stride_head, out_stride_token, out_stride_head;
+  const int32_t* block_table;
+  int64_t ld_table;
+  int max_pages;
+  int max_q_len;
+  int64_t max_kv_len;
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  float softmax_scale;
+  int causal;
+  int window;
+  int reserved;
+} bfp8_attention_args;
+
+bfp8_status bfp8_paged_attention(const bfp8_attention_args* args, const bfp8_kv_cache* cache,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes bfp8_paged_attention needs on the current device for up to
+ * max_q_len new tokens a sequence. */
+bfp8_status bfp8_paged_attention_workspace_size(int num_heads, int num_kv_heads, int head_dim,
+                                                int max_q_len, size_t* bytes);
+
+/* ------------------------------------------------------------------------ */
 /* Status and diagnostics                                                    */
 /* ------------------------------------------------------------------------ */
 
@@ -441,6 +596,7 @@ const char* bfp8_status_string(int status);
 #define BFP8_DEV_TIMEOUT_EPILOGUE 3         /*   promotion / epilogue warps */
 #define BFP8_DEV_TIMEOUT_TAIL 4             /*   draining copies before exit */
 #define BFP8_DEV_BAD_GROUPED_LAYOUT 5       /* bfp8_gemm_grouped: invalid grouped_layout */
+#define BFP8_DEV_BAD_CACHE_INDEX 6          /* a slot or page number outside the cache */
 /* After a timeout code, a workspace the call used may hold non-zero counters:
  * zero it before reusing it. */
 bfp8_status bfp8_device_status(int* code, int clear);
