@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
   const int head = blockIdx.y;
   const int kvh = head / a.group;
   const SeqLens sl = seq_lens(a, b);
+  if (static_cast<int64_t>(sl.q_len) * a.group <= a.few_rows) return;
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (i >= sl.q_len) return;
   const int64_t row = sl.row0 + i;
@@ -80,6 +81,8 @@ bfp8_status bad(const char* fmt, V... v) {
   return set_last_errorf(BFP8_ERR_INVALID_ARG, fmt, v...);
 }
 
+constexpr int kFewRows = 32;
+
 bfp8_status check_heads(int heads, int kv_heads, int dim, int max_q) {
   if (kv_heads < 1 || heads < kv_heads || heads > 65535 || heads % kv_heads != 0)
     return bad("num_heads = %d is not a multiple of num_kv_heads = %d (at most 65535)", heads, kv_heads);
@@ -87,6 +90,17 @@ bfp8_status check_heads(int heads, int kv_heads, int dim, int max_q) {
   if (dim != 64 && dim != 128) return bad("head_dim = %d (expected 64 or 128)", dim);
   if (max_q < 1 || max_q > (1 << 24)) return bad("max_q_len = %d (expected 1 .. 2^24)", max_q);
   return BFP8_OK;
+}
+
+// Rows of a sequence up to which the kernel for few rows takes it, as a count
+// of eights: all sequences when even the longest is that short, else those of
+// a single token (a batch of chunks and decoding sequences).
+int few_groups(int group, int64_t max_q) {
+  return attn_decode_groups(max_q * group <= kFewRows ? max_q * group : group);
+}
+
+size_t workspace_bytes_for(int group, int dim, int max_q, int sms) {
+  return kCounterHeaderBytes + attn_decode_partial_bytes(few_groups(group, max_q), dim, sms);
 }
 
 }  // namespace
@@ -98,10 +112,13 @@ using namespace bfp8;
 extern "C" bfp8_status bfp8_paged_attention_workspace_size(int num_heads, int num_kv_heads,
                                                            int head_dim, int max_q_len,
                                                            size_t* bytes) {
-  const bfp8_status st = check_heads(num_heads, num_kv_heads, head_dim, max_q_len);
+  bfp8_status st = check_heads(num_heads, num_kv_heads, head_dim, max_q_len);
   if (st != BFP8_OK) return st;
   if (!bytes) return bad("bytes is null");
-  *bytes = kCounterHeaderBytes;
+  int sms = 0;
+  int* err = nullptr;
+  if ((st = device_for_call(&sms, &err)) != BFP8_OK) return st;
+  *bytes = workspace_bytes_for(num_heads / num_kv_heads, head_dim, max_q_len, sms);
   return set_last_error(BFP8_OK, "");
 }
 
@@ -136,14 +153,18 @@ extern "C" bfp8_status bfp8_paged_attention(const bfp8_attention_args* p, const 
   if (off_align(p->q, 16) || off_align(p->out, 16) || off_align(p->lse, 4) || off_align(p->block_table, 4) ||
       off_align(p->cu_q, 4) || off_align(p->kv_lens, 4))
     return set_last_errorf(BFP8_ERR_ALIGNMENT, "q and out must be 16-byte aligned, the rest 4-byte");
-  size_t need = 0;
-  if ((st = bfp8_paged_attention_workspace_size(p->num_heads, a.c.heads, a.c.dim, p->max_q_len, &need)) != BFP8_OK)
+  int sms = 0;
+  if ((st = device_for_call(&sms, &a.err)) != BFP8_OK) {
+    // a host without a device still learns of a missing workspace
+    if (!workspace || workspace_bytes < kCounterHeaderBytes || off_align(workspace, 256))
+      return set_last_errorf(BFP8_ERR_WORKSPACE, "workspace missing, too small or not 256-byte aligned");
     return st;
+  }
+  a.group = p->num_heads / a.c.heads;
+  const size_t need = workspace_bytes_for(a.group, a.c.dim, p->max_q_len, sms);
   if (!workspace || workspace_bytes < need)
     return set_last_errorf(BFP8_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   if (off_align(workspace, 256)) return set_last_errorf(BFP8_ERR_WORKSPACE, "workspace is not 256-byte aligned");
-  int sms = 0;
-  if ((st = device_for_call(&sms, &a.err)) != BFP8_OK) return st;
   a.q = static_cast<const __nv_bfloat16*>(p->q);
   a.out = static_cast<__nv_bfloat16*>(p->out);
   a.lse = p->lse;
@@ -158,16 +179,35 @@ extern "C" bfp8_status bfp8_paged_attention(const bfp8_attention_args* p, const 
   a.total_q = p->total_q;
   a.max_kv = p->max_kv_len;
   a.heads = p->num_heads;
-  a.group = p->num_heads / a.c.heads;
   a.batch = p->batch;
   a.max_q = p->max_q_len;
   a.causal = p->causal;
   a.window = p->window;
   a.scale = p->softmax_scale;
-  const dim3 grid((p->max_q_len + 7) / 8, p->num_heads, p->batch);
-  if (a.c.dim == 128) attn_rows_kernel<128><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  else attn_rows_kernel<64><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const int groups = few_groups(a.group, p->max_q_len);
+  a.few_rows = groups * 8;
+  const uint64_t dims[4] = {static_cast<uint64_t>(a.c.dim), static_cast<uint64_t>(a.c.page_size),
+                            static_cast<uint64_t>(a.c.heads), static_cast<uint64_t>(a.c.num_pages)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(a.c.st_tok), static_cast<uint64_t>(a.c.st_head),
+                               static_cast<uint64_t>(a.c.st_page)};
+  const uint32_t box[4] = {static_cast<uint32_t>(a.c.dim),
+                           static_cast<uint32_t>(a.c.page_size < 128 ? a.c.page_size : 128), 1u, 1u};
+  CUtensorMap mk, mv;
+  if ((st = encode_bytes_tiled(&mk, a.c.k, 4, dims, strides, box, a.c.dim)) != BFP8_OK) return st;
+  if ((st = encode_bytes_tiled(&mv, a.c.v, 4, dims, strides, box, a.c.dim)) != BFP8_OK) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (a.group <= kFewRows)
+    e = launch_attn_decode(mk, mv, a, groups, sms, static_cast<int32_t*>(workspace),
+                           reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterHeaderBytes), cs);
+  else
+    a.few_rows = 0;
+  if (e == cudaSuccess && static_cast<int64_t>(p->max_q_len) * a.group > a.few_rows) {
+    const dim3 grid((p->max_q_len + 7) / 8, p->num_heads, p->batch);
+    if (a.c.dim == 128) attn_rows_kernel<128><<<grid, 256, 0, cs>>>(a);
+    else attn_rows_kernel<64><<<grid, 256, 0, cs>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
   return set_last_error(BFP8_OK, "");
 }

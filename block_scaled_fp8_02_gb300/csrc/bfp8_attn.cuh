@@ -2,7 +2,9 @@
 // lengths of a sequence as they stand on the device.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
 
 #include <cstdint>
 
@@ -26,6 +28,7 @@ struct AttnArgs {
   int32_t max_q;
   int32_t causal;
   int32_t window;
+  int32_t few_rows;             // sequences of at most this many rows (new tokens x group) go to the kernel for few
   float scale;
   CacheView c;
   int* err;
@@ -58,5 +61,13 @@ __device__ __forceinline__ void seen_range(const AttnArgs& a, int32_t kv_len, in
   if (lo < 0) lo = 0;
   if (hi > kv_len) hi = kv_len;
 }
+
+// The kernel for few rows a sequence (bfp8_attn_decode.cu): `groups` (1, 2 or 4)
+// eights of rows, `ctas` persistent CTAs, counters[ctas] zero.
+// k, v: tensor maps [dim, token, head, page] of bytes, boxes of min(page_size, 128) tokens.
+int attn_decode_groups(int64_t rows);
+size_t attn_decode_partial_bytes(int groups, int dim, int ctas);
+cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int groups, int ctas,
+                               int32_t* counters, float* partials, cudaStream_t stream);
 
 }  // namespace bfp8
