@@ -1,5 +1,5 @@
 // bfp8_attn.cu -- attention of new tokens over the paged e4m3 cache: the C
-// entry points and a kernel of one warp per (token, query head).
+// entry points, and which kernel takes which sequences.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -7,72 +7,11 @@
 #include <cstdint>
 
 #include "bfp8_attn.cuh"
-#include "bfp8_devstatus.cuh"
 #include "bfp8_internal.h"
-#include "bfp8_ptx.cuh"
-#include "bfp8_vec8.cuh"
 
 namespace bfp8 {
 
 namespace {
-
-// One warp a row (token, head): lanes hold D / 32 elements each, one pass over
-// the tokens with the running maximum and sum of the softmax.
-template <int D>
-__global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.z;
-  const int head = blockIdx.y;
-  const int kvh = head / a.group;
-  const SeqLens sl = seq_lens(a, b);
-  if (static_cast<int64_t>(sl.q_len) * a.group <= a.few_rows) return;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= sl.q_len) return;
-  const int64_t row = sl.row0 + i;
-  float q[E], o[E];
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(a.q[row * a.q_st + head * a.q_sh + lane * E + e]);
-    o[e] = 0.f;
-  }
-  int32_t lo, hi;
-  seen_range(a, sl.kv_len, sl.kv_len - sl.q_len + i, lo, hi);
-  float m = -INFINITY;
-  double l = 0.0;      // tens of thousands of equal weights would drift in 32 bits
-  for (int32_t j = lo; j < hi; ++j) {
-    const int32_t page = a.table[b * a.ld_table + (j >> a.c.page_shift)];
-    if (page < 0 || page >= a.c.num_pages) {
-      report_failure(a.err, kDevBadCacheIndex);
-      continue;
-    }
-    const int32_t off = j & (a.c.page_size - 1);
-    const int64_t at = page * a.c.st_page + kvh * a.c.st_head + off * a.c.st_tok + lane * E;
-    const int64_t sat = page * a.c.ss_page + kvh * a.c.ss_head + off;
-    float k4[4], v4[4];
-    uint32_t kw, vw;
-    if constexpr (E == 4) {
-      kw = *reinterpret_cast<const uint32_t*>(a.c.k + at);
-      vw = *reinterpret_cast<const uint32_t*>(a.c.v + at);
-    } else {
-      kw = *reinterpret_cast<const uint16_t*>(a.c.k + at);
-      vw = *reinterpret_cast<const uint16_t*>(a.c.v + at);
-    }
-    e4m3x4_to_f32(kw, k4);
-    e4m3x4_to_f32(vw, v4);
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], k4[e], s);
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.c.ks[sat] * a.scale;
-    const float mn = fmaxf(m, s), c = expf(m - mn), p = expf(s - mn), pv = p * a.c.vs[sat];
-    l = l * c + p;
-    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], c, pv * v4[e]);
-    m = mn;
-  }
-  const float inv = l > 0.0 ? static_cast<float>(1.0 / l) : 0.f;
-  for (int e = 0; e < E; ++e)
-    a.out[row * a.o_st + head * a.o_sh + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
-  if (a.lse != nullptr && lane == 0) a.lse[row * a.heads + head] = l > 0.0 ? static_cast<float>(m + log(l)) : -INFINITY;
-}
 
 inline bool off_align(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
@@ -99,8 +38,18 @@ int few_groups(int group, int64_t max_q) {
   return attn_decode_groups(max_q * group <= kFewRows ? max_q * group : group);
 }
 
+bool has_many(int group, int max_q) {
+  return group > kFewRows || static_cast<int64_t>(max_q) * group > 8 * few_groups(group, max_q);
+}
+
+size_t few_bytes(int group, int dim, int max_q, int sms) {
+  return (attn_decode_partial_bytes(few_groups(group, max_q), dim, sms) + 255) / 256 * 256;
+}
+
+// Counter header, partial rows of the kernel for few rows, those of the other.
 size_t workspace_bytes_for(int group, int dim, int max_q, int sms) {
-  return kCounterHeaderBytes + attn_decode_partial_bytes(few_groups(group, max_q), dim, sms);
+  return kCounterHeaderBytes + few_bytes(group, dim, max_q, sms) +
+         (has_many(group, max_q) ? attn_tile_partial_bytes(dim, sms) : 0);
 }
 
 }  // namespace
@@ -196,18 +145,16 @@ extern "C" bfp8_status bfp8_paged_attention(const bfp8_attention_args* p, const 
   if ((st = encode_bytes_tiled(&mk, a.c.k, 4, dims, strides, box, a.c.dim)) != BFP8_OK) return st;
   if ((st = encode_bytes_tiled(&mv, a.c.v, 4, dims, strides, box, a.c.dim)) != BFP8_OK) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  int32_t* counters = static_cast<int32_t*>(workspace);
+  char* partials = static_cast<char*>(workspace) + kCounterHeaderBytes;
   cudaError_t e = cudaSuccess;
   if (a.group <= kFewRows)
-    e = launch_attn_decode(mk, mv, a, groups, sms, static_cast<int32_t*>(workspace),
-                           reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterHeaderBytes), cs);
+    e = launch_attn_decode(mk, mv, a, groups, sms, counters, reinterpret_cast<float*>(partials), cs);
   else
     a.few_rows = 0;
-  if (e == cudaSuccess && static_cast<int64_t>(p->max_q_len) * a.group > a.few_rows) {
-    const dim3 grid((p->max_q_len + 7) / 8, p->num_heads, p->batch);
-    if (a.c.dim == 128) attn_rows_kernel<128><<<grid, 256, 0, cs>>>(a);
-    else attn_rows_kernel<64><<<grid, 256, 0, cs>>>(a);
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess && has_many(a.group, p->max_q_len))
+    e = launch_attn_tile(mk, mv, a, sms, counters + sms,
+                         reinterpret_cast<float*>(partials + few_bytes(a.group, a.c.dim, p->max_q_len, sms)), cs);
   if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
   return set_last_error(BFP8_OK, "");
 }

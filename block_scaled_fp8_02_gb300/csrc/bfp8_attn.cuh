@@ -70,4 +70,9 @@ size_t attn_decode_partial_bytes(int groups, int dim, int ctas);
 cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int groups, int ctas,
                                int32_t* counters, float* partials, cudaStream_t stream);
 
+// The kernel for more rows (bfp8_attn_tile.cu); counters[2 * ctas] zero.
+size_t attn_tile_partial_bytes(int dim, int ctas);
+cudaError_t launch_attn_tile(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int ctas, int32_t* counters,
+                             float* partials, cudaStream_t stream);
+
 }  // namespace bfp8

@@ -39,6 +39,7 @@
 #include <cstdint>
 
 #include "bfp8_attn.cuh"
+#include "bfp8_attn_math.cuh"
 #include "bfp8_devstatus.cuh"
 #include "bfp8_internal.h"
 #include "bfp8_ptx.cuh"
@@ -116,21 +117,6 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part) {
   return v;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float r;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // f16 pairs of the low and high two e4m3 codes of a word (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"

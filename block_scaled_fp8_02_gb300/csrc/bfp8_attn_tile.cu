@@ -1,0 +1,951 @@
+// bfp8_attn_tile.cu -- attention of many new tokens a sequence over the paged
+// e4m3 cache, on the 5th-generation tensor cores: bound by the two products.
+//
+// The query rows of a kv head (new tokens x the group's heads, heads innermost)
+// are cut into blocks of 256: two 128-row tiles a CTA, which take turns on the
+// tensor core and the softmax.  A block's context comes in 128-token tiles.
+//   S = Q K^T   tcgen05.mma kind::f8f6f4 straight from the cache's codes.  A bf16
+//               query element (8 significant bits) is the sum of two e4m3 numbers
+//               (4 bits each) after scaling its row by a power of two, so Q is kept
+//               as two e4m3 operands and S takes two passes: exact products at the
+//               time of one 16-bit pass, and no conversion of K.
+//   O += P V    kind::f16: P from tensor memory, over the columns of S; V converted
+//               from e4m3 by one warpgroup, scaled by its token's scale relative
+//               to the tile's largest (one f16 rounding).
+// Roles: two softmax warpgroups (a thread a row: scores from tensor memory, key
+// scales, mask, running maximum and sum, P, and the rare rescaling of O), one
+// converting V, and single warps for TMA, for the MMAs and for the tiles'
+// scales.
+//
+// Scores x are in powers of two.  A tile's values share the scale 2^lv, which
+// joins the exponent: P = 2^(x + lv - mv + 7) with mv a running maximum of x + lv
+// that may lag by up to 8 (then O and the sum are rescaled), and the sum of the
+// weights collects P 2^-lv, a tile's sum at a time.  Where a tile's value scales
+// differ by more than 2^11 its tokens' own log2 scales join the exponents instead.
+//
+// As in the kernel for few rows, the tiles of all blocks form one line that the
+// persistent CTAs share equally; a block cut by a border leaves fp32 partial
+// rows in the workspace and the last CTA to arrive adds them in CTA order.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "bfp8_attn.cuh"
+#include "bfp8_attn_math.cuh"
+#include "bfp8_devstatus.cuh"
+#include "bfp8_internal.h"
+#include "bfp8_ptx.cuh"
+
+namespace bfp8 {
+
+namespace {
+
+constexpr int kTile = 128;                 // tokens of a tile, rows of a query tile
+constexpr int kBlockRows = 2 * kTile;
+constexpr int kTileThreads = 512;
+constexpr int kWarpTma = 12, kWarpMma = 13, kWarpScale = 14;
+constexpr int kSeqChunk = 2048;            // sequences whose tile counts are held at once
+constexpr int kKStages = 3, kVStages = 2, kFStages = 2, kScSlots = 4;
+constexpr float kNoMax = -3.0e38f;
+constexpr float kLag = 8.f;
+constexpr float kLift = 7.f;               // P <= 2^15
+constexpr int kVUp = 6;                    // values are scaled up by 2^6 in f16: 448 * 2^6 < 65504
+constexpr float kWide = 0x1p-11f;          // below this ratio of value scales a tile takes the other path
+
+template <int D>
+struct TileCfg {
+  static constexpr int kQ = kTile * D;                    // one e4m3 part of a query tile
+  static constexpr int kK = kTile * D;
+  static constexpr int kV16 = kTile * D * 2;
+  static constexpr int kHalf = kTile * 128;               // 64 columns of V in f16
+  static constexpr int kOffQ = 0;                         // [tile][hi, lo]
+  static constexpr int kOffK = kOffQ + 4 * kQ;
+  static constexpr int kOffV = kOffK + kKStages * kK;
+  static constexpr int kOffF = kOffV + kVStages * kK;
+  static constexpr int kOffRaw = kOffF + kFStages * kV16;     // scales as in the cache: K then V
+  static constexpr int kOffKs = kOffRaw + kScSlots * 2 * kTile * 4;
+  static constexpr int kOffRv = kOffKs + kScSlots * kTile * 4;
+  static constexpr int kOffDl = kOffRv + kScSlots * kTile * 4;   // wide tiles: log2 vs - lv
+  static constexpr int kOffIv = kOffDl + kScSlots * kTile * 4;   // wide tiles: 1 / vs
+  static constexpr int kOffInfo = kOffIv + kScSlots * kTile * 4; // lv, 2^-lv, wide
+  static constexpr int kOffBar = kOffInfo + kScSlots * 16;
+  static constexpr int kBars = 2 * kKStages + 2 * kVStages + 2 * kFStages + 3 * kScSlots + 8;
+  static constexpr int kSmem = kOffBar + kBars * 8 + 64 + 1024;
+  static constexpr uint32_t kColO = 256;                  // S (and P) of the tiles at 0 and 128
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  static_assert(kSeqChunk * 8 <= kOffRaw, "tile counts fit the operands' space");
+};
+
+struct TileArgs {
+  AttnArgs a;
+  int32_t* counters;          // two a CTA, zero between calls
+  float* partials;            // two slots a CTA
+  unsigned long long wait_limit;
+  int32_t min_tiles;          // least tiles of a share
+};
+
+// Floats of a slot: [2 tiles][D / 4][128 rows][4], then the rows' log2 sums.
+template <int D>
+__host__ __device__ constexpr int64_t slot_floats() { return kBlockRows * D + kBlockRows; }
+
+// Row blocks and context of a sequence.
+struct SeqBlocks {
+  int64_t row0;
+  int32_t q_len, kv_len, pos0;
+  int32_t blocks;             // 0: not this kernel's
+};
+__device__ __forceinline__ SeqBlocks seq_blocks(const AttnArgs& a, int b) {
+  const SeqLens s = seq_lens(a, b);
+  SeqBlocks w;
+  w.row0 = s.row0;
+  w.q_len = s.q_len;
+  w.kv_len = s.kv_len;
+  w.pos0 = s.kv_len - s.q_len;
+  const int64_t rows = static_cast<int64_t>(s.q_len) * a.group;
+  w.blocks = rows > a.few_rows ? static_cast<int32_t>((rows + kBlockRows - 1) / kBlockRows) : 0;
+  return w;
+}
+// Tokens [t0, t1) that some row of block rb sees, and its tiles.
+__device__ __forceinline__ int32_t block_tiles(const AttnArgs& a, const SeqBlocks& w, int rb, int32_t& t0,
+                                               int32_t& t1) {
+  const int64_t r0 = static_cast<int64_t>(rb) * kBlockRows;
+  const int32_t i0 = static_cast<int32_t>(r0 / a.group);
+  int64_t i1 = (r0 + kBlockRows - 1) / a.group;
+  if (i1 > w.q_len - 1) i1 = w.q_len - 1;
+  int32_t lo, hi, x;
+  seen_range(a, w.kv_len, w.pos0 + i0, lo, x);
+  seen_range(a, w.kv_len, w.pos0 + static_cast<int32_t>(i1), x, hi);
+  t0 = lo;
+  t1 = hi;
+  return hi > lo ? (hi + kTile - 1) / kTile - lo / kTile : 1;
+}
+
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// kind::f16, A = B = f16, D = f32, A K-major, B MN-major (bit 16).
+__host__ __device__ constexpr uint32_t idesc_f16_bmn(int m, int n) {
+  return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+// K-major rows of 64 bytes with the 64-byte swizzle: 8-row groups 512 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_k_sw64(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(16u >> 4) << 16;
+  d |= static_cast<uint64_t>(512u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(4u) << 61;
+  return d;
+}
+// MN-major f16 with the 128-byte swizzle: rows (contraction index) of 64
+// elements, 8-row groups 1024 bytes apart (stride offset), the next 64
+// elements `next` bytes on (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t next) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(next >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Orders later uses of the registers after the preceding wait.
+__device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    attn_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ TileArgs p) {
+  using C = TileCfg<D>;
+  const AttnArgs& a = p.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int H = a.c.heads;
+  // barriers
+  auto bar = [&](int i) { return sbase + static_cast<uint32_t>(C::kOffBar + 8 * i); };
+  const int bKf = 0, bKe = bKf + kKStages, bVf = bKe + kKStages, bVe = bVf + kVStages, bFf = bVe + kVStages,
+            bFe = bFf + kFStages, bRf = bFe + kFStages, bSf = bRf + kScSlots, bSe = bSf + kScSlots,
+            bQ = bSe + kScSlots, bS = bQ + 2, bP = bS + 2, bO = bP + 2;
+  __shared__ uint32_t s_tmem;
+  __shared__ int64_t s_before, s_total;
+  __shared__ int s_b;
+  __shared__ int s_last[2];
+
+  if (tid == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(bar(bKf + i), 1);
+      mbar_init(bar(bKe + i), 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(bar(bVf + i), 1);
+      mbar_init(bar(bVe + i), 4);
+    }
+    for (int i = 0; i < kFStages; ++i) {
+      mbar_init(bar(bFf + i), 128);
+      mbar_init(bar(bFe + i), 1);
+    }
+    for (int i = 0; i < kScSlots; ++i) {
+      mbar_init(bar(bRf + i), 1);
+      mbar_init(bar(bSf + i), 32);
+      mbar_init(bar(bSe + i), 12);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(bQ + i), 128);
+      mbar_init(bar(bS + i), 1);
+      mbar_init(bar(bP + i), 128);
+      mbar_init(bar(bO + i), 1);
+    }
+    fence_barrier_init();
+  }
+  griddep_launch_dependents();
+  griddep_wait();
+
+  // ---- this CTA's share of the line of tiles: the tiles of each sequence and
+  // kv head, a warp a sequence, in the operands' space; then one warp adds up
+  int64_t* cnt = reinterpret_cast<int64_t*>(smem);
+  auto count_chunk = [&](int b0) {
+    const int n = a.batch - b0 < kSeqChunk ? a.batch - b0 : kSeqChunk;
+    for (int i = warp; i < n; i += kTileThreads / 32) {
+      const SeqBlocks w = seq_blocks(a, b0 + i);
+      int64_t v = 0;
+      int32_t t0, t1;
+      for (int rb = lane; rb < w.blocks; rb += 32) v += block_tiles(a, w, rb, t0, t1);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) cnt[i] = v;
+    }
+    __syncthreads();
+    return n;
+  };
+  int64_t run = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kSeqChunk) {
+    const int n = count_chunk(b0);
+    if (warp == 0) {
+      int64_t v = 0;
+      for (int i = lane; i < n; i += 32) v += cnt[i];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) s_total = v;
+    }
+    __syncthreads();
+    run += s_total;
+    __syncthreads();
+  }
+  const int64_t total = run * H;
+  int64_t ctas = total / p.min_tiles;
+  if (ctas < 1) ctas = 1;
+  if (ctas > gridDim.x) ctas = gridDim.x;
+  if (total == 0 || blockIdx.x >= ctas) return;         // whole CTA: nothing allocated or in flight yet
+  const int64_t u0 = blockIdx.x * total / ctas, u1 = (blockIdx.x + 1) * total / ctas;
+  run = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kSeqChunk) {
+    const int n = a.batch <= kSeqChunk ? a.batch : count_chunk(b0);
+    if (warp == 0) {
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const int64_t own = i0 + lane < n ? cnt[i0 + lane] : 0;
+        int64_t v = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += t;
+        }
+        const int64_t before = (run + v - own) * H;
+        if (own > 0 && before <= u0 && u0 < before + own * H) {
+          s_b = b0 + i0 + lane;
+          s_before = before;
+        }
+        run += __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_addr(&s_tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  fence_proxy_async_smem();                     // the counts' space is handed to the TMA
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  // cursor over the share: block (b, h, rb), its tiles [k0, k1) here, its place in the line
+  struct Cursor {
+    int b, h, rb;
+    int64_t item0;
+    int32_t n, k0, k1;
+    int32_t t0, t1;
+    SeqBlocks w;
+  };
+  auto clip = [&](Cursor& c) {
+    c.k0 = static_cast<int32_t>(u0 > c.item0 ? u0 - c.item0 : 0);
+    c.k1 = static_cast<int32_t>(c.item0 + c.n < u1 ? c.n : u1 - c.item0);
+  };
+  auto step_block = [&](Cursor& c) {            // the block after (b, h, rb)
+    if (++c.rb == c.w.blocks) {
+      c.rb = 0;
+      if (++c.h == H) {
+        c.h = 0;
+        do {
+          c.w = seq_blocks(a, ++c.b);
+        } while (c.w.blocks == 0);
+      }
+    }
+    c.n = block_tiles(a, c.w, c.rb, c.t0, c.t1);
+  };
+  auto start = [&](Cursor& c) {
+    c.b = s_b;
+    c.w = seq_blocks(a, c.b);
+    c.rb = 0;
+    c.h = 0;
+    c.item0 = s_before;
+    c.n = block_tiles(a, c.w, 0, c.t0, c.t1);
+    while (c.item0 + c.n <= u0) {
+      c.item0 += c.n;
+      step_block(c);
+    }
+    clip(c);
+  };
+  auto next = [&](Cursor& c) -> bool {
+    c.item0 += c.n;
+    if (c.item0 >= u1) return false;
+    step_block(c);
+    clip(c);
+    return true;
+  };
+
+  bool ok = true;
+  // one lane waits for its warp
+  auto wait_warp = [&](int i, uint32_t parity, int code) {
+    if (!ok) return;
+    int r = 1;
+    if (lane == 0) r = mbar_wait_bounded(bar(i), parity, p.wait_limit);
+    ok = __shfl_sync(0xffffffffu, r, 0) != 0;
+    if (!ok && lane == 0) report_failure(a.err, code);
+  };
+  // every lane waits (it reads what the barrier guards)
+  auto wait_all = [&](int i, uint32_t parity, int code) {
+    if (!ok) return;
+    const bool r = mbar_wait_bounded(bar(i), parity, p.wait_limit);
+    ok = __all_sync(0xffffffffu, r);
+    if (!ok && lane == 0) report_failure(a.err, code);
+  };
+  auto ph = [](int64_t q, int stages) { return static_cast<uint32_t>((q / stages) & 1); };
+
+  if (warp >= 12) {
+    setmaxnreg_dec<48>();
+    if (warp == kWarpTma) {
+      // ------------------------------------------------------------- TMA
+      const int page = a.c.page_size, shift = a.c.page_shift;
+      const int ppu = page >= kTile ? 1 : kTile / page;
+      const int box = page >= kTile ? kTile : page;
+      int64_t q = 0;
+      Cursor c;
+      start(c);
+      do {
+        const int32_t ub = c.t0 / kTile;
+        const int32_t* row = a.table + c.b * a.ld_table;
+        int32_t cached = -1, entry = 0;
+        for (int32_t k = c.k0; k < c.k1 && ok; ++k, ++q) {
+          const int32_t tok = (ub + k) * kTile;
+          const int32_t first = tok / box;
+          if (first / 32 != cached) {
+            cached = first / 32;
+            const int64_t t = (static_cast<int64_t>(cached) * 32 + lane) * box;
+            entry = 0;
+            if (t < c.t1 && t + box > c.t0) {
+              entry = __ldg(row + (t >> shift));
+              if (entry < 0 || entry >= a.c.num_pages) {
+                report_failure(a.err, kDevBadCacheIndex);
+                entry = 0;
+              }
+            }
+          }
+          const int32_t t = tok + lane * box;
+          const bool live = lane < ppu && t < c.t1 && t + box > c.t0;
+          const int n = __popc(__ballot_sync(0xffffffffu, live));
+          const int32_t pg = __shfl_sync(0xffffffffu, entry, (first + lane) & 31);
+          const int off = t & (page - 1);
+          const int sc = static_cast<int>(q % kScSlots), ks = static_cast<int>(q % kKStages),
+                    vs = static_cast<int>(q % kVStages);
+          wait_warp(bSe + sc, ph(q, kScSlots) ^ 1u, kDevTimeoutProducer);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(bRf + sc), static_cast<uint32_t>(n * 2 * box * 4));
+          __syncwarp();
+          if (live) {
+            const int64_t so = pg * a.c.ss_page + c.h * a.c.ss_head + off;
+            const uint32_t sd = sbase + static_cast<uint32_t>(C::kOffRaw + (sc * 2 * kTile + lane * box) * 4);
+            bulk_load(sd, a.c.ks + so, box * 4, bar(bRf + sc));
+            bulk_load(sd + kTile * 4, a.c.vs + so, box * 4, bar(bRf + sc));
+          }
+          wait_warp(bKe + ks, ph(q, kKStages) ^ 1u, kDevTimeoutProducer);
+          if (!ok) {
+            ++q;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(bKf + ks), static_cast<uint32_t>(n * box * D));
+          __syncwarp();
+          if (live)
+            tma_load_4d(sbase + static_cast<uint32_t>(C::kOffK + ks * C::kK + lane * box * D), &tmK, bar(bKf + ks), 0,
+                        off, c.h, pg);
+          wait_warp(bVe + vs, ph(q, kVStages) ^ 1u, kDevTimeoutProducer);
+          if (!ok) {
+            ++q;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(bVf + vs), static_cast<uint32_t>(n * box * D));
+          __syncwarp();
+          if (live)
+            tma_load_4d(sbase + static_cast<uint32_t>(C::kOffV + vs * C::kK + lane * box * D), &tmV, bar(bVf + vs), 0,
+                        off, c.h, pg);
+        }
+      } while (ok && next(c));
+      // no copy may still be landing when the CTA exits (after a failure: bounded waits all the same)
+      auto drain = [&](int b0, int stages) {
+        for (int64_t i = q > stages ? q - stages : 0; i < q; ++i)
+          if (lane == 0 && !mbar_wait_bounded(bar(b0 + static_cast<int>(i % stages)), ph(i, stages), p.wait_limit)) {
+            report_failure(a.err, kDevTimeoutTail);
+            break;
+          }
+        __syncwarp();
+      };
+      drain(bRf, kScSlots);
+      drain(bKf, kKStages);
+      drain(bVf, kVStages);
+    } else if (warp == kWarpMma) {
+      // ------------------------------------------------------------- MMA
+      if (lane == 0) {
+        const uint32_t idS = idesc_e4m3_f32(128, 128), idO = idesc_f16_bmn(128, D);
+        auto wait1 = [&](int i, uint32_t parity) {
+          if (ok && !mbar_wait_bounded(bar(i), parity, p.wait_limit)) {
+            report_failure(a.err, kDevTimeoutMma);
+            ok = false;
+          }
+          return ok;
+        };
+        auto desc = [&](int off) {
+          return D == 128 ? sdesc_k_sw128(sbase + static_cast<uint32_t>(off))
+                          : sdesc_k_sw64(sbase + static_cast<uint32_t>(off));
+        };
+        auto qk = [&](int t, int ks) {
+          const uint64_t kd = desc(C::kOffK + ks * C::kK);
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const uint64_t qd = desc(C::kOffQ + (2 * t + part) * C::kQ);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              mma_f8f6f4(tmem + t * 128, qd + 2 * i, kd + 2 * i, idS, (part | i) != 0);
+          }
+        };
+        auto pv = [&](int t, int fs, bool first) {
+          const uint64_t vd = sdesc_mn_sw128(sbase + static_cast<uint32_t>(C::kOffF + fs * C::kV16), C::kHalf);
+#pragma unroll
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_f16_ts(tmem + C::kColO + t * 128, tmem + t * 128 + 8 * i, vd + 128 * i, idO, !(first && i == 0));
+        };
+        int64_t q = 0, done = 0;
+        uint32_t item = 0, pp = 0;               // blocks done; P phases
+        Cursor c;
+        start(c);
+        do {
+          wait1(bQ, item & 1);
+          wait1(bQ + 1, item & 1);
+          wait1(bKf + static_cast<int>(q % kKStages), ph(q, kKStages));
+          if (!ok) break;
+          tc_fence_after();
+          qk(0, static_cast<int>(q % kKStages));
+          mma_commit(bar(bS));
+          qk(1, static_cast<int>(q % kKStages));
+          mma_commit(bar(bS + 1));
+          mma_commit(bar(bKe + static_cast<int>(q % kKStages)));
+          for (int32_t k = c.k0; k < c.k1 && ok; ++k, ++q, ++pp) {
+            const bool more = k + 1 < c.k1;
+            const int fs = static_cast<int>(q % kFStages), kn = static_cast<int>((q + 1) % kKStages);
+            wait1(bFf + fs, ph(q, kFStages));
+            for (int t = 0; t < 2 && ok; ++t) {
+              if (!wait1(bP + t, pp & 1)) break;
+              tc_fence_after();
+              pv(t, fs, k == c.k0);
+              if (t == 1) mma_commit(bar(bFe + fs));
+              if (more) {
+                if (t == 0 && !wait1(bKf + kn, ph(q + 1, kKStages))) break;
+                tc_fence_after();
+                qk(t, kn);
+                mma_commit(bar(bS + t));
+                if (t == 1) mma_commit(bar(bKe + kn));
+              } else {
+                mma_commit(bar(bO + t));
+              }
+            }
+            if (ok) done = q + 1;
+          }
+          ++item;
+        } while (ok && next(c));
+        // every commit has arrived before the CTA exits
+        for (int64_t i = done > kFStages ? done - kFStages : 0; i < done; ++i)
+          mbar_wait_bounded(bar(bFe + static_cast<int>(i % kFStages)), ph(i, kFStages), p.wait_limit);
+        for (int64_t i = done > kKStages ? done - kKStages : 0; i < done; ++i)
+          mbar_wait_bounded(bar(bKe + static_cast<int>(i % kKStages)), ph(i, kKStages), p.wait_limit);
+      }
+      __syncwarp();
+    } else if (warp == kWarpScale) {
+      // ---------------------------------------------- the tiles' scales
+      int64_t q = 0;
+      Cursor c;
+      start(c);
+      do {
+        const int32_t ub = c.t0 / kTile;
+        for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
+          const int sl = static_cast<int>(q % kScSlots);
+          wait_all(bRf + sl, ph(q, kScSlots), kDevTimeoutEpilogue);
+          const int32_t tok = (ub + k) * kTile + lane * 4;
+          const float4 kr = *reinterpret_cast<const float4*>(smem + C::kOffRaw + (sl * 2 * kTile + lane * 4) * 4);
+          const float4 vr = *reinterpret_cast<const float4*>(smem + C::kOffRaw + ((sl * 2 + 1) * kTile + lane * 4) * 4);
+          float ks[4] = {kr.x, kr.y, kr.z, kr.w}, vs[4] = {vr.x, vr.y, vr.z, vr.w};
+          bool live[4];
+          float top = 0.f, low = 3.0e38f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            live[e] = tok + e >= c.t0 && tok + e < c.t1;
+            if (!live[e]) ks[e] = vs[e] = 0.f;
+            top = fmaxf(top, vs[e]);
+            if (live[e]) low = fminf(low, vs[e]);
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+          }
+          // vref = 2^E >= top; values are held as code * (vs / vref) * 2^kVUp, so 2^lv = vref 2^-kVUp
+          uint32_t bits = (__float_as_uint(top) + 0x7FFFFFu) & 0xFF800000u;
+          if (bits < 0x10000000u) bits = 0x10000000u;                    // 2^-95: an all-zero tile
+          const float vinv = __uint_as_float(0x7F000000u - bits);
+          const bool wide = low < top * kWide;
+          const float lv = static_cast<float>(static_cast<int>(bits >> 23) - 127 - kVUp);
+          float4 r, dl, iv;
+          float rr[4], dd[4], ii[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            rr[e] = !(vs[e] > 0.f) ? 0.f : wide ? static_cast<float>(1 << kVUp) : vs[e] * vinv * static_cast<float>(1 << kVUp);
+            // a scale of zero is a value of zero: its weight counts all the same
+            dd[e] = vs[e] > 0.f ? lg2(vs[e] * vinv) : 0.f;
+            ii[e] = (vs[e] > 0.f ? 1.f / vs[e] : vinv) * static_cast<float>(1 << kVUp);
+          }
+          r = make_float4(rr[0], rr[1], rr[2], rr[3]);
+          dl = make_float4(dd[0], dd[1], dd[2], dd[3]);
+          iv = make_float4(ii[0], ii[1], ii[2], ii[3]);
+          *reinterpret_cast<float4*>(smem + C::kOffKs + (sl * kTile + lane * 4) * 4) = make_float4(ks[0], ks[1], ks[2], ks[3]);
+          *reinterpret_cast<float4*>(smem + C::kOffRv + (sl * kTile + lane * 4) * 4) = r;
+          if (wide) {
+            *reinterpret_cast<float4*>(smem + C::kOffDl + (sl * kTile + lane * 4) * 4) = dl;
+            *reinterpret_cast<float4*>(smem + C::kOffIv + (sl * kTile + lane * 4) * 4) = iv;
+          }
+          if (lane == 0)
+            *reinterpret_cast<float4*>(smem + C::kOffInfo + sl * 16) =
+                make_float4(lv, vinv * static_cast<float>(1 << kVUp), wide ? 1.f : 0.f, 0.f);
+          mbar_arrive(bar(bSf + sl));                  // each lane releases its own stores
+        }
+      } while (next(c));
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ converters
+    setmaxnreg_dec<80>();
+    const int cw = warp - 8, c8 = lane & 7, rsub = lane >> 3;
+    constexpr int CH = D / 16;                        // 16-code chunks of a row
+    int64_t q = 0;
+    Cursor c;
+    start(c);
+    do {
+      for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
+        const int sl = static_cast<int>(q % kScSlots), vs = static_cast<int>(q % kVStages),
+                  fs = static_cast<int>(q % kFStages);
+        wait_all(bSf + sl, ph(q, kScSlots), kDevTimeoutEpilogue);
+        wait_all(bVf + vs, ph(q, kVStages), kDevTimeoutEpilogue);
+        wait_all(bFe + fs, ph(q, kFStages) ^ 1u, kDevTimeoutEpilogue);
+        const uint8_t* src = smem + C::kOffV + vs * C::kK;
+        uint8_t* dst = smem + C::kOffF + fs * C::kV16;
+        const float* rv = reinterpret_cast<const float*>(smem + C::kOffRv) + sl * kTile;
+        constexpr int RPI = 32 / CH;                  // rows a warp takes at once
+        const int ch = D == 128 ? c8 : lane & 3, sub = D == 128 ? rsub : lane >> 2;
+#pragma unroll 2
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int row = cw * 32 + i * RPI + sub;
+          const uint32_t so = D == 128 ? static_cast<uint32_t>(row * 128 + ((ch ^ (row & 7)) << 4))
+                                       : static_cast<uint32_t>(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
+          const uint4 w = *reinterpret_cast<const uint4*>(src + so);
+          const float r = rv[row];
+          uint32_t o[8];
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float f[4];
+            e4m3x4_to_f32(ww[e], f);
+            o[2 * e] = pack_f16x2(f[0] * r, f[1] * r);
+            o[2 * e + 1] = pack_f16x2(f[2] * r, f[3] * r);
+          }
+          if (r == 0.f) {                             // unused places may hold anything
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = 0u;
+          }
+          // two 16-byte chunks of the row's 64-column half; lanes of the second half store them in
+          // the other order, so that a quarter-warp's stores fall on different banks
+          const int half = ch >> 2, c0 = 2 * (ch & 3);
+          uint8_t* drow = dst + half * C::kHalf + row * 128;
+          const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+          const int f0 = half & 1;
+          *reinterpret_cast<uint4*>(drow + (((c0 + f0) ^ (row & 7)) << 4)) = f0 ? hi : lo;
+          *reinterpret_cast<uint4*>(drow + (((c0 + 1 - f0) ^ (row & 7)) << 4)) = f0 ? lo : hi;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(bFf + fs));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(bVe + vs));
+          mbar_arrive(bar(bSe + sl));
+        }
+      }
+    } while (next(c));
+  } else {
+    // --------------------------------------------------------------- softmax
+    setmaxnreg_inc<192>();
+    const int t = warp >> 2;                          // query tile of this warpgroup
+    const int r = (warp & 3) * 32 + lane;             // row of the tile
+    const uint32_t tS = tmem + t * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t tO = tS - t * 128 + C::kColO + t * 128;
+    int64_t q = 0;
+    uint32_t item = 0, sp = 0;                        // blocks done; S phases
+    Cursor c;
+    start(c);
+    bool more = true;
+    while (more) {
+      // ---- this row's query, as two e4m3 rows
+      const int64_t R = static_cast<int64_t>(c.rb) * kBlockRows + t * kTile + r;
+      const int32_t i = static_cast<int32_t>(R / a.group);
+      const int head = c.h * a.group + static_cast<int>(R - static_cast<int64_t>(i) * a.group);
+      const bool live = i < c.w.q_len;
+      float cq;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (c.w.row0 + (live ? i : 0)) * a.q_st + head * a.q_sh);
+        uint4 raw[D / 8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          raw[j] = live ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+          // largest magnitude of the bf16 pairs: the halves compare as integers
+          const uint32_t ww[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = __vmaxu2(top, ww[e] & 0x7FFF7FFFu);
+        }
+        top = (top >> 16) > (top & 0xFFFFu) ? top >> 16 : top & 0xFFFFu;
+        int ex = static_cast<int>(top >> 7) - 127;
+        if (ex < -126) ex = -126;
+        const int sh = 7 - ex, s1 = sh / 2, s2 = sh - s1;           // |q| 2^sh < 2^8
+        float f1 = __uint_as_float(static_cast<uint32_t>(127 + s1) << 23);
+        const float f2 = __uint_as_float(static_cast<uint32_t>(127 + s2) << 23);
+        const float d1 = __uint_as_float(static_cast<uint32_t>(127 - s1) << 23);
+        const float d2 = __uint_as_float(static_cast<uint32_t>(127 - s2) << 23);
+        cq = fmaxf(fabsf(a.scale) * 1.4426950408889634f * d1 * d2, 1.2e-38f);
+        if (a.scale < 0.f) f1 = -f1;
+        if (a.scale == 0.f) f1 = 0.f;
+        uint8_t* qh = smem + C::kOffQ + 2 * t * C::kQ;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4& u = raw[2 * j + (e >> 1)];
+            const uint32_t w0 = e & 1 ? u.z : u.x, w1 = e & 1 ? u.w : u.y;
+            const float f[4] = {__uint_as_float(w0 << 16) * f1 * f2, __uint_as_float(w0 & 0xFFFF0000u) * f1 * f2,
+                                __uint_as_float(w1 << 16) * f1 * f2, __uint_as_float(w1 & 0xFFFF0000u) * f1 * f2};
+            hi[e] = cvt_e4m3x2(f[0], f[1]) | (static_cast<uint32_t>(cvt_e4m3x2(f[2], f[3])) << 16);
+            float back[4];
+            e4m3x4_to_f32(hi[e], back);
+            lo[e] = cvt_e4m3x2(f[0] - back[0], f[1] - back[1]) |
+                    (static_cast<uint32_t>(cvt_e4m3x2(f[2] - back[2], f[3] - back[3])) << 16);
+          }
+          const uint32_t off = D == 128 ? static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4))
+                                        : static_cast<uint32_t>(r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+          *reinterpret_cast<uint4*>(qh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(qh + C::kQ + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(bQ + t));
+      int32_t lo = 0, hi = 0;
+      if (live) seen_range(a, c.w.kv_len, c.w.pos0 + i, lo, hi);
+
+      float m = kNoMax, l = 0.f;
+      const int32_t ub = c.t0 / kTile;
+      for (int32_t k = c.k0; k < c.k1; ++k, ++q, ++sp) {
+        const int sl = static_cast<int>(q % kScSlots);
+        wait_all(bS + t, sp & 1, kDevTimeoutEpilogue);
+        wait_all(bSf + sl, ph(q, kScSlots), kDevTimeoutEpilogue);
+        tc_fence_after();
+        const float4 info = *reinterpret_cast<const float4*>(smem + C::kOffInfo + sl * 16);
+        const float lv = info.x;
+        const float4* ks4 = reinterpret_cast<const float4*>(smem + C::kOffKs) + sl * (kTile / 4);
+        const int32_t j0 = (ub + k) * kTile;
+        // ---- scores with the key scales, masked
+        float x[kTile];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t s[32];
+          tmem_ld32(tS + 32 * g, s);
+          tmem_wait_ld();
+          reg_fence32(s);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 kv = ks4[8 * g + e];
+            x[32 * g + 4 * e] = __uint_as_float(s[4 * e]) * kv.x;
+            x[32 * g + 4 * e + 1] = __uint_as_float(s[4 * e + 1]) * kv.y;
+            x[32 * g + 4 * e + 2] = __uint_as_float(s[4 * e + 2]) * kv.z;
+            x[32 * g + 4 * e + 3] = __uint_as_float(s[4 * e + 3]) * kv.w;
+          }
+        }
+        if (__any_sync(0xffffffffu, lo > j0 || hi < j0 + kTile)) {
+          const int32_t from = lo - j0, to = hi - j0;
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) x[j] = j >= from && j < to ? x[j] : -INFINITY;
+        }
+        const bool wide = info.z != 0.f;
+        if (wide) {
+          // per-token scales join the exponent: cq x + dl
+          const float* dl = reinterpret_cast<const float*>(smem + C::kOffDl) + sl * kTile;
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) x[j] = x[j] * cq + dl[j];
+        }
+        const float cc = wide ? 1.f : cq;
+        float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+#pragma unroll
+        for (int j = 4; j < kTile; j += 4) {
+          mx0 = fmaxf(mx0, x[j]);
+          mx1 = fmaxf(mx1, x[j + 1]);
+          mx2 = fmaxf(mx2, x[j + 2]);
+          mx3 = fmaxf(mx3, x[j + 3]);
+        }
+        const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * cc + lv;
+        if (__any_sync(0xffffffffu, top > m + kLag)) {
+          const float mn = fmaxf(m, top);
+          const float f = ex2(m - mn);
+          m = mn;
+          l *= f;
+          if (k > c.k0) {
+#pragma unroll 1
+            for (int g = 0; g < D / 16; ++g) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16 * g, o);
+              tmem_wait_ld();
+              reg_fence16(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(tO + 16 * g, o);
+            }
+          }
+        }
+        // ---- weights
+        const float off = lv - m + kLift;
+        float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const int j = 32 * g + 2 * e;
+            const float p0 = ex2(fmaf(x[j], cc, off)), p1 = ex2(fmaf(x[j + 1], cc, off));
+            const float p2 = ex2(fmaf(x[j + 2], cc, off)), p3 = ex2(fmaf(x[j + 3], cc, off));
+            pk[e] = pack_f16x2(p0, p1);
+            pk[e + 1] = pack_f16x2(p2, p3);
+            if (wide) {
+              x[j] = p0;
+              x[j + 1] = p1;
+              x[j + 2] = p2;
+              x[j + 3] = p3;
+            } else {
+              sum0 += p0;
+              sum1 += p1;
+              sum2 += p2;
+              sum3 += p3;
+            }
+          }
+          tmem_st16(tS + 16 * g, pk);
+        }
+        if (wide) {
+          const float* iv = reinterpret_cast<const float*>(smem + C::kOffIv) + sl * kTile;
+#pragma unroll
+          for (int j = 0; j < kTile; j += 2) {
+            sum0 = fmaf(x[j], iv[j], sum0);
+            sum1 = fmaf(x[j + 1], iv[j + 1], sum1);
+          }
+          l += sum0 + sum1;
+        } else {
+          l = fmaf((sum0 + sum1) + (sum2 + sum3), info.y, l);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(bP + t));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bSe + sl));
+      }
+
+      // ---- output rows
+      wait_all(bO + t, item & 1, kDevTimeoutEpilogue);
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float lse2 = l > 0.f ? m - kLift + log2f(l) : -INFINITY;
+      const bool whole = c.k0 == 0 && c.k1 == c.n;
+      const int slot_id = 2 * blockIdx.x + (c.item0 + c.k0 == u0 ? 0 : 1);
+      float* part = p.partials + slot_id * slot_floats<D>();
+      float* part_lse = part + kBlockRows * D;
+      __nv_bfloat16* dst = a.out + (c.w.row0 + (live ? i : 0)) * a.o_st + head * a.o_sh;
+#pragma unroll 1
+      for (int g = 0; g < D / 32; ++g) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * g, o);
+        tmem_wait_ld();
+        reg_fence32(o);
+        if (whole) {
+          if (live && ok) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              st_global_v4(dst + 32 * g + e,
+                           pack_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv),
+                           pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv),
+                           pack_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv),
+                           pack_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + ((t * (D / 4) + 8 * g + e / 4) * kTile + r) * 4) =
+                make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                            __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+        }
+      }
+      if (whole) {
+        if (live && ok && a.lse != nullptr) a.lse[(c.w.row0 + i) * a.heads + head] = lse2 * 0.6931471805599453f;
+      } else {
+        part_lse[t * kTile + r] = lse2;
+        const int64_t i0 = c.item0, i1 = c.item0 + c.n;
+        const int c_first = static_cast<int>(((i0 + 1) * ctas - 1) / total);
+        const int c_last = static_cast<int>((i1 * ctas - 1) / total);
+        __threadfence();
+        named_bar_sync(1 + t, kTile);
+        if (r == 0) {
+          const int n = atomicAdd(p.counters + 2 * c_first + t, 1);
+          s_last[t] = n == c_last - c_first;
+          if (s_last[t]) p.counters[2 * c_first + t] = 0;
+        }
+        named_bar_sync(1 + t, kTile);
+        if (s_last[t]) {
+          __threadfence();
+          auto slot_of = [&](int cta) -> const float* {
+            return p.partials + (2 * cta + (i0 <= cta * total / ctas ? 0 : 1)) * slot_floats<D>();
+          };
+          float best = -INFINITY;
+          for (int cta = c_first; cta <= c_last; ++cta)
+            best = fmaxf(best, __ldcg(slot_of(cta) + kBlockRows * D + t * kTile + r));
+          const float ref = best == -INFINITY ? 0.f : best;
+          float sum = 0.f;
+#pragma unroll 1
+          for (int g = 0; g < D / 32; ++g) {
+            float o[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            sum = 0.f;
+            for (int cta = c_first; cta <= c_last; ++cta) {
+              const float* src = slot_of(cta);
+              const float w = ex2(__ldcg(src + kBlockRows * D + t * kTile + r) - ref);
+              sum += w;
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                    src + ((t * (D / 4) + 8 * g + e / 4) * kTile + r) * 4));
+                o[e] = fmaf(v.x, w, o[e]);
+                o[e + 1] = fmaf(v.y, w, o[e + 1]);
+                o[e + 2] = fmaf(v.z, w, o[e + 2]);
+                o[e + 3] = fmaf(v.w, w, o[e + 3]);
+              }
+            }
+            const float is = sum > 0.f ? 1.f / sum : 0.f;
+            if (live && ok) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                st_global_v4(dst + 32 * g + e, pack_bf16x2(o[e] * is, o[e + 1] * is),
+                             pack_bf16x2(o[e + 2] * is, o[e + 3] * is), pack_bf16x2(o[e + 4] * is, o[e + 5] * is),
+                             pack_bf16x2(o[e + 6] * is, o[e + 7] * is));
+            }
+          }
+          if (live && ok && a.lse != nullptr)
+            a.lse[(c.w.row0 + i) * a.heads + head] = sum > 0.f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+      tc_fence_before();                       // O and S are read: the next block may overwrite them
+      ++item;
+      more = next(c);
+    }
+  }
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_tile(const CUtensorMap& k, const CUtensorMap& v, const TileArgs& p, int ctas, cudaStream_t stream) {
+  using C = TileCfg<D>;
+  cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_tile_kernel<D>, k, v, p);
+}
+
+}  // namespace
+
+size_t attn_tile_partial_bytes(int dim, int ctas) {
+  return static_cast<size_t>(2) * ctas * (dim == 128 ? slot_floats<128>() : slot_floats<64>()) * sizeof(float);
+}
+
+cudaError_t launch_attn_tile(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int ctas, int32_t* counters,
+                             float* partials, cudaStream_t stream) {
+  TileArgs p;
+  p.a = a;
+  p.counters = counters;
+  p.partials = partials;
+  p.wait_limit = 1ull << 31;
+  p.min_tiles = 4;
+  return a.c.dim == 128 ? launch_tile<128>(k, v, p, ctas, stream) : launch_tile<64>(k, v, p, ctas, stream);
+}
+
+}  // namespace bfp8
