@@ -70,7 +70,8 @@ struct TileCfg {
   static constexpr int kOffDl = kOffRv + kScSlots * kTile * 4;   // wide tiles: log2 vs - lv
   static constexpr int kOffIv = kOffDl + kScSlots * kTile * 4;   // wide tiles: 1 / vs
   static constexpr int kOffInfo = kOffIv + kScSlots * kTile * 4; // lv, 2^-lv, wide
-  static constexpr int kOffBar = kOffInfo + kScSlots * 16;
+  static constexpr int kOffCur = kOffInfo + kScSlots * 16;       // a cursor a warp
+  static constexpr int kOffBar = kOffCur + (kTileThreads / 32) * 80;
   static constexpr int kBars = 2 * kKStages + 2 * kVStages + 2 * kFStages + 3 * kScSlots + 8;
   static constexpr int kSmem = kOffBar + kBars * 8 + 64 + 1024;
   static constexpr uint32_t kColO = 256;                  // S (and P) of the tiles at 0 and 128
@@ -122,13 +123,24 @@ __device__ __forceinline__ int32_t block_tiles(const AttnArgs& a, const SeqBlock
   return hi > lo ? (hi + kTile - 1) / kTile - lo / kTile : 1;
 }
 
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+// MMAs whose descriptors come as low words (start address >> 4 and leading
+// offset) and a constant high word: the issuing thread keeps few registers.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // kind::f16, A = B = f16, D = f32, A K-major, B MN-major (bit 16).
@@ -171,6 +183,15 @@ __device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i])::"memory");
 }
 
+struct Cursor {
+  int64_t item0;
+  SeqBlocks w;
+  int32_t b, h, rb;
+  int32_t n, k0, k1;
+  int32_t t0, t1;
+};
+static_assert(sizeof(Cursor) <= 80, "space of a warp's cursor");
+
 template <int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -190,6 +211,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             bQ = bSe + kScSlots, bS = bQ + 2, bP = bS + 2, bO = bP + 2;
   __shared__ uint32_t s_tmem;
   __shared__ int64_t s_before, s_total;
+  __shared__ int64_t s_u0, s_u1;                 // this CTA's share of the line of s_total tiles
+  __shared__ int s_ctas;
   __shared__ int s_b;
   __shared__ int s_last[2];
 
@@ -253,16 +276,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     run += s_total;
     __syncthreads();
   }
-  const int64_t total = run * H;
-  int64_t ctas = total / p.min_tiles;
-  if (ctas < 1) ctas = 1;
-  if (ctas > gridDim.x) ctas = gridDim.x;
-  if (total == 0 || blockIdx.x >= ctas) return;         // whole CTA: nothing allocated or in flight yet
-  const int64_t u0 = blockIdx.x * total / ctas, u1 = (blockIdx.x + 1) * total / ctas;
+  {
+    const int64_t total = run * H;
+    int64_t ctas = total / p.min_tiles;
+    if (ctas < 1) ctas = 1;
+    if (ctas > gridDim.x) ctas = gridDim.x;
+    if (total == 0 || blockIdx.x >= ctas) return;       // whole CTA: nothing allocated or in flight yet
+    if (tid == 0) {
+      s_total = total;
+      s_ctas = static_cast<int>(ctas);
+      s_u0 = blockIdx.x * total / ctas;
+      s_u1 = (blockIdx.x + 1) * total / ctas;
+    }
+    __syncthreads();
+  }
   run = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kSeqChunk) {
     const int n = a.batch <= kSeqChunk ? a.batch : count_chunk(b0);
     if (warp == 0) {
+      const int64_t u0 = s_u0;
       for (int i0 = 0; i0 < n; i0 += 32) {
         const int64_t own = i0 + lane < n ? cnt[i0 + lane] : 0;
         int64_t v = own;
@@ -291,18 +323,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
-  // cursor over the share: block (b, h, rb), its tiles [k0, k1) here, its place in the line
-  struct Cursor {
-    int b, h, rb;
-    int64_t item0;
-    int32_t n, k0, k1;
-    int32_t t0, t1;
-    SeqBlocks w;
-  };
-  auto clip = [&](Cursor& c) {
-    c.k0 = static_cast<int32_t>(u0 > c.item0 ? u0 - c.item0 : 0);
-    c.k1 = static_cast<int32_t>(c.item0 + c.n < u1 ? c.n : u1 - c.item0);
-  };
+  // Cursor over the share: block (b, h, rb), its tiles [k0, k1) here, its place
+  // in the line.  Each warp has one in shared memory, kept by its first lane:
+  // the loops over tiles need their registers for other things.
   auto step_block = [&](Cursor& c) {            // the block after (b, h, rb)
     if (++c.rb == c.w.blocks) {
       c.rb = 0;
@@ -315,25 +338,41 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     c.n = block_tiles(a, c.w, c.rb, c.t0, c.t1);
   };
-  auto start = [&](Cursor& c) {
-    c.b = s_b;
-    c.w = seq_blocks(a, c.b);
-    c.rb = 0;
-    c.h = 0;
-    c.item0 = s_before;
-    c.n = block_tiles(a, c.w, 0, c.t0, c.t1);
-    while (c.item0 + c.n <= u0) {
-      c.item0 += c.n;
-      step_block(c);
-    }
-    clip(c);
+  auto clip = [&](Cursor& c) {
+    c.k0 = static_cast<int32_t>(s_u0 > c.item0 ? s_u0 - c.item0 : 0);
+    c.k1 = static_cast<int32_t>(c.item0 + c.n < s_u1 ? c.n : s_u1 - c.item0);
   };
-  auto next = [&](Cursor& c) -> bool {
-    c.item0 += c.n;
-    if (c.item0 >= u1) return false;
-    step_block(c);
-    clip(c);
-    return true;
+  Cursor& c = reinterpret_cast<Cursor*>(smem + C::kOffCur)[warp];
+  auto start = [&]() {
+    if (lane == 0) {
+      c.b = s_b;
+      c.w = seq_blocks(a, c.b);
+      c.rb = 0;
+      c.h = 0;
+      c.item0 = s_before;
+      c.n = block_tiles(a, c.w, 0, c.t0, c.t1);
+      while (c.item0 + c.n <= s_u0) {
+        c.item0 += c.n;
+        step_block(c);
+      }
+      clip(c);
+    }
+    __syncwarp();
+  };
+  auto next = [&]() -> bool {                   // false: the share is done
+    __syncwarp();
+    int more = 0;
+    if (lane == 0) {
+      c.item0 += c.n;
+      if (c.item0 < s_u1) {
+        step_block(c);
+        clip(c);
+        more = 1;
+      }
+    }
+    more = __shfl_sync(0xffffffffu, more, 0);
+    __syncwarp();
+    return more != 0;
   };
 
   bool ok = true;
@@ -352,7 +391,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     ok = __all_sync(0xffffffffu, r);
     if (!ok && lane == 0) report_failure(a.err, code);
   };
-  auto ph = [](int64_t q, int stages) { return static_cast<uint32_t>((q / stages) & 1); };
+  auto ph = [](uint32_t q, int stages) { return (q / static_cast<uint32_t>(stages)) & 1u; };
 
   if (warp >= 12) {
     setmaxnreg_dec<48>();
@@ -361,9 +400,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int page = a.c.page_size, shift = a.c.page_shift;
       const int ppu = page >= kTile ? 1 : kTile / page;
       const int box = page >= kTile ? kTile : page;
-      int64_t q = 0;
-      Cursor c;
-      start(c);
+      uint32_t q = 0;
+      start();
       do {
         const int32_t ub = c.t0 / kTile;
         const int32_t* row = a.table + c.b * a.ld_table;
@@ -421,10 +459,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tma_load_4d(sbase + static_cast<uint32_t>(C::kOffV + vs * C::kK + lane * box * D), &tmV, bar(bVf + vs), 0,
                         off, c.h, pg);
         }
-      } while (ok && next(c));
+      } while (next() && ok);
       // no copy may still be landing when the CTA exits (after a failure: bounded waits all the same)
       auto drain = [&](int b0, int stages) {
-        for (int64_t i = q > stages ? q - stages : 0; i < q; ++i)
+        for (uint32_t i = q > static_cast<uint32_t>(stages) ? q - stages : 0; i < q; ++i)
           if (lane == 0 && !mbar_wait_bounded(bar(b0 + static_cast<int>(i % stages)), ph(i, stages), p.wait_limit)) {
             report_failure(a.err, kDevTimeoutTail);
             break;
@@ -436,62 +474,61 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       drain(bVf, kVStages);
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------- MMA
-      if (lane == 0) {
-        const uint32_t idS = idesc_e4m3_f32(128, 128), idO = idesc_f16_bmn(128, D);
-        auto wait1 = [&](int i, uint32_t parity) {
-          if (ok && !mbar_wait_bounded(bar(i), parity, p.wait_limit)) {
-            report_failure(a.err, kDevTimeoutMma);
-            ok = false;
-          }
-          return ok;
-        };
-        auto desc = [&](int off) {
-          return D == 128 ? sdesc_k_sw128(sbase + static_cast<uint32_t>(off))
-                          : sdesc_k_sw64(sbase + static_cast<uint32_t>(off));
-        };
-        auto qk = [&](int t, int ks) {
-          const uint64_t kd = desc(C::kOffK + ks * C::kK);
+      // the whole warp walks; its first lane waits and issues
+      const uint32_t idS = idesc_e4m3_f32(128, 128), idO = idesc_f16_bmn(128, D);
+      auto wait1 = [&](int i, uint32_t parity) {
+        if (ok && !mbar_wait_bounded(bar(i), parity, p.wait_limit)) {
+          report_failure(a.err, kDevTimeoutMma);
+          ok = false;
+        }
+        return ok;
+      };
+      const uint64_t kdesc = D == 128 ? sdesc_k_sw128(sbase) : sdesc_k_sw64(sbase), vdesc = sdesc_mn_sw128(sbase, C::kHalf);
+      const uint32_t klo = static_cast<uint32_t>(kdesc), khi = static_cast<uint32_t>(kdesc >> 32),
+                     vlo = static_cast<uint32_t>(vdesc), vhi = static_cast<uint32_t>(vdesc >> 32);
+      auto qk = [&](int t, int ks) {
+        const uint32_t kd = klo + (C::kOffK >> 4) + ks * (C::kK >> 4), qd = klo + (C::kOffQ >> 4) + 2 * t * (C::kQ >> 4);
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const uint64_t qd = desc(C::kOffQ + (2 * t + part) * C::kQ);
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              mma_f8f6f4(tmem + t * 128, qd + 2 * i, kd + 2 * i, idS, (part | i) != 0);
-          }
-        };
-        auto pv = [&](int t, int fs, bool first) {
-          const uint64_t vd = sdesc_mn_sw128(sbase + static_cast<uint32_t>(C::kOffF + fs * C::kV16), C::kHalf);
+          for (int i = 0; i < D / 32; ++i)
+            mma_f8_ss(tmem + t * 128, qd + part * (C::kQ >> 4) + 2 * i, kd + 2 * i, khi, idS, (part | i) != 0);
+      };
+      auto pv = [&](int t, int fs, bool first) {
+        const uint32_t vd = vlo + (C::kOffF >> 4) + fs * (C::kV16 >> 4);
 #pragma unroll
-          for (int i = 0; i < kTile / 16; ++i)
-            mma_f16_ts(tmem + C::kColO + t * 128, tmem + t * 128 + 8 * i, vd + 128 * i, idO, !(first && i == 0));
-        };
-        int64_t q = 0, done = 0;
-        uint32_t item = 0, pp = 0;               // blocks done; P phases
-        Cursor c;
-        start(c);
-        do {
+        for (int i = 0; i < kTile / 16; ++i)
+          mma_f16_ts(tmem + C::kColO + t * 128, tmem + t * 128 + 8 * i, vd + 128 * i, vhi, idO, !(first && i == 0));
+      };
+      uint32_t q = 0, done = 0;                  // stages are counted in 32 bits: at most 2^30 tokens an item
+      uint32_t item = 0;
+      start();
+      do {
+        const int32_t n = c.k1 - c.k0;
+        if (lane == 0 && ok) {
           wait1(bQ, item & 1);
           wait1(bQ + 1, item & 1);
           wait1(bKf + static_cast<int>(q % kKStages), ph(q, kKStages));
-          if (!ok) break;
-          tc_fence_after();
-          qk(0, static_cast<int>(q % kKStages));
-          mma_commit(bar(bS));
-          qk(1, static_cast<int>(q % kKStages));
-          mma_commit(bar(bS + 1));
-          mma_commit(bar(bKe + static_cast<int>(q % kKStages)));
-          for (int32_t k = c.k0; k < c.k1 && ok; ++k, ++q, ++pp) {
-            const bool more = k + 1 < c.k1;
+          if (ok) {
+            tc_fence_after();
+            qk(0, static_cast<int>(q % kKStages));
+            mma_commit(bar(bS));
+            qk(1, static_cast<int>(q % kKStages));
+            mma_commit(bar(bS + 1));
+            mma_commit(bar(bKe + static_cast<int>(q % kKStages)));
+          }
+          for (int32_t k = 0; k < n && ok; ++k, ++q) {
+            const bool more = k + 1 < n;
             const int fs = static_cast<int>(q % kFStages), kn = static_cast<int>((q + 1) % kKStages);
             wait1(bFf + fs, ph(q, kFStages));
-            for (int t = 0; t < 2 && ok; ++t) {
-              if (!wait1(bP + t, pp & 1)) break;
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+              if (!wait1(bP + t, q & 1)) break;
               tc_fence_after();
-              pv(t, fs, k == c.k0);
+              pv(t, fs, k == 0);
               if (t == 1) mma_commit(bar(bFe + fs));
               if (more) {
                 if (t == 0 && !wait1(bKf + kn, ph(q + 1, kKStages))) break;
-                tc_fence_after();
                 qk(t, kn);
                 mma_commit(bar(bS + t));
                 if (t == 1) mma_commit(bar(bKe + kn));
@@ -502,19 +539,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (ok) done = q + 1;
           }
           ++item;
-        } while (ok && next(c));
-        // every commit has arrived before the CTA exits
-        for (int64_t i = done > kFStages ? done - kFStages : 0; i < done; ++i)
+        }
+      } while (next());
+      // every commit has arrived before the CTA exits
+      if (lane == 0) {
+        for (uint32_t i = done > kFStages ? done - kFStages : 0; i < done; ++i)
           mbar_wait_bounded(bar(bFe + static_cast<int>(i % kFStages)), ph(i, kFStages), p.wait_limit);
-        for (int64_t i = done > kKStages ? done - kKStages : 0; i < done; ++i)
+        for (uint32_t i = done > kKStages ? done - kKStages : 0; i < done; ++i)
           mbar_wait_bounded(bar(bKe + static_cast<int>(i % kKStages)), ph(i, kKStages), p.wait_limit);
       }
       __syncwarp();
     } else if (warp == kWarpScale) {
       // ---------------------------------------------- the tiles' scales
-      int64_t q = 0;
-      Cursor c;
-      start(c);
+      uint32_t q = 0;
+      start();
       do {
         const int32_t ub = c.t0 / kTile;
         for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
@@ -567,16 +605,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 make_float4(lv, vinv * static_cast<float>(1 << kVUp), wide ? 1.f : 0.f, 0.f);
           mbar_arrive(bar(bSf + sl));                  // each lane releases its own stores
         }
-      } while (next(c));
+      } while (next());
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ converters
     setmaxnreg_dec<80>();
     const int cw = warp - 8, c8 = lane & 7, rsub = lane >> 3;
     constexpr int CH = D / 16;                        // 16-code chunks of a row
-    int64_t q = 0;
-    Cursor c;
-    start(c);
+    uint32_t q = 0;
+    start();
     do {
       for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
         const int sl = static_cast<int>(q % kScSlots), vs = static_cast<int>(q % kVStages),
@@ -626,7 +663,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           mbar_arrive(bar(bSe + sl));
         }
       }
-    } while (next(c));
+    } while (next());
   } else {
     // --------------------------------------------------------------- softmax
     setmaxnreg_inc<192>();
@@ -634,10 +671,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int r = (warp & 3) * 32 + lane;             // row of the tile
     const uint32_t tS = tmem + t * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t tO = tS - t * 128 + C::kColO + t * 128;
-    int64_t q = 0;
-    uint32_t item = 0, sp = 0;                        // blocks done; S phases
-    Cursor c;
-    start(c);
+    uint32_t q = 0;
+    uint32_t item = 0;                                // blocks done
+    start();
     bool more = true;
     while (more) {
       // ---- this row's query, as two e4m3 rows
@@ -697,32 +733,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (live) seen_range(a, c.w.kv_len, c.w.pos0 + i, lo, hi);
 
       float m = kNoMax, l = 0.f;
-      const int32_t ub = c.t0 / kTile;
-      for (int32_t k = c.k0; k < c.k1; ++k, ++q, ++sp) {
+      const int32_t ub = c.t0 / kTile, k0 = c.k0, k1 = c.k1;
+      for (int32_t k = k0; k < k1; ++k, ++q) {
         const int sl = static_cast<int>(q % kScSlots);
-        wait_all(bS + t, sp & 1, kDevTimeoutEpilogue);
+        wait_all(bS + t, q & 1, kDevTimeoutEpilogue);
         wait_all(bSf + sl, ph(q, kScSlots), kDevTimeoutEpilogue);
         tc_fence_after();
         const float4 info = *reinterpret_cast<const float4*>(smem + C::kOffInfo + sl * 16);
         const float lv = info.x;
-        const float4* ks4 = reinterpret_cast<const float4*>(smem + C::kOffKs) + sl * (kTile / 4);
+        const ulonglong2* ks2 = reinterpret_cast<const ulonglong2*>(smem + C::kOffKs) + sl * (kTile / 4);
         const int32_t j0 = (ub + k) * kTile;
-        // ---- scores with the key scales, masked
+        // ---- scores with the key scales, masked; pairs of columns in 64-bit registers
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) tmem_ld32(tS + 32 * g, sr[g]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) reg_fence32(sr[g]);
         float x[kTile];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          uint32_t s[32];
-          tmem_ld32(tS + 32 * g, s);
-          tmem_wait_ld();
-          reg_fence32(s);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 kv = ks4[8 * g + e];
-            x[32 * g + 4 * e] = __uint_as_float(s[4 * e]) * kv.x;
-            x[32 * g + 4 * e + 1] = __uint_as_float(s[4 * e + 1]) * kv.y;
-            x[32 * g + 4 * e + 2] = __uint_as_float(s[4 * e + 2]) * kv.z;
-            x[32 * g + 4 * e + 3] = __uint_as_float(s[4 * e + 3]) * kv.w;
-          }
+        for (int j = 0; j < kTile; j += 4) {
+          const ulonglong2 kv = ks2[j / 4];
+          unpack_f32x2(mul_f32x2(pack_u32x2(sr[j / 32][j % 32], sr[j / 32][j % 32 + 1]), kv.x), x[j], x[j + 1]);
+          unpack_f32x2(mul_f32x2(pack_u32x2(sr[j / 32][j % 32 + 2], sr[j / 32][j % 32 + 3]), kv.y), x[j + 2], x[j + 3]);
         }
         if (__any_sync(0xffffffffu, lo > j0 || hi < j0 + kTile)) {
           const int32_t from = lo - j0, to = hi - j0;
@@ -730,28 +763,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int j = 0; j < kTile; ++j) x[j] = j >= from && j < to ? x[j] : -INFINITY;
         }
         const bool wide = info.z != 0.f;
+        float cc = cq;
         if (wide) {
           // per-token scales join the exponent: cq x + dl
           const float* dl = reinterpret_cast<const float*>(smem + C::kOffDl) + sl * kTile;
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) x[j] = x[j] * cq + dl[j];
+          for (int j = 0; j < kTile; ++j) x[j] = fmaf(x[j], cq, dl[j]);
+          cc = 1.f;
         }
-        const float cc = wide ? 1.f : cq;
-        float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+        float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int j = 4; j < kTile; j += 4) {
-          mx0 = fmaxf(mx0, x[j]);
-          mx1 = fmaxf(mx1, x[j + 1]);
-          mx2 = fmaxf(mx2, x[j + 2]);
-          mx3 = fmaxf(mx3, x[j + 3]);
-        }
-        const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * cc + lv;
+        for (int j = 4; j + 7 < kTile; j += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[kTile - 4 + e]);
+        const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), cc, lv);
         if (__any_sync(0xffffffffu, top > m + kLag)) {
           const float mn = fmaxf(m, top);
           const float f = ex2(m - mn);
           m = mn;
           l *= f;
-          if (k > c.k0) {
+          if (k > k0) {
 #pragma unroll 1
             for (int g = 0; g < D / 16; ++g) {
               uint32_t o[16];
@@ -766,41 +799,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         // ---- weights
         const float off = lv - m + kLift;
-        float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
+        if (wide) {
+          const float* iv = reinterpret_cast<const float*>(smem + C::kOffIv) + sl * kTile;
+          float ws = 0.f;
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) ws = fmaf(ex2(x[j] + off), iv[j], ws);
+          l += ws;
+        }
+        const uint64_t cc2 = pack_u32x2(__float_as_uint(cc), __float_as_uint(cc));
+        const uint64_t off2 = pack_u32x2(__float_as_uint(off), __float_as_uint(off));
+        uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
+          for (int e = 0; e < 16; ++e) {
             const int j = 32 * g + 2 * e;
-            const float p0 = ex2(fmaf(x[j], cc, off)), p1 = ex2(fmaf(x[j + 1], cc, off));
-            const float p2 = ex2(fmaf(x[j + 2], cc, off)), p3 = ex2(fmaf(x[j + 3], cc, off));
+            float p0, p1;
+            unpack_f32x2(fma_f32x2(pack_u32x2(__float_as_uint(x[j]), __float_as_uint(x[j + 1])), cc2, off2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
             pk[e] = pack_f16x2(p0, p1);
-            pk[e + 1] = pack_f16x2(p2, p3);
-            if (wide) {
-              x[j] = p0;
-              x[j + 1] = p1;
-              x[j + 2] = p2;
-              x[j + 3] = p3;
-            } else {
-              sum0 += p0;
-              sum1 += p1;
-              sum2 += p2;
-              sum3 += p3;
-            }
+            sum[e & 3] = add_f32x2(sum[e & 3], pack_u32x2(__float_as_uint(p0), __float_as_uint(p1)));
           }
           tmem_st16(tS + 16 * g, pk);
         }
-        if (wide) {
-          const float* iv = reinterpret_cast<const float*>(smem + C::kOffIv) + sl * kTile;
-#pragma unroll
-          for (int j = 0; j < kTile; j += 2) {
-            sum0 = fmaf(x[j], iv[j], sum0);
-            sum1 = fmaf(x[j + 1], iv[j + 1], sum1);
-          }
-          l += sum0 + sum1;
-        } else {
-          l = fmaf((sum0 + sum1) + (sum2 + sum3), info.y, l);
+        if (!wide) {
+          float s0, s1;
+          unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), s0, s1);
+          l = fmaf(s0 + s1, info.y, l);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -815,7 +842,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const float lse2 = l > 0.f ? m - kLift + log2f(l) : -INFINITY;
       const bool whole = c.k0 == 0 && c.k1 == c.n;
-      const int slot_id = 2 * blockIdx.x + (c.item0 + c.k0 == u0 ? 0 : 1);
+      const int slot_id = 2 * blockIdx.x + (c.item0 + c.k0 == s_u0 ? 0 : 1);
       float* part = p.partials + slot_id * slot_floats<D>();
       float* part_lse = part + kBlockRows * D;
       __nv_bfloat16* dst = a.out + (c.w.row0 + (live ? i : 0)) * a.o_st + head * a.o_sh;
@@ -847,7 +874,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (live && ok && a.lse != nullptr) a.lse[(c.w.row0 + i) * a.heads + head] = lse2 * 0.6931471805599453f;
       } else {
         part_lse[t * kTile + r] = lse2;
-        const int64_t i0 = c.item0, i1 = c.item0 + c.n;
+        const int64_t i0 = c.item0, i1 = c.item0 + c.n, total = s_total, ctas = s_ctas;
         const int c_first = static_cast<int>(((i0 + 1) * ctas - 1) / total);
         const int c_last = static_cast<int>((i1 * ctas - 1) / total);
         __threadfence();
@@ -903,7 +930,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       tc_fence_before();                       // O and S are read: the next block may overwrite them
       ++item;
-      more = next(c);
+      more = next();
     }
   }
   __syncthreads();
