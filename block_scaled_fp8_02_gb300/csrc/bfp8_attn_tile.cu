@@ -28,6 +28,7 @@
 // rows in the workspace and the last CTA to arrive adds them in CTA order.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -67,7 +68,7 @@ struct TileCfg {
   static constexpr int kOffRaw = kOffF + kFStages * kV16;     // scales as in the cache: K then V
   static constexpr int kOffKs = kOffRaw + kScSlots * 2 * kTile * 4;
   static constexpr int kOffRv = kOffKs + kScSlots * kTile * 4;
-  static constexpr int kOffDl = kOffRv + kScSlots * kTile * 4;   // wide tiles: log2 vs - lv
+  static constexpr int kOffDl = kOffRv + kScSlots * kTile * 8;   // wide tiles: log2 vs - lv
   static constexpr int kOffIv = kOffDl + kScSlots * kTile * 4;   // wide tiles: 1 / vs
   static constexpr int kOffInfo = kOffIv + kScSlots * kTile * 4; // lv, 2^-lv, wide
   static constexpr int kOffCur = kOffInfo + kScSlots * 16;       // a cursor a warp
@@ -567,7 +568,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             live[e] = tok + e >= c.t0 && tok + e < c.t1;
-            if (!live[e]) ks[e] = vs[e] = 0.f;
+            if (!live[e]) vs[e] = 0.f;
+            // masked scores are -inf before the key scale: it must not be zero or NaN
+            ks[e] = live[e] ? fmaxf(ks[e], 1.2e-38f) : 1.f;
             top = fmaxf(top, vs[e]);
             if (live[e]) low = fminf(low, vs[e]);
           }
@@ -582,7 +585,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const float vinv = __uint_as_float(0x7F000000u - bits);
           const bool wide = low < top * kWide;
           const float lv = static_cast<float>(static_cast<int>(bits >> 23) - 127 - kVUp);
-          float4 r, dl, iv;
+          float4 dl, iv;
           float rr[4], dd[4], ii[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -591,11 +594,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             dd[e] = vs[e] > 0.f ? lg2(vs[e] * vinv) : 0.f;
             ii[e] = (vs[e] > 0.f ? 1.f / vs[e] : vinv) * static_cast<float>(1 << kVUp);
           }
-          r = make_float4(rr[0], rr[1], rr[2], rr[3]);
           dl = make_float4(dd[0], dd[1], dd[2], dd[3]);
           iv = make_float4(ii[0], ii[1], ii[2], ii[3]);
-          *reinterpret_cast<float4*>(smem + C::kOffKs + (sl * kTile + lane * 4) * 4) = make_float4(ks[0], ks[1], ks[2], ks[3]);
-          *reinterpret_cast<float4*>(smem + C::kOffRv + (sl * kTile + lane * 4) * 4) = r;
+          *reinterpret_cast<float4*>(smem + C::kOffKs + (sl * kTile + lane * 4) * 4) =
+              wide ? make_float4(1.f, 1.f, 1.f, 1.f) : make_float4(ks[0], ks[1], ks[2], ks[3]);
+          // the value factor as two f16 numbers, each twice: rh + rl holds 22 bits of it
+          uint32_t rh[4], rl[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half h = __float2half_rn(rr[e]);
+            const __half d = __float2half_rn(rr[e] - __half2float(h));
+            rh[e] = __half_as_ushort(h) * 0x10001u;
+            rl[e] = __half_as_ushort(d) * 0x10001u;
+          }
+          uint4* rv = reinterpret_cast<uint4*>(smem + C::kOffRv + (sl * kTile + lane * 4) * 8);
+          rv[0] = make_uint4(rh[0], rl[0], rh[1], rl[1]);
+          rv[1] = make_uint4(rh[2], rl[2], rh[3], rl[3]);
           if (wide) {
             *reinterpret_cast<float4*>(smem + C::kOffDl + (sl * kTile + lane * 4) * 4) = dl;
             *reinterpret_cast<float4*>(smem + C::kOffIv + (sl * kTile + lane * 4) * 4) = iv;
@@ -623,7 +637,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         wait_all(bFe + fs, ph(q, kFStages) ^ 1u, kDevTimeoutEpilogue);
         const uint8_t* src = smem + C::kOffV + vs * C::kK;
         uint8_t* dst = smem + C::kOffF + fs * C::kV16;
-        const float* rv = reinterpret_cast<const float*>(smem + C::kOffRv) + sl * kTile;
+        const uint2* rv = reinterpret_cast<const uint2*>(smem + C::kOffRv) + sl * kTile;
         constexpr int RPI = 32 / CH;                  // rows a warp takes at once
         const int ch = D == 128 ? c8 : lane & 3, sub = D == 128 ? rsub : lane >> 2;
 #pragma unroll 2
@@ -632,17 +646,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint32_t so = D == 128 ? static_cast<uint32_t>(row * 128 + ((ch ^ (row & 7)) << 4))
                                        : static_cast<uint32_t>(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
           const uint4 w = *reinterpret_cast<const uint4*>(src + so);
-          const float r = rv[row];
+          const uint2 r = rv[row];
           uint32_t o[8];
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float f[4];
-            e4m3x4_to_f32(ww[e], f);
-            o[2 * e] = pack_f16x2(f[0] * r, f[1] * r);
-            o[2 * e + 1] = pack_f16x2(f[2] * r, f[3] * r);
+            // code * rh + (code * rl): one f16 rounding of the product, and 2^-22 of it
+            e4m3x4_to_f16(ww[e], o[2 * e], o[2 * e + 1]);
+            o[2 * e] = hfma2(o[2 * e], r.x, hmul2(o[2 * e], r.y));
+            o[2 * e + 1] = hfma2(o[2 * e + 1], r.x, hmul2(o[2 * e + 1], r.y));
           }
-          if (r == 0.f) {                             // unused places may hold anything
+          if (r.x == 0u) {                            // unused places may hold anything
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = 0u;
           }
@@ -743,41 +757,59 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float lv = info.x;
         const ulonglong2* ks2 = reinterpret_cast<const ulonglong2*>(smem + C::kOffKs) + sl * (kTile / 4);
         const int32_t j0 = (ub + k) * kTile;
-        // ---- scores with the key scales, masked; pairs of columns in 64-bit registers
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) tmem_ld32(tS + 32 * g, sr[g]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int g = 0; g < 4; ++g) reg_fence32(sr[g]);
-        float x[kTile];
-#pragma unroll
-        for (int j = 0; j < kTile; j += 4) {
-          const ulonglong2 kv = ks2[j / 4];
-          unpack_f32x2(mul_f32x2(pack_u32x2(sr[j / 32][j % 32], sr[j / 32][j % 32 + 1]), kv.x), x[j], x[j + 1]);
-          unpack_f32x2(mul_f32x2(pack_u32x2(sr[j / 32][j % 32 + 2], sr[j / 32][j % 32 + 3]), kv.y), x[j + 2], x[j + 3]);
-        }
-        if (__any_sync(0xffffffffu, lo > j0 || hi < j0 + kTile)) {
-          const int32_t from = lo - j0, to = hi - j0;
-#pragma unroll
-          for (int j = 0; j < kTile; ++j) x[j] = j >= from && j < to ? x[j] : -INFINITY;
-        }
         const bool wide = info.z != 0.f;
-        float cc = cq;
-        if (wide) {
-          // per-token scales join the exponent: cq x + dl
+        if (wide || __any_sync(0xffffffffu, lo > j0 || hi < j0 + kTile)) {
+          // few tiles: masked scores become -inf, and a wide tile's take their tokens' own scales
+          // (its ks are ones), in tensor memory
+          const int32_t from = lo - j0, to = hi - j0;
+          const float* kr = reinterpret_cast<const float*>(smem + C::kOffRaw) + sl * 2 * kTile;
           const float* dl = reinterpret_cast<const float*>(smem + C::kOffDl) + sl * kTile;
+#pragma unroll 1
+          for (int g = 0; g < kTile / 16; ++g) {
+            uint32_t o[16];
+            tmem_ld16(tS + 16 * g, o);
+            tmem_wait_ld();
+            reg_fence16(o);
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) x[j] = fmaf(x[j], cq, dl[j]);
-          cc = 1.f;
+            for (int e = 0; e < 16; ++e) {
+              const int j = 16 * g + e;
+              float v = __uint_as_float(o[e]);
+              if (wide) v = fmaf(v * kr[j], cq, dl[j]);
+              o[e] = __float_as_uint(j >= from && j < to ? v : -INFINITY);
+            }
+            tmem_st16(tS + 16 * g, o);
+          }
+          tmem_wait_st();
         }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
+        const float cc = wide ? 1.f : cq;
+        // ---- scores with the key scales, pairs of columns in 64-bit registers, a quarter's load under
+        // way while the one before it is scaled
+        uint64_t x[kTile / 2];
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        {
+          uint32_t sr[2][32];
+          tmem_ld32(tS, sr[0]);
 #pragma unroll
-        for (int j = 4; j + 7 < kTile; j += 8)
+          for (int g = 0; g < 4; ++g) {
+            uint64_t kv[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
+            for (int e = 0; e < 8; ++e) {
+              const ulonglong2 v = ks2[8 * g + e];
+              kv[2 * e] = v.x;
+              kv[2 * e + 1] = v.y;
+            }
+            tmem_wait_ld();
+            reg_fence32(sr[g & 1]);
+            if (g < 3) tmem_ld32(tS + 32 * (g + 1), sr[(g + 1) & 1]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[kTile - 4 + e]);
+            for (int e = 0; e < 16; ++e) {
+              x[16 * g + e] = mul_f32x2(pack_u32x2(sr[g & 1][2 * e], sr[g & 1][2 * e + 1]), kv[e]);
+              float e0, e1;
+              unpack_f32x2(x[16 * g + e], e0, e1);
+              mx[e & 3] = max3(mx[e & 3], e0, e1);
+            }
+          }
+        }
         const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), cc, lv);
         if (__any_sync(0xffffffffu, top > m + kLag)) {
           const float mn = fmaxf(m, top);
@@ -802,8 +834,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (wide) {
           const float* iv = reinterpret_cast<const float*>(smem + C::kOffIv) + sl * kTile;
           float ws = 0.f;
+#pragma unroll 1
+          for (int g = 0; g < kTile / 16; ++g) {
+            uint32_t o[16];
+            tmem_ld16(tS + 16 * g, o);
+            tmem_wait_ld();
+            reg_fence16(o);
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) ws = fmaf(ex2(x[j] + off), iv[j], ws);
+            for (int e = 0; e < 16; ++e) ws = fmaf(ex2(__uint_as_float(o[e]) + off), iv[16 * g + e], ws);
+          }
           l += ws;
         }
         const uint64_t cc2 = pack_u32x2(__float_as_uint(cc), __float_as_uint(cc));
@@ -814,9 +853,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int j = 32 * g + 2 * e;
             float p0, p1;
-            unpack_f32x2(fma_f32x2(pack_u32x2(__float_as_uint(x[j]), __float_as_uint(x[j + 1])), cc2, off2), p0, p1);
+            unpack_f32x2(fma_f32x2(x[16 * g + e], cc2, off2), p0, p1);
             p0 = ex2(p0);
             p1 = ex2(p1);
             pk[e] = pack_f16x2(p0, p1);
