@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   constexpr int kRows = NG * 8;
   const AttnArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  // aligned by an offset: the compiler has to see that this is shared memory
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_addr(smem);
   auto bar_full = [&](int s) { return sbase + static_cast<uint32_t>(C::kOffBar + 8 * s); };
   auto bar_empty = [&](int s) { return sbase + static_cast<uint32_t>(C::kOffBar + 8 * (C::kStages + s)); };

@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   using C = TileCfg<D>;
   const AttnArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  // aligned by an offset: the compiler has to see that this is shared memory
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.c.heads;
@@ -750,72 +750,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int32_t ub = c.t0 / kTile, k0 = c.k0, k1 = c.k1;
       for (int32_t k = k0; k < k1; ++k, ++q) {
         const int sl = static_cast<int>(q % kScSlots);
-        wait_all(bS + t, q & 1, kDevTimeoutEpilogue);
         wait_all(bSf + sl, ph(q, kScSlots), kDevTimeoutEpilogue);
-        tc_fence_after();
         const float4 info = *reinterpret_cast<const float4*>(smem + C::kOffInfo + sl * 16);
         const float lv = info.x;
-        const ulonglong2* ks2 = reinterpret_cast<const ulonglong2*>(smem + C::kOffKs) + sl * (kTile / 4);
-        const int32_t j0 = (ub + k) * kTile;
         const bool wide = info.z != 0.f;
-        if (wide || __any_sync(0xffffffffu, lo > j0 || hi < j0 + kTile)) {
-          // few tiles: masked scores become -inf, and a wide tile's take their tokens' own scales
-          // (its ks are ones), in tensor memory
-          const int32_t from = lo - j0, to = hi - j0;
-          const float* kr = reinterpret_cast<const float*>(smem + C::kOffRaw) + sl * 2 * kTile;
-          const float* dl = reinterpret_cast<const float*>(smem + C::kOffDl) + sl * kTile;
-#pragma unroll 1
-          for (int g = 0; g < kTile / 16; ++g) {
-            uint32_t o[16];
-            tmem_ld16(tS + 16 * g, o);
-            tmem_wait_ld();
-            reg_fence16(o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int j = 16 * g + e;
-              float v = __uint_as_float(o[e]);
-              if (wide) v = fmaf(v * kr[j], cq, dl[j]);
-              o[e] = __float_as_uint(j >= from && j < to ? v : -INFINITY);
-            }
-            tmem_st16(tS + 16 * g, o);
-          }
-          tmem_wait_st();
-        }
+        const ulonglong2* ks2 = reinterpret_cast<const ulonglong2*>(smem + C::kOffKs) + sl * (kTile / 4);
+        const int32_t from = lo - (ub + k) * kTile, to = hi - (ub + k) * kTile;
+        const bool odd = wide || __any_sync(0xffffffffu, from > 0 || to < kTile);
         const float cc = wide ? 1.f : cq;
-        // ---- scores with the key scales, pairs of columns in 64-bit registers, a quarter's load under
-        // way while the one before it is scaled
-        uint64_t x[kTile / 2];
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        {
-          uint32_t sr[2][32];
-          tmem_ld32(tS, sr[0]);
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint64_t kv[16];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const ulonglong2 v = ks2[8 * g + e];
-              kv[2 * e] = v.x;
-              kv[2 * e + 1] = v.y;
-            }
-            tmem_wait_ld();
-            reg_fence32(sr[g & 1]);
-            if (g < 3) tmem_ld32(tS + 32 * (g + 1), sr[(g + 1) & 1]);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              x[16 * g + e] = mul_f32x2(pack_u32x2(sr[g & 1][2 * e], sr[g & 1][2 * e + 1]), kv[e]);
-              float e0, e1;
-              unpack_f32x2(x[16 * g + e], e0, e1);
-              mx[e & 3] = max3(mx[e & 3], e0, e1);
-            }
-          }
-        }
-        const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), cc, lv);
-        if (__any_sync(0xffffffffu, top > m + kLag)) {
+        uint64_t sum[2] = {0, 0};
+        // moves the running maximum to `top` where it lags too far, `chunks` of this tile's weights being stored already
+        auto move_max = [&](float top, int chunks) {
           const float mn = fmaxf(m, top);
           const float f = ex2(m - mn);
           m = mn;
           l *= f;
+          const uint64_t f2 = pack_u32x2(__float_as_uint(f), __float_as_uint(f));
+          sum[0] = mul_f32x2(sum[0], f2);
+          sum[1] = mul_f32x2(sum[1], f2);
+          if (chunks > 0) {
+            tmem_wait_st();
+#pragma unroll 1
+            for (int g = 0; g < chunks; ++g) {
+              uint32_t o[16];
+              tmem_ld16(tS + 16 * g, o);
+              tmem_wait_ld();
+              reg_fence16(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&o[e]));
+                o[e] = pack_f16x2(v.x * f, v.y * f);
+              }
+              tmem_st16(tS + 16 * g, o);
+            }
+          }
           if (k > k0) {
 #pragma unroll 1
             for (int g = 0; g < D / 16; ++g) {
@@ -828,12 +796,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               tmem_st16(tO + 16 * g, o);
             }
           }
-        }
-        // ---- weights
-        const float off = lv - m + kLift;
-        if (wide) {
-          const float* iv = reinterpret_cast<const float*>(smem + C::kOffIv) + sl * kTile;
-          float ws = 0.f;
+        };
+        wait_all(bS + t, q & 1, kDevTimeoutEpilogue);
+        tc_fence_after();
+        if (odd) {
+          // few tiles: masked scores become -inf, and a wide tile's take their tokens' own scales
+          // (its ks are ones), in tensor memory
+          const float* kr = reinterpret_cast<const float*>(smem + C::kOffRaw) + sl * 2 * kTile;
+          const float* dl = reinterpret_cast<const float*>(smem + C::kOffDl) + sl * kTile;
+          float top = -INFINITY;
 #pragma unroll 1
           for (int g = 0; g < kTile / 16; ++g) {
             uint32_t o[16];
@@ -841,30 +812,92 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tmem_wait_ld();
             reg_fence16(o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ws = fmaf(ex2(__uint_as_float(o[e]) + off), iv[16 * g + e], ws);
+            for (int e = 0; e < 16; ++e) {
+              const int j = 16 * g + e;
+              float v = __uint_as_float(o[e]);
+              if (wide) v = fmaf(v * kr[j], cq, dl[j]);
+              v = j >= from && j < to ? v : -INFINITY;
+              top = fmaxf(top, v);
+              o[e] = __float_as_uint(v);
+            }
+            tmem_st16(tS + 16 * g, o);
           }
-          l += ws;
-        }
-        const uint64_t cc2 = pack_u32x2(__float_as_uint(cc), __float_as_uint(cc));
-        const uint64_t off2 = pack_u32x2(__float_as_uint(off), __float_as_uint(off));
-        uint64_t sum[4] = {0, 0, 0, 0};
+          tmem_wait_st();
+          if (wide) {
+            // its weights are summed here, by the maximum that the pass below then need not move
+            if (__any_sync(0xffffffffu, top + lv > m + kLag)) move_max(top + lv, 0);
+            const float* iv = reinterpret_cast<const float*>(smem + C::kOffIv) + sl * kTile;
+            const float off = lv - m + kLift;
+            float ws = 0.f;
+#pragma unroll 1
+            for (int g = 0; g < kTile / 16; ++g) {
+              uint32_t o[16];
+              tmem_ld16(tS + 16 * g, o);
+              tmem_wait_ld();
+              reg_fence16(o);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          uint32_t pk[16];
+              for (int e = 0; e < 16; ++e) ws = fmaf(ex2(__uint_as_float(o[e]) + off), iv[16 * g + e], ws);
+            }
+            l += ws;
+          }
+        }
+        // ---- one pass, 32 columns at a time and the next 32 under way: key scales, the running maximum
+        // (moved when the chunk passes it by more than kLag), weights.  Few live registers: with a
+        // whole row in them the compiler had none left to overlap anything (2000 cycles a row against
+        // 700 for this arithmetic alone)
+        const uint64_t cc2 = pack_u32x2(__float_as_uint(cc), __float_as_uint(cc));
+        auto weigh = [&](const uint32_t (&sr)[32], int chunk) {
+          uint64_t y[16];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const ulonglong2 kv = ks2[8 * chunk + e];
+            y[2 * e] = mul_f32x2(pack_u32x2(sr[4 * e], sr[4 * e + 1]), kv.x);
+            y[2 * e + 1] = mul_f32x2(pack_u32x2(sr[4 * e + 2], sr[4 * e + 3]), kv.y);
+          }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float p0, p1;
-            unpack_f32x2(fma_f32x2(x[16 * g + e], cc2, off2), p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            pk[e] = pack_f16x2(p0, p1);
-            sum[e & 3] = add_f32x2(sum[e & 3], pack_u32x2(__float_as_uint(p0), __float_as_uint(p1)));
+            float e0, e1;
+            unpack_f32x2(y[e], e0, e1);
+            mx[e & 3] = max3(mx[e & 3], e0, e1);
           }
-          tmem_st16(tS + 16 * g, pk);
+          const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), cc, lv);
+          if (__any_sync(0xffffffffu, top > m + kLag)) move_max(top, chunk);
+          const float off = lv - m + kLift;
+          const uint64_t off2 = pack_u32x2(__float_as_uint(off), __float_as_uint(off));
+          float w[32];
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) unpack_f32x2(fma_f32x2(y[e], cc2, off2), w[2 * e], w[2 * e + 1]);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = ex2(w[e]);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            pk[e] = pack_f16x2(w[2 * e], w[2 * e + 1]);
+            sum[e & 1] = add_f32x2(sum[e & 1], pack_u32x2(__float_as_uint(w[2 * e]), __float_as_uint(w[2 * e + 1])));
+          }
+          tmem_st16(tS + 16 * chunk, pk);
+        };
+        {
+          uint32_t sa[32], sb[32];
+          tmem_ld32(tS, sa);
+          tmem_wait_ld();
+          reg_fence32(sa);
+#pragma unroll 1
+          for (int g = 0; g < 2; ++g) {
+            tmem_ld32(tS + 64 * g + 32, sb);
+            weigh(sa, 2 * g);
+            tmem_wait_ld();
+            reg_fence32(sb);
+            if (g == 0) tmem_ld32(tS + 64, sa);
+            weigh(sb, 2 * g + 1);
+            tmem_wait_ld();
+            reg_fence32(sa);
+          }
         }
         if (!wide) {
           float s0, s1;
-          unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), s0, s1);
+          unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
           l = fmaf(s0 + s1, info.y, l);
         }
         tmem_wait_st();
