@@ -10,12 +10,11 @@
 //               as two e4m3 operands and S takes two passes: exact products at the
 //               time of one 16-bit pass, and no conversion of K.
 //   O += P V    kind::f16: P from tensor memory, over the columns of S; V converted
-//               from e4m3 by one warpgroup, scaled by its token's scale relative
+//               from e4m3 by two warps, scaled by its token's scale relative
 //               to the tile's largest (one f16 rounding).
 // Roles: two softmax warpgroups (a thread a row: scores from tensor memory, key
-// scales, mask, running maximum and sum, P, and the rare rescaling of O), one
-// converting V, and single warps for TMA, for the MMAs and for the tiles'
-// scales.
+// scales, mask, running maximum and sum, P, and the rare rescaling of O), two warps
+// converting V, one for the MMAs, and one for TMA and the tiles' scales.
 //
 // Scores x are in powers of two.  A tile's values share the scale 2^lv, which
 // joins the exponent: P = 2^(x + lv - mv + 7) with mv a running maximum of x + lv
@@ -45,8 +44,12 @@ namespace {
 
 constexpr int kTile = 128;                 // tokens of a tile, rows of a query tile
 constexpr int kBlockRows = 2 * kTile;
-constexpr int kTileThreads = 512;
-constexpr int kWarpTma = 12, kWarpMma = 13, kWarpScale = 14;
+// 8 softmax warps, one for the MMAs, one for TMA and the tiles' scales, two that
+// convert V.  Three warpgroups and no more: the compiler plans for the registers
+// that a thread has at launch (168), and with 128 the softmax ran at half speed.
+// 208 and 88 a thread after they are handed around.
+constexpr int kTileThreads = 384;
+constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpConv = 10, kConvWarps = 2;
 constexpr int kSeqChunk = 2048;            // sequences whose tile counts are held at once
 constexpr int kKStages = 3, kVStages = 2, kFStages = 2, kScSlots = 4;
 constexpr float kNoMax = -3.0e38f;
@@ -224,16 +227,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(bar(bVf + i), 1);
-      mbar_init(bar(bVe + i), 4);
+      mbar_init(bar(bVe + i), kConvWarps);
     }
     for (int i = 0; i < kFStages; ++i) {
-      mbar_init(bar(bFf + i), 128);
+      mbar_init(bar(bFf + i), 32 * kConvWarps);
       mbar_init(bar(bFe + i), 1);
     }
     for (int i = 0; i < kScSlots; ++i) {
       mbar_init(bar(bRf + i), 1);
       mbar_init(bar(bSf + i), 32);
-      mbar_init(bar(bSe + i), 12);
+      mbar_init(bar(bSe + i), 8 + kConvWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(bQ + i), 128);
@@ -394,27 +397,93 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   };
   auto ph = [](uint32_t q, int stages) { return (q / static_cast<uint32_t>(stages)) & 1u; };
 
-  if (warp >= 12) {
-    setmaxnreg_dec<48>();
-    if (warp == kWarpTma) {
-      // ------------------------------------------------------------- TMA
+  if (warp >= kWarpMma) {
+    setmaxnreg_dec<88>();
+    if (warp == kWarpLoad) {
+      // --------------------------------------------- TMA and the tiles' scales
+      // scales of tile q as the softmax and the converters take them, from the raw ones; run one
+      // tile after their load, before anything that waits for the tile's consumers
+      auto scales = [&](uint32_t q, int32_t tok0, int32_t t0, int32_t t1) {
+        const int sl = static_cast<int>(q % kScSlots);
+        wait_all(bRf + sl, ph(q, kScSlots), kDevTimeoutEpilogue);
+        const int32_t tok = tok0 + lane * 4;
+        const float4 kr = *reinterpret_cast<const float4*>(smem + C::kOffRaw + (sl * 2 * kTile + lane * 4) * 4);
+        const float4 vr = *reinterpret_cast<const float4*>(smem + C::kOffRaw + ((sl * 2 + 1) * kTile + lane * 4) * 4);
+        float ks[4] = {kr.x, kr.y, kr.z, kr.w}, vs[4] = {vr.x, vr.y, vr.z, vr.w};
+        bool live[4];
+        float top = 0.f, low = 3.0e38f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          live[e] = tok + e >= t0 && tok + e < t1;
+          if (!live[e]) vs[e] = 0.f;
+          // masked scores are -inf before the key scale: it must not be zero or NaN
+          ks[e] = live[e] ? fmaxf(ks[e], 1.2e-38f) : 1.f;
+          top = fmaxf(top, vs[e]);
+          if (live[e]) low = fminf(low, vs[e]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+        }
+        // vref = 2^E >= top; values are held as code * (vs / vref) * 2^kVUp, so 2^lv = vref 2^-kVUp
+        uint32_t bits = (__float_as_uint(top) + 0x7FFFFFu) & 0xFF800000u;
+        if (bits < 0x10000000u) bits = 0x10000000u;                    // 2^-95: an all-zero tile
+        const float vinv = __uint_as_float(0x7F000000u - bits);
+        const bool wide = low < top * kWide;
+        const float lv = static_cast<float>(static_cast<int>(bits >> 23) - 127 - kVUp);
+        float4 dl, iv;
+        float rr[4], dd[4], ii[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          rr[e] = !(vs[e] > 0.f) ? 0.f : wide ? static_cast<float>(1 << kVUp) : vs[e] * vinv * static_cast<float>(1 << kVUp);
+          // a scale of zero is a value of zero: its weight counts all the same
+          dd[e] = vs[e] > 0.f ? lg2(vs[e] * vinv) : 0.f;
+          ii[e] = (vs[e] > 0.f ? 1.f / vs[e] : vinv) * static_cast<float>(1 << kVUp);
+        }
+        dl = make_float4(dd[0], dd[1], dd[2], dd[3]);
+        iv = make_float4(ii[0], ii[1], ii[2], ii[3]);
+        *reinterpret_cast<float4*>(smem + C::kOffKs + (sl * kTile + lane * 4) * 4) =
+            wide ? make_float4(1.f, 1.f, 1.f, 1.f) : make_float4(ks[0], ks[1], ks[2], ks[3]);
+        // the value factor as two f16 numbers, each twice: rh + rl holds 22 bits of it
+        uint32_t rh[4], rl[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half h = __float2half_rn(rr[e]);
+          const __half d = __float2half_rn(rr[e] - __half2float(h));
+          rh[e] = __half_as_ushort(h) * 0x10001u;
+          rl[e] = __half_as_ushort(d) * 0x10001u;
+        }
+        uint4* rv = reinterpret_cast<uint4*>(smem + C::kOffRv + (sl * kTile + lane * 4) * 8);
+        rv[0] = make_uint4(rh[0], rl[0], rh[1], rl[1]);
+        rv[1] = make_uint4(rh[2], rl[2], rh[3], rl[3]);
+        if (wide) {
+          *reinterpret_cast<float4*>(smem + C::kOffDl + (sl * kTile + lane * 4) * 4) = dl;
+          *reinterpret_cast<float4*>(smem + C::kOffIv + (sl * kTile + lane * 4) * 4) = iv;
+        }
+        if (lane == 0)
+          *reinterpret_cast<float4*>(smem + C::kOffInfo + sl * 16) =
+              make_float4(lv, vinv * static_cast<float>(1 << kVUp), wide ? 1.f : 0.f, 0.f);
+        mbar_arrive(bar(bSf + sl));                  // each lane releases its own stores
+      };
       const int page = a.c.page_size, shift = a.c.page_shift;
       const int ppu = page >= kTile ? 1 : kTile / page;
       const int box = page >= kTile ? kTile : page;
-      uint32_t q = 0;
+      uint32_t q = 0, pending = 0;                      // loads begun; a tile whose scales wait
+      int32_t p_tok = 0, p_t0 = 0, p_t1 = 0;
       start();
       do {
-        const int32_t ub = c.t0 / kTile;
+        const int32_t ub = c.t0 / kTile, t0 = c.t0, t1 = c.t1, h = c.h, k1 = c.k1;
         const int32_t* row = a.table + c.b * a.ld_table;
         int32_t cached = -1, entry = 0;
-        for (int32_t k = c.k0; k < c.k1 && ok; ++k, ++q) {
+        for (int32_t k = c.k0; k < k1 && ok; ++k) {
           const int32_t tok = (ub + k) * kTile;
           const int32_t first = tok / box;
           if (first / 32 != cached) {
             cached = first / 32;
             const int64_t t = (static_cast<int64_t>(cached) * 32 + lane) * box;
             entry = 0;
-            if (t < c.t1 && t + box > c.t0) {
+            if (t < t1 && t + box > t0) {
               entry = __ldg(row + (t >> shift));
               if (entry < 0 || entry >= a.c.num_pages) {
                 report_failure(a.err, kDevBadCacheIndex);
@@ -423,7 +492,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
           const int32_t t = tok + lane * box;
-          const bool live = lane < ppu && t < c.t1 && t + box > c.t0;
+          const bool live = lane < ppu && t < t1 && t + box > t0;
           const int n = __popc(__ballot_sync(0xffffffffu, live));
           const int32_t pg = __shfl_sync(0xffffffffu, entry, (first + lane) & 31);
           const int off = t & (page - 1);
@@ -431,36 +500,39 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     vs = static_cast<int>(q % kVStages);
           wait_warp(bSe + sc, ph(q, kScSlots) ^ 1u, kDevTimeoutProducer);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(bar(bRf + sc), static_cast<uint32_t>(n * 2 * box * 4));
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(bRf + sc), static_cast<uint32_t>(n * 2 * box * 4));
+          }
           __syncwarp();
           if (live) {
-            const int64_t so = pg * a.c.ss_page + c.h * a.c.ss_head + off;
+            const int64_t so = pg * a.c.ss_page + h * a.c.ss_head + off;
             const uint32_t sd = sbase + static_cast<uint32_t>(C::kOffRaw + (sc * 2 * kTile + lane * box) * 4);
             bulk_load(sd, a.c.ks + so, box * 4, bar(bRf + sc));
             bulk_load(sd + kTile * 4, a.c.vs + so, box * 4, bar(bRf + sc));
           }
-          wait_warp(bKe + ks, ph(q, kKStages) ^ 1u, kDevTimeoutProducer);
-          if (!ok) {
-            ++q;
-            break;
-          }
+          ++q;                                          // its copies are in flight
+          if (pending) scales(q - 2, p_tok, p_t0, p_t1);
+          pending = 1;
+          p_tok = tok;
+          p_t0 = t0;
+          p_t1 = t1;
+          wait_warp(bKe + ks, ph(q - 1, kKStages) ^ 1u, kDevTimeoutProducer);
+          if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(bar(bKf + ks), static_cast<uint32_t>(n * box * D));
           __syncwarp();
           if (live)
             tma_load_4d(sbase + static_cast<uint32_t>(C::kOffK + ks * C::kK + lane * box * D), &tmK, bar(bKf + ks), 0,
-                        off, c.h, pg);
-          wait_warp(bVe + vs, ph(q, kVStages) ^ 1u, kDevTimeoutProducer);
-          if (!ok) {
-            ++q;
-            break;
-          }
+                        off, h, pg);
+          wait_warp(bVe + vs, ph(q - 1, kVStages) ^ 1u, kDevTimeoutProducer);
+          if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(bar(bVf + vs), static_cast<uint32_t>(n * box * D));
           __syncwarp();
           if (live)
             tma_load_4d(sbase + static_cast<uint32_t>(C::kOffV + vs * C::kK + lane * box * D), &tmV, bar(bVf + vs), 0,
-                        off, c.h, pg);
+                        off, h, pg);
         }
       } while (next() && ok);
+      if (pending) scales(q - 1, p_tok, p_t0, p_t1);
       // no copy may still be landing when the CTA exits (after a failure: bounded waits all the same)
       auto drain = [&](int b0, int stages) {
         for (uint32_t i = q > static_cast<uint32_t>(stages) ? q - stages : 0; i < q; ++i)
@@ -550,137 +622,66 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           mbar_wait_bounded(bar(bKe + static_cast<int>(i % kKStages)), ph(i, kKStages), p.wait_limit);
       }
       __syncwarp();
-    } else if (warp == kWarpScale) {
-      // ---------------------------------------------- the tiles' scales
+    } else {
+      // ---------------------------------------------------------- converters
+      const int cw = warp - kWarpConv, c8 = lane & 7, rsub = lane >> 3;
+      constexpr int CH = D / 16;                        // 16-code chunks of a row
       uint32_t q = 0;
       start();
       do {
-        const int32_t ub = c.t0 / kTile;
         for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
-          const int sl = static_cast<int>(q % kScSlots);
-          wait_all(bRf + sl, ph(q, kScSlots), kDevTimeoutEpilogue);
-          const int32_t tok = (ub + k) * kTile + lane * 4;
-          const float4 kr = *reinterpret_cast<const float4*>(smem + C::kOffRaw + (sl * 2 * kTile + lane * 4) * 4);
-          const float4 vr = *reinterpret_cast<const float4*>(smem + C::kOffRaw + ((sl * 2 + 1) * kTile + lane * 4) * 4);
-          float ks[4] = {kr.x, kr.y, kr.z, kr.w}, vs[4] = {vr.x, vr.y, vr.z, vr.w};
-          bool live[4];
-          float top = 0.f, low = 3.0e38f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            live[e] = tok + e >= c.t0 && tok + e < c.t1;
-            if (!live[e]) vs[e] = 0.f;
-            // masked scores are -inf before the key scale: it must not be zero or NaN
-            ks[e] = live[e] ? fmaxf(ks[e], 1.2e-38f) : 1.f;
-            top = fmaxf(top, vs[e]);
-            if (live[e]) low = fminf(low, vs[e]);
+          const int sl = static_cast<int>(q % kScSlots), vs = static_cast<int>(q % kVStages),
+                    fs = static_cast<int>(q % kFStages);
+          wait_all(bSf + sl, ph(q, kScSlots), kDevTimeoutEpilogue);
+          wait_all(bVf + vs, ph(q, kVStages), kDevTimeoutEpilogue);
+          wait_all(bFe + fs, ph(q, kFStages) ^ 1u, kDevTimeoutEpilogue);
+          const uint8_t* src = smem + C::kOffV + vs * C::kK;
+          uint8_t* dst = smem + C::kOffF + fs * C::kV16;
+          const uint2* rv = reinterpret_cast<const uint2*>(smem + C::kOffRv) + sl * kTile;
+          constexpr int RPI = 32 / CH;                  // rows a warp takes at once
+          const int ch = D == 128 ? c8 : lane & 3, sub = D == 128 ? rsub : lane >> 2;
+  #pragma unroll 2
+          for (int i = 0; i < kTile / kConvWarps / RPI; ++i) {
+            const int row = cw * (kTile / kConvWarps) + i * RPI + sub;
+            const uint32_t so = D == 128 ? static_cast<uint32_t>(row * 128 + ((ch ^ (row & 7)) << 4))
+                                         : static_cast<uint32_t>(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
+            const uint4 w = *reinterpret_cast<const uint4*>(src + so);
+            const uint2 r = rv[row];
+            uint32_t o[8];
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+  #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // code * rh + (code * rl): one f16 rounding of the product, and 2^-22 of it
+              e4m3x4_to_f16(ww[e], o[2 * e], o[2 * e + 1]);
+              o[2 * e] = hfma2(o[2 * e], r.x, hmul2(o[2 * e], r.y));
+              o[2 * e + 1] = hfma2(o[2 * e + 1], r.x, hmul2(o[2 * e + 1], r.y));
+            }
+            if (r.x == 0u) {                            // unused places may hold anything
+  #pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = 0u;
+            }
+            // two 16-byte chunks of the row's 64-column half; lanes of the second half store them in
+            // the other order, so that a quarter-warp's stores fall on different banks
+            const int half = ch >> 2, c0 = 2 * (ch & 3);
+            uint8_t* drow = dst + half * C::kHalf + row * 128;
+            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+            const int f0 = half & 1;
+            *reinterpret_cast<uint4*>(drow + (((c0 + f0) ^ (row & 7)) << 4)) = f0 ? hi : lo;
+            *reinterpret_cast<uint4*>(drow + (((c0 + 1 - f0) ^ (row & 7)) << 4)) = f0 ? lo : hi;
           }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+          fence_proxy_async_smem();
+          mbar_arrive(bar(bFf + fs));
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(bVe + vs));
+            mbar_arrive(bar(bSe + sl));
           }
-          // vref = 2^E >= top; values are held as code * (vs / vref) * 2^kVUp, so 2^lv = vref 2^-kVUp
-          uint32_t bits = (__float_as_uint(top) + 0x7FFFFFu) & 0xFF800000u;
-          if (bits < 0x10000000u) bits = 0x10000000u;                    // 2^-95: an all-zero tile
-          const float vinv = __uint_as_float(0x7F000000u - bits);
-          const bool wide = low < top * kWide;
-          const float lv = static_cast<float>(static_cast<int>(bits >> 23) - 127 - kVUp);
-          float4 dl, iv;
-          float rr[4], dd[4], ii[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            rr[e] = !(vs[e] > 0.f) ? 0.f : wide ? static_cast<float>(1 << kVUp) : vs[e] * vinv * static_cast<float>(1 << kVUp);
-            // a scale of zero is a value of zero: its weight counts all the same
-            dd[e] = vs[e] > 0.f ? lg2(vs[e] * vinv) : 0.f;
-            ii[e] = (vs[e] > 0.f ? 1.f / vs[e] : vinv) * static_cast<float>(1 << kVUp);
-          }
-          dl = make_float4(dd[0], dd[1], dd[2], dd[3]);
-          iv = make_float4(ii[0], ii[1], ii[2], ii[3]);
-          *reinterpret_cast<float4*>(smem + C::kOffKs + (sl * kTile + lane * 4) * 4) =
-              wide ? make_float4(1.f, 1.f, 1.f, 1.f) : make_float4(ks[0], ks[1], ks[2], ks[3]);
-          // the value factor as two f16 numbers, each twice: rh + rl holds 22 bits of it
-          uint32_t rh[4], rl[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __half h = __float2half_rn(rr[e]);
-            const __half d = __float2half_rn(rr[e] - __half2float(h));
-            rh[e] = __half_as_ushort(h) * 0x10001u;
-            rl[e] = __half_as_ushort(d) * 0x10001u;
-          }
-          uint4* rv = reinterpret_cast<uint4*>(smem + C::kOffRv + (sl * kTile + lane * 4) * 8);
-          rv[0] = make_uint4(rh[0], rl[0], rh[1], rl[1]);
-          rv[1] = make_uint4(rh[2], rl[2], rh[3], rl[3]);
-          if (wide) {
-            *reinterpret_cast<float4*>(smem + C::kOffDl + (sl * kTile + lane * 4) * 4) = dl;
-            *reinterpret_cast<float4*>(smem + C::kOffIv + (sl * kTile + lane * 4) * 4) = iv;
-          }
-          if (lane == 0)
-            *reinterpret_cast<float4*>(smem + C::kOffInfo + sl * 16) =
-                make_float4(lv, vinv * static_cast<float>(1 << kVUp), wide ? 1.f : 0.f, 0.f);
-          mbar_arrive(bar(bSf + sl));                  // each lane releases its own stores
         }
       } while (next());
     }
-  } else if (warp >= 8) {
-    // ------------------------------------------------------------ converters
-    setmaxnreg_dec<80>();
-    const int cw = warp - 8, c8 = lane & 7, rsub = lane >> 3;
-    constexpr int CH = D / 16;                        // 16-code chunks of a row
-    uint32_t q = 0;
-    start();
-    do {
-      for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
-        const int sl = static_cast<int>(q % kScSlots), vs = static_cast<int>(q % kVStages),
-                  fs = static_cast<int>(q % kFStages);
-        wait_all(bSf + sl, ph(q, kScSlots), kDevTimeoutEpilogue);
-        wait_all(bVf + vs, ph(q, kVStages), kDevTimeoutEpilogue);
-        wait_all(bFe + fs, ph(q, kFStages) ^ 1u, kDevTimeoutEpilogue);
-        const uint8_t* src = smem + C::kOffV + vs * C::kK;
-        uint8_t* dst = smem + C::kOffF + fs * C::kV16;
-        const uint2* rv = reinterpret_cast<const uint2*>(smem + C::kOffRv) + sl * kTile;
-        constexpr int RPI = 32 / CH;                  // rows a warp takes at once
-        const int ch = D == 128 ? c8 : lane & 3, sub = D == 128 ? rsub : lane >> 2;
-#pragma unroll 2
-        for (int i = 0; i < 32 / RPI; ++i) {
-          const int row = cw * 32 + i * RPI + sub;
-          const uint32_t so = D == 128 ? static_cast<uint32_t>(row * 128 + ((ch ^ (row & 7)) << 4))
-                                       : static_cast<uint32_t>(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
-          const uint4 w = *reinterpret_cast<const uint4*>(src + so);
-          const uint2 r = rv[row];
-          uint32_t o[8];
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // code * rh + (code * rl): one f16 rounding of the product, and 2^-22 of it
-            e4m3x4_to_f16(ww[e], o[2 * e], o[2 * e + 1]);
-            o[2 * e] = hfma2(o[2 * e], r.x, hmul2(o[2 * e], r.y));
-            o[2 * e + 1] = hfma2(o[2 * e + 1], r.x, hmul2(o[2 * e + 1], r.y));
-          }
-          if (r.x == 0u) {                            // unused places may hold anything
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = 0u;
-          }
-          // two 16-byte chunks of the row's 64-column half; lanes of the second half store them in
-          // the other order, so that a quarter-warp's stores fall on different banks
-          const int half = ch >> 2, c0 = 2 * (ch & 3);
-          uint8_t* drow = dst + half * C::kHalf + row * 128;
-          const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-          const int f0 = half & 1;
-          *reinterpret_cast<uint4*>(drow + (((c0 + f0) ^ (row & 7)) << 4)) = f0 ? hi : lo;
-          *reinterpret_cast<uint4*>(drow + (((c0 + 1 - f0) ^ (row & 7)) << 4)) = f0 ? lo : hi;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(bFf + fs));
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(bVe + vs));
-          mbar_arrive(bar(bSe + sl));
-        }
-      }
-    } while (next());
   } else {
     // --------------------------------------------------------------- softmax
-    setmaxnreg_inc<192>();
+    setmaxnreg_inc<208>();
     const int t = warp >> 2;                          // query tile of this warpgroup
     const int r = (warp & 3) * 32 + lane;             // row of the tile
     const uint32_t tS = tmem + t * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -841,58 +842,53 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             l += ws;
           }
         }
-        // ---- one pass, 32 columns at a time and the next 32 under way: key scales, the running maximum
+        // ---- one pass, 64 columns at a time (a load takes some 30 cycles): key scales, the running maximum
         // (moved when the chunk passes it by more than kLag), weights.  Few live registers: with a
         // whole row in them the compiler had none left to overlap anything (2000 cycles a row against
         // 700 for this arithmetic alone)
         const uint64_t cc2 = pack_u32x2(__float_as_uint(cc), __float_as_uint(cc));
-        auto weigh = [&](const uint32_t (&sr)[32], int chunk) {
-          uint64_t y[16];
+#pragma unroll 1
+        for (int g = 0; g < kTile / 64; ++g) {
+          uint32_t sr[2][32];
+          tmem_ld32(tS + 64 * g, sr[0]);
+          tmem_ld32(tS + 64 * g + 32, sr[1]);
+          tmem_wait_ld();
+          reg_fence32(sr[0]);
+          reg_fence32(sr[1]);
+          uint64_t y[32];
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const ulonglong2 kv = ks2[8 * chunk + e];
-            y[2 * e] = mul_f32x2(pack_u32x2(sr[4 * e], sr[4 * e + 1]), kv.x);
-            y[2 * e + 1] = mul_f32x2(pack_u32x2(sr[4 * e + 2], sr[4 * e + 3]), kv.y);
+          for (int e = 0; e < 32; e += 2) {
+            const ulonglong2 kv = ks2[16 * g + e / 2];
+            const int c0 = 2 * e % 32;
+            y[e] = mul_f32x2(pack_u32x2(sr[e / 16][c0], sr[e / 16][c0 + 1]), kv.x);
+            y[e + 1] = mul_f32x2(pack_u32x2(sr[e / 16][c0 + 2], sr[e / 16][c0 + 3]), kv.y);
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 32; ++e) {
             float e0, e1;
             unpack_f32x2(y[e], e0, e1);
             mx[e & 3] = max3(mx[e & 3], e0, e1);
           }
           const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), cc, lv);
-          if (__any_sync(0xffffffffu, top > m + kLag)) move_max(top, chunk);
+          if (__any_sync(0xffffffffu, top > m + kLag)) move_max(top, 2 * g);
           const float off = lv - m + kLift;
           const uint64_t off2 = pack_u32x2(__float_as_uint(off), __float_as_uint(off));
-          float w[32];
-          uint32_t pk[16];
+          float w[64];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) unpack_f32x2(fma_f32x2(y[e], cc2, off2), w[2 * e], w[2 * e + 1]);
+          for (int e = 0; e < 32; ++e) unpack_f32x2(fma_f32x2(y[e], cc2, off2), w[2 * e], w[2 * e + 1]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = ex2(w[e]);
+          for (int e = 0; e < 64; ++e) w[e] = ex2(w[e]);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            pk[e] = pack_f16x2(w[2 * e], w[2 * e + 1]);
-            sum[e & 1] = add_f32x2(sum[e & 1], pack_u32x2(__float_as_uint(w[2 * e]), __float_as_uint(w[2 * e + 1])));
-          }
-          tmem_st16(tS + 16 * chunk, pk);
-        };
-        {
-          uint32_t sa[32], sb[32];
-          tmem_ld32(tS, sa);
-          tmem_wait_ld();
-          reg_fence32(sa);
-#pragma unroll 1
-          for (int g = 0; g < 2; ++g) {
-            tmem_ld32(tS + 64 * g + 32, sb);
-            weigh(sa, 2 * g);
-            tmem_wait_ld();
-            reg_fence32(sb);
-            if (g == 0) tmem_ld32(tS + 64, sa);
-            weigh(sb, 2 * g + 1);
-            tmem_wait_ld();
-            reg_fence32(sa);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int j = 32 * h + 2 * e;
+              pk[e] = pack_f16x2(w[j], w[j + 1]);
+              sum[e & 1] = add_f32x2(sum[e & 1], pack_u32x2(__float_as_uint(w[j]), __float_as_uint(w[j + 1])));
+            }
+            tmem_st16(tS + 32 * g + 16 * h, pk);
           }
         }
         if (!wide) {
