@@ -640,34 +640,46 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint2* rv = reinterpret_cast<const uint2*>(smem + C::kOffRv) + sl * kTile;
           constexpr int RPI = 32 / CH;                  // rows a warp takes at once
           const int ch = D == 128 ? c8 : lane & 3, sub = D == 128 ? rsub : lane >> 2;
-  #pragma unroll 2
-          for (int i = 0; i < kTile / kConvWarps / RPI; ++i) {
-            const int row = cw * (kTile / kConvWarps) + i * RPI + sub;
-            const uint32_t so = D == 128 ? static_cast<uint32_t>(row * 128 + ((ch ^ (row & 7)) << 4))
-                                         : static_cast<uint32_t>(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
-            const uint4 w = *reinterpret_cast<const uint4*>(src + so);
-            const uint2 r = rv[row];
-            uint32_t o[8];
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-  #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // code * rh + (code * rl): one f16 rounding of the product, and 2^-22 of it
-              e4m3x4_to_f16(ww[e], o[2 * e], o[2 * e + 1]);
-              o[2 * e] = hfma2(o[2 * e], r.x, hmul2(o[2 * e], r.y));
-              o[2 * e + 1] = hfma2(o[2 * e + 1], r.x, hmul2(o[2 * e + 1], r.y));
+#pragma unroll 1
+          for (int i0 = 0; i0 < kTile / kConvWarps / RPI; i0 += 4) {
+            // four rows' loads, then their arithmetic, then their stores: the compiler cannot tell that
+            // the stores leave the loads alone
+            uint4 w[4];
+            uint2 r[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int row = cw * (kTile / kConvWarps) + (i0 + u) * RPI + sub;
+              w[u] = *reinterpret_cast<const uint4*>(
+                  src + (D == 128 ? row * 128 + ((ch ^ (row & 7)) << 4) : row * 64 + ((ch ^ ((row >> 1) & 3)) << 4)));
+              r[u] = rv[row];
             }
-            if (r.x == 0u) {                            // unused places may hold anything
-  #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = 0u;
+            uint32_t o[4][8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) e4m3x4_to_f16(ww[e], o[u][2 * e], o[u][2 * e + 1]);
             }
+            // code * rh + (code * rl): one f16 rounding of the product, and 2^-22 of it
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                o[u][e] = hfma2(o[u][e], r[u].x, hmul2(o[u][e], r[u].y));
+                if (r[u].x == 0u) o[u][e] = 0u;         // unused places may hold anything
+              }
             // two 16-byte chunks of the row's 64-column half; lanes of the second half store them in
             // the other order, so that a quarter-warp's stores fall on different banks
-            const int half = ch >> 2, c0 = 2 * (ch & 3);
-            uint8_t* drow = dst + half * C::kHalf + row * 128;
-            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-            const int f0 = half & 1;
-            *reinterpret_cast<uint4*>(drow + (((c0 + f0) ^ (row & 7)) << 4)) = f0 ? hi : lo;
-            *reinterpret_cast<uint4*>(drow + (((c0 + 1 - f0) ^ (row & 7)) << 4)) = f0 ? lo : hi;
+            const int half = ch >> 2, c0 = 2 * (ch & 3), f0 = half & 1;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int row = cw * (kTile / kConvWarps) + (i0 + u) * RPI + sub;
+              uint8_t* drow = dst + half * C::kHalf + row * 128;
+              const uint4 lo = make_uint4(o[u][0], o[u][1], o[u][2], o[u][3]),
+                          hi = make_uint4(o[u][4], o[u][5], o[u][6], o[u][7]);
+              *reinterpret_cast<uint4*>(drow + (((c0 + f0) ^ (row & 7)) << 4)) = f0 ? hi : lo;
+              *reinterpret_cast<uint4*>(drow + (((c0 + 1 - f0) ^ (row & 7)) << 4)) = f0 ? lo : hi;
+            }
           }
           fence_proxy_async_smem();
           mbar_arrive(bar(bFf + fs));
