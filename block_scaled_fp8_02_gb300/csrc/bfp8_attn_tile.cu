@@ -230,18 +230,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(bar(bVe + i), kConvWarps);
     }
     for (int i = 0; i < kFStages; ++i) {
-      mbar_init(bar(bFf + i), 32 * kConvWarps);
+      mbar_init(bar(bFf + i), kConvWarps);
       mbar_init(bar(bFe + i), 1);
     }
     for (int i = 0; i < kScSlots; ++i) {
       mbar_init(bar(bRf + i), 1);
-      mbar_init(bar(bSf + i), 32);
+      mbar_init(bar(bSf + i), 1);
       mbar_init(bar(bSe + i), 8 + kConvWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(bQ + i), 128);
+      mbar_init(bar(bQ + i), 4);
       mbar_init(bar(bS + i), 1);
-      mbar_init(bar(bP + i), 128);
+      mbar_init(bar(bP + i), 4);
       mbar_init(bar(bO + i), 1);
     }
     fence_barrier_init();
@@ -464,7 +464,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0)
           *reinterpret_cast<float4*>(smem + C::kOffInfo + sl * 16) =
               make_float4(lv, vinv * static_cast<float>(1 << kVUp), wide ? 1.f : 0.f, 0.f);
-        mbar_arrive(bar(bSf + sl));                  // each lane releases its own stores
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bSf + sl));
       };
       const int page = a.c.page_size, shift = a.c.page_shift;
       const int ppu = page >= kTile ? 1 : kTile / page;
@@ -682,9 +683,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
           fence_proxy_async_smem();
-          mbar_arrive(bar(bFf + fs));
           __syncwarp();
           if (lane == 0) {
+            mbar_arrive(bar(bFf + fs));
             mbar_arrive(bar(bVe + vs));
             mbar_arrive(bar(bSe + sl));
           }
@@ -755,7 +756,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(bar(bQ + t));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bQ + t));
       int32_t lo = 0, hi = 0;
       if (live) seen_range(a, c.w.kv_len, c.w.pos0 + i, lo, hi);
 
@@ -910,9 +912,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(bP + t));
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bSe + sl));
+        if (lane == 0) {
+          mbar_arrive(bar(bP + t));
+          mbar_arrive(bar(bSe + sl));
+        }
       }
 
       // ---- output rows
