@@ -8,6 +8,7 @@ part, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -539,11 +540,30 @@ def linear(x: torch.Tensor, B: torch.Tensor, Bs: torch.Tensor, out: torch.Tensor
 _IN_DTYPE = {torch.bfloat16: BFP8_IN_BF16, torch.float32: BFP8_IN_F32}
 
 
-def _rows(t: torch.Tensor, name: str, M: int, K: int, dtype) -> int:
-    """Row stride of a [M, K] tensor with unit inner stride."""
-    if t.shape != (M, K) or t.dtype != dtype or (K > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a {dtype} tensor of shape ({M}, {K}) with unit inner stride")
-    return t.stride(0) if M > 1 else K
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _stream_of(stream) -> int:
+    """_stream_ptr without building a Stream object for the current one (3 us of a small call's 10)."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(_current_device())
+    return _stream_ptr(stream)
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
+    """Row stride of a tensor of the given 2-D shape with unit inner stride."""
+    st = t.stride()
+    if t.shape != shape or t.dtype != dtype or (st[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} with unit inner stride")
+    return st[0] if shape[0] > 1 else shape[1]
+
+
+def _col_major_scales(M: int, G: int, ld: int, dev) -> torch.Tensor:
+    """[M, G] fp32 with strides (1, ld) over G * ld floats (the whole rows are the GEMM's to copy)."""
+    if M == ld:
+        return torch.empty_strided((M, G), (1, ld), dtype=torch.float32, device=dev)
+    return torch.empty_strided((ld, G), (1, ld), dtype=torch.float32, device=dev)[:M]
 
 
 def bfp8_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None, residual: torch.Tensor | None = None,
@@ -557,17 +577,18 @@ def bfp8_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None, residual: t
     want_y, (q, s, y) with y in bf16; without quantise q and s are None."""
     if x.dim() != 2 or x.dtype not in _IN_DTYPE:
         raise ValueError("x must be a 2-D bfloat16 or float32 tensor")
-    M, K = x.shape
-    ld_x = _rows(x, "x", M, K, x.dtype)
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    M, K = shape
+    ld_x = _rows(x, "x", shape, dtype)
     r_ptr = ro_ptr = w_ptr = y_ptr = q_ptr = s_ptr = None
     ld_r = ld_ro = ld_q = ld_s = K
     if residual is not None:
-        ld_r = _rows(residual, "residual", M, K, x.dtype)
+        ld_r = _rows(residual, "residual", shape, dtype)
         r_ptr = residual.data_ptr()
         if residual_out is None:
             residual_out = residual
     if residual_out is not None:
-        ld_ro = ld_r if residual_out is residual else _rows(residual_out, "residual_out", M, K, x.dtype)
+        ld_ro = ld_r if residual_out is residual else _rows(residual_out, "residual_out", shape, dtype)
         ro_ptr = residual_out.data_ptr()
     w_dtype = BFP8_IN_BF16
     if weight is not None:
@@ -577,22 +598,21 @@ def bfp8_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None, residual: t
     q = s = y = None
     if quantise:
         G = (K + 127) // 128
-        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
-        if col_major:
+        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+        if col_major:                          # [M, G] over a [G, ld_s] buffer, as bfp8_group_quant returns it
             ld_s = (M + 3) // 4 * 4
-            st = torch.empty((G, ld_s), dtype=torch.float32, device=x.device)
-            s = st[:, :M].t()
+            s = _col_major_scales(M, G, ld_s, dev)
         else:
             ld_s = G
-            s = st = torch.empty((M, G), dtype=torch.float32, device=x.device)
-        q_ptr, s_ptr = q.data_ptr(), st.data_ptr()
+            s = torch.empty((M, G), dtype=torch.float32, device=dev)
+        q_ptr, s_ptr = q.data_ptr(), s.data_ptr()
     if want_y:
-        y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+        y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
         y_ptr = y.data_ptr()
-    rc = lib().bfp8_rmsnorm_quant(x.data_ptr(), _IN_DTYPE[x.dtype], ld_x, r_ptr, ld_r, ro_ptr, ld_ro, w_ptr,
-                                  w_dtype, eps, M, K, y_ptr, K, int(col_major),
-                                  SCALE_UE8M0 if ue8m0 else SCALE_FP32, q_ptr, ld_q, s_ptr, ld_s,
-                                  _stream_ptr(stream))
+    rc = (_lib or lib()).bfp8_rmsnorm_quant(x.data_ptr(), _IN_DTYPE[dtype], ld_x, r_ptr, ld_r, ro_ptr, ld_ro, w_ptr,
+                                            w_dtype, eps, M, K, y_ptr, K, int(col_major),
+                                            SCALE_UE8M0 if ue8m0 else SCALE_FP32, q_ptr, ld_q, s_ptr, ld_s,
+                                            _stream_of(stream))
     _check(rc, "bfp8_rmsnorm_quant")
     return (q, s, y) if want_y else (q, s)
 
@@ -656,10 +676,10 @@ def bfp8_kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots:
     if k.stride(2) != 1 or v.stride(2) != 1:
         raise ValueError("k and v must have unit inner stride")
     T = _check_slots(slots, k.shape[0])
-    _check(lib().bfp8_kv_cache_write(k.data_ptr(), v.data_ptr(), _IN_DTYPE[k.dtype], k.stride(0), k.stride(1),
+    _check((_lib or lib()).bfp8_kv_cache_write(k.data_ptr(), v.data_ptr(), _IN_DTYPE[k.dtype], k.stride(0), k.stride(1),
                                      v.stride(0), v.stride(1), slots.data_ptr(), T,
                                      SCALE_UE8M0 if ue8m0 else SCALE_FP32, ctypes.byref(cache._desc),
-                                     _stream_ptr(stream)), "bfp8_kv_cache_write")
+                                     _stream_of(stream)), "bfp8_kv_cache_write")
 
 
 def bfp8_kv_cache_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, stream=None):
@@ -670,8 +690,8 @@ def bfp8_kv_cache_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16
     _, H, _, D = cache.k.shape
     k = torch.empty((T, H, D), dtype=dtype, device=slots.device)
     v = torch.empty((T, H, D), dtype=dtype, device=slots.device)
-    _check(lib().bfp8_kv_cache_read(ctypes.byref(cache._desc), slots.data_ptr(), T, _IN_DTYPE[dtype], k.data_ptr(),
-                                    H * D, v.data_ptr(), H * D, _stream_ptr(stream)), "bfp8_kv_cache_read")
+    _check((_lib or lib()).bfp8_kv_cache_read(ctypes.byref(cache._desc), slots.data_ptr(), T, _IN_DTYPE[dtype], k.data_ptr(),
+                                    H * D, v.data_ptr(), H * D, _stream_of(stream)), "bfp8_kv_cache_read")
     return k, v
 
 
@@ -680,6 +700,11 @@ def bfp8_paged_attention_workspace_size(num_heads: int, num_kv_heads: int, head_
     _check(lib().bfp8_paged_attention_workspace_size(num_heads, num_kv_heads, head_dim, max_q_len, ctypes.byref(n)),
            "bfp8_paged_attention_workspace_size")
     return int(n.value)
+
+
+@functools.lru_cache(maxsize=None)
+def _attention_workspace(device, num_heads: int, num_kv_heads: int, head_dim: int, max_q_len: int) -> int:
+    return bfp8_paged_attention_workspace_size(num_heads, num_kv_heads, head_dim, max_q_len)
 
 
 def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
@@ -691,30 +716,39 @@ def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
     (int32 [batch], the new ones included) on the pages block_table[b] (int32 [batch, max_pages]).  max_q_len and
     max_kv_len bound the lengths; scale defaults to head_dim ** -0.5.  Returns out (bf16, like q), or (out, lse)
     with lse fp32 [total_q, heads]."""
-    P, H, page, D = cache.k.shape
-    if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
+    _, H, _, D = cache.k.shape
+    qs, dev = q.shape, q.device
+    if len(qs) != 3 or qs[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
         raise ValueError(f"q must be bfloat16 [total_q, heads, {D}] with unit inner stride")
-    T, Hq, _ = q.shape
-    B = kv_lens.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != B or (B > 0 and block_table.stride(1) != 1):
-        raise ValueError(f"block_table must be [{B}, max_pages] with unit inner stride")
-    if kv_lens.dim() != 1 or cu_q.shape != (B + 1,) or not kv_lens.is_contiguous() or not cu_q.is_contiguous():
+    T, Hq, _ = qs
+    ts, tst = block_table.shape, block_table.stride()
+    if kv_lens.dim() != 1 or cu_q.shape != (len(kv_lens) + 1,) or not kv_lens.is_contiguous() or not cu_q.is_contiguous():
         raise ValueError("kv_lens must be a contiguous [batch] tensor and cu_q a contiguous [batch + 1] one")
+    B = len(kv_lens)
+    if len(ts) != 2 or ts[0] != B or (B > 0 and tst[1] != 1):
+        raise ValueError(f"block_table must be [{B}, max_pages] with unit inner stride")
     if block_table.dtype != torch.int32 or cu_q.dtype != torch.int32 or kv_lens.dtype != torch.int32:
         raise ValueError("block_table, cu_q and kv_lens must be int32")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.stride(2) != 1:
+        out = torch.empty(qs, dtype=torch.bfloat16, device=dev)
+    elif out.shape != qs or out.dtype != torch.bfloat16 or out.stride(2) != 1:
         raise ValueError("out must be bfloat16, shaped like q, with unit inner stride")
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    sp = _stream_of(stream)
     if workspace is None:
-        workspace = workspace_for(bfp8_paged_attention_workspace_size(Hq, H, D, max_q_len), q.device, stream)
-    a = AttentionArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else None, T, Hq, B, q.stride(0),
-                      q.stride(1), out.stride(0), out.stride(1), block_table.data_ptr(),
-                      block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1], max_q_len,
+        need = _attention_workspace(dev, Hq, H, D, max_q_len)
+        workspace = _ws_cache.get((dev.index, sp))
+        if workspace is None or workspace.numel() < need:
+            workspace = workspace_for(need, dev, stream)
+        ws_bytes = workspace.numel()
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    q_st, out_st = q.stride(), out.stride()
+    a = AttentionArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else None, T, Hq, B, q_st[0], q_st[1],
+                      out_st[0], out_st[1], block_table.data_ptr(), tst[0] if B > 1 else ts[1], ts[1], max_q_len,
                       max_kv_len, cu_q.data_ptr(), kv_lens.data_ptr(), D ** -0.5 if scale is None else scale,
-                      int(causal), window, 0)
-    _check(lib().bfp8_paged_attention(ctypes.byref(a), ctypes.byref(cache._desc), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
+                      causal, window, 0)
+    _check((_lib or lib()).bfp8_paged_attention(ctypes.byref(a), ctypes.byref(cache._desc), workspace.data_ptr(), ws_bytes,
+                                                sp),
            "bfp8_paged_attention")
     return (out, lse) if return_lse else out
