@@ -4,10 +4,12 @@
 //   write: s = max(amax_d |x|, 1e-10) / 448, code = e4m3(x / s) per (token, head)
 //   read:  x' = code * s, one rounding
 //
-// Both are streams of rows of head_dim elements, (token, k or v, head) in that
-// order so that neighbouring lanes read neighbouring heads of a token.  Bound
-// by memory: write 2 bytes in and 1 + 4 / head_dim out an element (bf16), read
-// the other way round.
+// A thread holds 16 elements of one (key or value, head) place and keeps that
+// place from token to token, so that a token costs it a slot and two address
+// sums; places that do not fill a block of 256 threads share it with the next
+// tokens, those beyond it are the grid's second dimension.  Four tokens' loads
+// are in flight together.  Bound by memory: write 2 bytes in and 1 + 4 /
+// head_dim out an element (bf16), read the other way round.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,63 +25,73 @@ namespace bfp8 {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kRowsInFlight = 4;      // warp steps whose loads are issued together
+constexpr int kThreads = 256;
+constexpr int kTokens = 4;            // tokens of a thread whose loads are issued together
+
+// The places of a token: nkv x heads x (dim / 16), shared out as above.
+struct Places {
+  int32_t count;                      // of a token
+  int32_t tokens;                     // that a block holds at once
+};
 
 struct WriteArgs {
   const void* k;
   const void* v;
   int64_t k_st, k_sh, v_st, v_sh;     // element strides
   const int64_t* slots;
-  uint32_t rows;                      // T * 2 * H
+  int64_t T;
   int32_t vec;
+  Places pl;
   CacheView c;
   int* err;
 };
 
 template <bool kF32, bool kUe8m0, int D>
-__global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constant__ WriteArgs a) {
   using T = typename std::conditional<kF32, float, uint16_t>::type;
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, sub = lane / LPR, li = lane % LPR;
-  const uint32_t warp0 = blockIdx.x * kWarps + (threadIdx.x >> 5), nw = gridDim.x * kWarps;
-  const uint32_t H = a.c.heads;
+  constexpr int LPR = D / 16;                         // threads of a row
+  const int ti = static_cast<int>(threadIdx.x) / a.pl.count;                   // token of the block
+  const int place = static_cast<int>(blockIdx.y) * kThreads + static_cast<int>(threadIdx.x) - ti * a.pl.count;
+  const bool mine = ti < a.pl.tokens && place < a.pl.count;
+  const int li = place % LPR, row = mine ? place / LPR : 0;
+  const bool is_v = row >= a.c.heads;
+  const int head = is_v ? row - a.c.heads : row;
+  const T* src = (is_v ? static_cast<const T*>(a.v) + head * a.v_sh : static_cast<const T*>(a.k) + head * a.k_sh) + li * 16;
+  const int64_t st = is_v ? a.v_st : a.k_st;
+  uint8_t* q = (is_v ? a.c.v : a.c.k) + head * a.c.st_head + li * 16;
+  float* s = (is_v ? a.c.vs : a.c.ks) + head * a.c.ss_head;
   const int64_t nslots = a.c.num_pages * a.c.page_size;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * a.pl.tokens;
   griddep_launch_dependents();
   griddep_wait();
-  for (uint32_t w = warp0; static_cast<uint64_t>(w) * RPW < a.rows; w += nw * kRowsInFlight) {
-    float x[kRowsInFlight][8];
-    int64_t slot[kRowsInFlight];
-    uint32_t head[kRowsInFlight];
-    bool is_v[kRowsInFlight];
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.pl.tokens; t0 < a.T; t0 += step * kTokens) {
+    Raw8<kF32> x[kTokens][2];
+    int64_t slot[kTokens];
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      const uint64_t row = (static_cast<uint64_t>(w) + static_cast<uint64_t>(u) * nw) * RPW + sub;
-      slot[u] = -1;
-      const bool ok = row < a.rows;
-      const uint32_t r = ok ? static_cast<uint32_t>(row) : 0u;
-      const uint32_t pair = r / H, t = pair >> 1;
-      head[u] = r - pair * H;
-      is_v[u] = pair & 1;
-      if (ok) slot[u] = __ldg(a.slots + t);
-      const T* src = is_v[u] ? static_cast<const T*>(a.v) + t * a.v_st + head[u] * a.v_sh
-                             : static_cast<const T*>(a.k) + t * a.k_st + head[u] * a.k_sh;
-      load8<kF32>(src + li * 8, a.vec, ok ? 8 : 0, x[u]);
+    for (int u = 0; u < kTokens; ++u) {
+      const int64_t t = t0 + u * step + ti;
+      const bool ok = mine && t < a.T;
+      slot[u] = ok ? __ldg(a.slots + t) : -1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) x[u][i].load(src + (ok ? t : 0) * st + 8 * i, a.vec, ok ? 8 : 0);
     }
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
+    for (int u = 0; u < kTokens; ++u) {
+      if (t0 + u * step >= a.T) break;                // whole blocks
+      float v[16];
+      x[u][0].get(reinterpret_cast<float(&)[8]>(v[0]));
+      x[u][1].get(reinterpret_cast<float(&)[8]>(v[8]));
       float scale;
-      uint32_t lo, hi;
-      quant8<LPR, kUe8m0>(x[u], scale, lo, hi);
+      uint32_t w[4];
+      quant16<LPR, kUe8m0>(v, scale, w);
       if (slot[u] < 0) continue;
       if (slot[u] >= nslots) {
         report_failure(a.err, kDevBadCacheIndex);
         continue;
       }
       const int64_t page = slot[u] >> a.c.page_shift, o = slot[u] & (a.c.page_size - 1);
-      uint8_t* q = (is_v[u] ? a.c.v : a.c.k) + page * a.c.st_page + head[u] * a.c.st_head + o * a.c.st_tok;
-      *reinterpret_cast<uint2*>(q + li * 8) = make_uint2(lo, hi);
-      if (li == 0) (is_v[u] ? a.c.vs : a.c.ks)[page * a.c.ss_page + head[u] * a.c.ss_head + o] = scale;
+      *reinterpret_cast<uint4*>(q + page * a.c.st_page + o * a.c.st_tok) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (li == 0) s[page * a.c.ss_page + o] = scale;
     }
   }
 }
@@ -89,74 +101,87 @@ struct ReadArgs {
   void* v;                            // or nullptr
   int64_t k_st, v_st;                 // element strides of tokens
   const int64_t* slots;
-  uint32_t rows;                      // T * nkv * H
-  uint32_t nkv;                       // 1: only one of k and v
+  int64_t T;
   int32_t vec;
+  Places pl;
   CacheView c;
   int* err;
 };
 
 template <bool kF32, int D>
-__global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_constant__ ReadArgs a) {
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ ReadArgs a) {
   using T = typename std::conditional<kF32, float, __nv_bfloat16>::type;
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, sub = lane / LPR, li = lane % LPR;
-  const uint32_t warp0 = blockIdx.x * kWarps + (threadIdx.x >> 5), nw = gridDim.x * kWarps;
-  const uint32_t H = a.c.heads;
-  const int64_t nslots = a.c.num_pages * a.c.page_size;
+  constexpr int LPR = D / 16;
+  const int ti = static_cast<int>(threadIdx.x) / a.pl.count;
+  const int place = static_cast<int>(blockIdx.y) * kThreads + static_cast<int>(threadIdx.x) - ti * a.pl.count;
   griddep_launch_dependents();
   griddep_wait();
-  for (uint32_t w = warp0; static_cast<uint64_t>(w) * RPW < a.rows; w += nw * kRowsInFlight) {
-    uint2 q[kRowsInFlight];
-    float s[kRowsInFlight];
-    T* dst[kRowsInFlight];
+  if (ti >= a.pl.tokens || place >= a.pl.count) return;
+  const int li = place % LPR, row = place / LPR;
+  const bool is_v = row >= a.c.heads || a.k == nullptr;
+  const int head = row >= a.c.heads ? row - a.c.heads : row;
+  const uint8_t* q = (is_v ? a.c.v : a.c.k) + head * a.c.st_head + li * 16;
+  const float* s = (is_v ? a.c.vs : a.c.ks) + head * a.c.ss_head;
+  T* dst = static_cast<T*>(is_v ? a.v : a.k) + head * D + li * 16;
+  const int64_t st = is_v ? a.v_st : a.k_st;
+  const int64_t nslots = a.c.num_pages * a.c.page_size;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * a.pl.tokens;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.pl.tokens + ti; t0 < a.T; t0 += step * kTokens) {
+    uint4 w[kTokens];
+    float sc[kTokens];
+    int64_t slot[kTokens];
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      const uint64_t row = (static_cast<uint64_t>(w) + static_cast<uint64_t>(u) * nw) * RPW + sub;
-      dst[u] = nullptr;
-      q[u] = make_uint2(0u, 0u);
-      s[u] = 0.f;
-      if (row >= a.rows) continue;
-      const uint32_t r = static_cast<uint32_t>(row), pair = r / H, h = r - pair * H;
-      const uint32_t t = a.nkv == 2 ? pair >> 1 : pair;
-      const bool is_v = a.nkv == 2 ? (pair & 1) : a.k == nullptr;
-      dst[u] = static_cast<T*>(is_v ? a.v : a.k) + t * (is_v ? a.v_st : a.k_st) + h * D + li * 8;
-      const int64_t slot = __ldg(a.slots + t);
-      if (slot >= nslots) {
+    for (int u = 0; u < kTokens; ++u) slot[u] = t0 + u * step < a.T ? __ldg(a.slots + t0 + u * step) : -1;
+#pragma unroll
+    for (int u = 0; u < kTokens; ++u) {
+      w[u] = make_uint4(0u, 0u, 0u, 0u);
+      sc[u] = 0.f;
+      if (slot[u] >= nslots) {
         report_failure(a.err, kDevBadCacheIndex);
-      } else if (slot >= 0) {
-        const int64_t page = slot >> a.c.page_shift, o = slot & (a.c.page_size - 1);
-        q[u] = __ldg(reinterpret_cast<const uint2*>((is_v ? a.c.v : a.c.k) + page * a.c.st_page +
-                                                    h * a.c.st_head + o * a.c.st_tok + li * 8));
-        s[u] = __ldg((is_v ? a.c.vs : a.c.ks) + page * a.c.ss_page + h * a.c.ss_head + o);
+      } else if (slot[u] >= 0) {
+        const int64_t page = slot[u] >> a.c.page_shift, o = slot[u] & (a.c.page_size - 1);
+        w[u] = __ldg(reinterpret_cast<const uint4*>(q + page * a.c.st_page + o * a.c.st_tok));
+        sc[u] = __ldg(s + page * a.c.ss_page + o);
       }
     }
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      if (dst[u] == nullptr) continue;
-      float v[8], lo[4], hi[4];
-      e4m3x4_to_f32(q[u].x, lo);
-      e4m3x4_to_f32(q[u].y, hi);
+    for (int u = 0; u < kTokens; ++u) {
+      if (t0 + u * step >= a.T) break;
+      const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      T* d = dst + (t0 + u * step) * st;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = __fmul_rn(lo[e], s[u]);
-        v[4 + e] = __fmul_rn(hi[e], s[u]);
+      for (int h = 0; h < 2; ++h) {
+        float v[8], lo[4], hi[4];
+        e4m3x4_to_f32(ww[2 * h], lo);
+        e4m3x4_to_f32(ww[2 * h + 1], hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = __fmul_rn(lo[e], sc[u]);
+          v[4 + e] = __fmul_rn(hi[e], sc[u]);
+        }
+        store8<kF32>(d + 8 * h, a.vec, 8, v);
       }
-      store8<kF32>(dst[u], a.vec, 8, v);
     }
   }
 }
 
+Places places_of(int nkv, const CacheView& c) {
+  Places p;
+  p.count = nkv * c.heads * (c.dim / 16);
+  p.tokens = p.count < kThreads ? kThreads / p.count : 1;
+  return p;
+}
+
 template <typename F, typename A>
-cudaError_t launch_rows(F* f, const A& a, uint64_t rows, int rpw, int num_sms, cudaStream_t stream) {
-  // 8 blocks of 8 warps a SM; each warp walks kRowsInFlight steps at a time
-  const uint64_t steps = (rows + rpw - 1) / rpw;
-  uint64_t blocks = (steps + kWarps - 1) / kWarps;
-  const uint64_t cap = static_cast<uint64_t>(num_sms) * 8;
-  if (blocks > cap) blocks = cap;
+cudaError_t launch_places(F* f, const A& a, int num_sms, cudaStream_t stream) {
+  const int64_t gy = (a.pl.count + kThreads - 1) / kThreads;
+  // 8 blocks a SM walk the tokens
+  int64_t gx = (a.T + a.pl.tokens - 1) / a.pl.tokens;
+  const int64_t cap = (static_cast<int64_t>(num_sms) * 8 + gy - 1) / gy;
+  if (gx > cap) gx = cap;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -173,7 +198,7 @@ bfp8_status bad(const char* fmt, V... v) {
   return set_last_errorf(BFP8_ERR_INVALID_ARG, fmt, v...);
 }
 
-// Rows of one launch: the kernels index them in 32 bits with room for a step.
+// Tokens x heads of one launch.
 constexpr int64_t kMaxRows = int64_t{1} << 31;
 
 }  // namespace
@@ -255,13 +280,14 @@ extern "C" bfp8_status bfp8_kv_cache_write(const void* k, const void* v, int in_
   a.v_st = v_stride_token;
   a.v_sh = v_stride_head;
   a.slots = slots;
-  a.rows = static_cast<uint32_t>(T * 2 * a.c.heads);
+  a.T = T;
+  a.pl = places_of(2, a.c);
   a.vec = !off_align(k, 16) && !off_align(v, 16) && k_stride_token * es % 16 == 0 &&
           k_stride_head * es % 16 == 0 && v_stride_token * es % 16 == 0 && v_stride_head * es % 16 == 0;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool f32 = in_dtype == BFP8_IN_F32, ue = scale_fmt == BFP8_SCALE_UE8M0;
   auto go = [&](auto f128, auto f64) {
-    return a.c.dim == 128 ? launch_rows(f128, a, a.rows, 2, sms, cs) : launch_rows(f64, a, a.rows, 4, sms, cs);
+    return a.c.dim == 128 ? launch_places(f128, a, sms, cs) : launch_places(f64, a, sms, cs);
   };
   const cudaError_t e =
       f32 ? (ue ? go(kv_write_kernel<true, true, 128>, kv_write_kernel<true, true, 64>)
@@ -299,13 +325,13 @@ extern "C" bfp8_status bfp8_kv_cache_read(const bfp8_kv_cache* cache, const int6
   a.k_st = k_stride_token;
   a.v_st = v_stride_token;
   a.slots = slots;
-  a.nkv = k_out && v_out ? 2 : 1;
-  a.rows = static_cast<uint32_t>(T * a.nkv * a.c.heads);
+  a.T = T;
+  a.pl = places_of(k_out && v_out ? 2 : 1, a.c);
   a.vec = !off_align(k_out, 16) && !off_align(v_out, 16) && (!k_out || k_stride_token * es % 16 == 0) &&
           (!v_out || v_stride_token * es % 16 == 0);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   auto go = [&](auto f128, auto f64) {
-    return a.c.dim == 128 ? launch_rows(f128, a, a.rows, 2, sms, cs) : launch_rows(f64, a, a.rows, 4, sms, cs);
+    return a.c.dim == 128 ? launch_places(f128, a, sms, cs) : launch_places(f64, a, sms, cs);
   };
   const cudaError_t e = out_dtype == BFP8_IN_F32 ? go(kv_read_kernel<true, 128>, kv_read_kernel<true, 64>)
                                                  : go(kv_read_kernel<false, 128>, kv_read_kernel<false, 64>);

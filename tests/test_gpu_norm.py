@@ -51,9 +51,11 @@ def _check(x, r, w, eps, q, s, ro, y_out, ue8m0):
     codes = torch.nn.functional.pad(q.cpu().float().double(), (0, G * 128 - K)).view(M, G, 128)
     ratio = yp / s[..., None]
     assert ((codes - ratio).abs() <= (2.0 ** -4 + 4 * e) * ratio.abs().clamp(min=2.0 ** -6)).all()
-    # and all but the near-ties are the codes of the exact quotient
-    exact = ratio.float().clamp(-448, 448).to(torch.float8_e4m3fn).float().double()
-    assert (codes != exact).double().mean() < 1e-3 + 64 * e
+    # and it is the code of some quotient within the arithmetic's error of the exact one
+    def encode(t):
+        return t.float().clamp(-448, 448).to(torch.float8_e4m3fn).float().double()
+    d = 4 * e + 2.0 ** -23
+    assert ((codes == encode(ratio * (1 - d))) | (codes == encode(ratio * (1 + d)))).all()
 
 
 CASES = [(1, 5120), (1, 1), (3, 127), (5, 128), (2, 129), (83, 7168), (1000, 1000), (7, 8192), (400, 264), (33, 12288),
@@ -97,7 +99,7 @@ def test_norm_in_place_equals_out_of_place(dev, M, K):
 def test_norm_strided_rows_and_plain_forms(dev, K):
     """Rows of a wider buffer at an odd column (the element-wise path), no residual, no weight, no quantisation."""
     M = 37
-    wide = torch.randn(M, K + 77, device=dev).bfloat16()
+    wide = torch.randn(M, K + 77, generator=torch.Generator().manual_seed(K)).bfloat16().to(dev)
     for first in (0, 8, 5):
         x = wide[:, first:first + K]
         q, s, y = bf.bfp8_rmsnorm_quant(x, None, eps=1e-5, want_y=True)
