@@ -62,6 +62,20 @@ __device__ __forceinline__ void seen_range(const AttnArgs& a, int32_t kv_len, in
   if (hi > kv_len) hi = kv_len;
 }
 
+// A line of `total` units shared equally by `ctas` CTAs: where share c begins,
+// and whose share unit u is in.  32-bit division (a tenth of the time) where the
+// products fit.
+__device__ __forceinline__ int64_t share_begin(int64_t c, int64_t total, int64_t ctas) {
+  if (total < (1 << 22) && ctas < (1 << 10))
+    return static_cast<uint32_t>(c) * static_cast<uint32_t>(total) / static_cast<uint32_t>(ctas);
+  return c * total / ctas;
+}
+__device__ __forceinline__ int share_of(int64_t u, int64_t total, int64_t ctas) {
+  if (total < (1 << 22) && ctas < (1 << 10))
+    return static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(ctas) - 1u) / static_cast<uint32_t>(total));
+  return static_cast<int>(((u + 1) * ctas - 1) / total);
+}
+
 // The kernel for few rows a sequence (bfp8_attn_decode.cu): `groups` (1, 2 or 4)
 // eights of rows, `ctas` persistent CTAs, counters[ctas] zero.
 // k, v: tensor maps [dim, token, head, page] of bytes, boxes of min(page_size, 128) tokens.

@@ -4,7 +4,8 @@
 //
 // Work is (sequence, kv head) items of 128-token units, all items' units in one
 // line; the persistent CTAs (one a SM) take equal shares of that line, so that
-// ragged contexts and single long ones load every SM alike.  A CTA computes its
+// ragged contexts and single long ones load every SM alike.  Ending an item costs
+// a CTA the time of kItemCost units, which lie behind its units in the line.  A CTA computes its
 // share from the lengths on the device.  An item cut by a share's border leaves
 // fp32 partial outputs in the workspace; the last CTA of it to arrive adds them
 // in CTA order (deterministic).
@@ -37,6 +38,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "bfp8_attn.cuh"
 #include "bfp8_attn_math.cuh"
@@ -53,6 +55,7 @@ constexpr int kUnit = 128;                 // tokens of a unit
 // two warpgroups of consumers and one whose first warp produces: registers are
 // handed from the third (56 a thread) to the first two (224) of 168 at launch
 constexpr int kDecThreads = (kDecWarps + 4) * 32;
+constexpr int kItemCost = 4;               // (measured: query, joining the warps, output 5000 cycles; a unit 1340)
 constexpr int kSeqCache = 64;              // sequences whose lengths a CTA keeps in shared memory
 constexpr float kNoMax = -3.0e38f;         // running maximum before any token
 constexpr float kLag = 8.f;                // how far scores may exceed the running maximum
@@ -64,6 +67,8 @@ struct DecCfg {
   static constexpr int kStageBytes = 2 * kCodes;
   static constexpr int kScaleFloats = 2 * kUnit;
   static constexpr int kStages = D == 128 ? 5 : 8;
+  // units a warp takes at once: two where the registers allow it
+  static constexpr int kAtOnce = NG <= 2 ? 2 : 1;
   static constexpr int kPitch = D + 4;                     // floats of a row of partials
   static constexpr int kOffScale = kStages * kStageBytes;
   static constexpr int kOffRed = kOffScale + kStages * kScaleFloats * 4;
@@ -101,6 +106,9 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, int b, int max_ro
     w.units = hi > lo ? (hi + kUnit - 1) / kUnit - lo / kUnit : 1;
   return w;
 }
+
+// Length of an item in the line.
+__device__ __forceinline__ int32_t line_cost(int32_t units) { return units > 0 ? units + kItemCost : 0; }
 
 // Inclusive sum over the block's threads (all call it).
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part) {
@@ -191,12 +199,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   __shared__ int64_t part[kDecThreads / 32];
   __shared__ int64_t s_before;
   __shared__ int s_b;
-  int64_t run = 0;
+  int64_t run = 0, incl0 = 0;
+  SeqWork mine{};                                      // sequence tid of the last chunk of them
   for (int b0 = 0; b0 < a.batch; b0 += kDecThreads) {
     const int b = b0 + tid;
-    const int64_t n = b < a.batch ? seq_work(a, b, kRows).units : 0;
-    const int64_t incl = block_scan(n, part);
-    if (tid == kDecThreads - 1) part[0] = incl;
+    mine.units = 0;
+    if (b < a.batch) mine = seq_work(a, b, kRows);
+    incl0 = block_scan(line_cost(mine.units), part);
+    if (tid == kDecThreads - 1) part[0] = incl0;
     __syncthreads();
     run += part[0];
     __syncthreads();
@@ -204,24 +214,33 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   const int64_t total = run * H;
   const int64_t ctas = total < gridDim.x ? total : gridDim.x;
   if (blockIdx.x >= ctas) return;                      // whole CTA: nothing is in flight yet
-  const int64_t u0 = blockIdx.x * total / ctas, u1 = (blockIdx.x + 1) * total / ctas;
-  run = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kDecThreads) {
-    const int b = b0 + tid;
-    const int64_t n = b < a.batch ? seq_work(a, b, kRows).units : 0;
-    const int64_t incl = run + block_scan(n, part);
+  const int64_t u0 = share_begin(blockIdx.x, total, ctas), u1 = share_begin(blockIdx.x + 1, total, ctas);
+  auto locate = [&](int b, int64_t incl, int32_t n) {
     if (n > 0 && (incl - n) * H <= u0 && u0 < incl * H) {
       s_b = b;
       s_before = (incl - n) * H;
     }
-    if (tid == kDecThreads - 1) part[0] = incl;
+  };
+  if (a.batch <= kDecThreads) {                        // the lengths are in registers
+    locate(tid, incl0, line_cost(mine.units));
     __syncthreads();
-    run = part[0];
-    __syncthreads();
+    if (tid >= s_b && tid < a.batch && tid - s_b < kSeqCache) seqs[tid - s_b] = mine;
+  } else {
+    run = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kDecThreads) {
+      const int b = b0 + tid;
+      const int32_t n = b < a.batch ? line_cost(seq_work(a, b, kRows).units) : 0;
+      const int64_t incl = run + block_scan(n, part);
+      locate(b, incl, n);
+      if (tid == kDecThreads - 1) part[0] = incl;
+      __syncthreads();
+      run = part[0];
+      __syncthreads();
+    }
+    if (tid < kSeqCache && s_b + tid < a.batch) seqs[tid] = seq_work(a, s_b + tid, kRows);
   }
-  const int b_first = s_b;
-  if (tid < kSeqCache && b_first + tid < a.batch) seqs[tid] = seq_work(a, b_first + tid, kRows);
   __syncthreads();
+  const int b_first = s_b;
   auto get_seq = [&](int b) -> SeqWork {
     return b - b_first < kSeqCache ? seqs[b - b_first] : seq_work(a, b, kRows);
   };
@@ -232,27 +251,30 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     int32_t k0, k1;
     SeqWork w;
   };
-  auto start = [&](Cursor& c) {
-    c.b = b_first;
-    c.w = get_seq(c.b);
-    const int64_t in_b = u0 - s_before;
-    c.h = static_cast<int>(in_b / c.w.units);
-    c.item0 = s_before + static_cast<int64_t>(c.h) * c.w.units;
-    c.k0 = static_cast<int32_t>(u0 - c.item0);
+  auto clip = [&](Cursor& c) {                  // false: only the item's end lies in the share
+    c.k0 = static_cast<int32_t>(u0 > c.item0 ? u0 - c.item0 : 0);
     c.k1 = static_cast<int32_t>(c.item0 + c.w.units < u1 ? c.w.units : u1 - c.item0);
+    return c.k0 < c.k1;
   };
   auto next = [&](Cursor& c) -> bool {          // false: the share is done
-    c.item0 += c.w.units;
-    if (c.item0 >= u1) return false;
-    if (++c.h == H) {
-      c.h = 0;
-      do {
-        c.w = get_seq(++c.b);
-      } while (c.w.units == 0);
-    }
-    c.k0 = 0;
-    c.k1 = static_cast<int32_t>(c.item0 + c.w.units < u1 ? c.w.units : u1 - c.item0);
+    do {
+      c.item0 += line_cost(c.w.units);
+      if (c.item0 >= u1) return false;
+      if (++c.h == H) {
+        c.h = 0;
+        do {
+          c.w = get_seq(++c.b);
+        } while (c.w.units == 0);
+      }
+    } while (!clip(c));
     return true;
+  };
+  auto start = [&](Cursor& c) -> bool {
+    c.b = b_first;
+    c.w = get_seq(c.b);
+    c.h = static_cast<int>((u0 - s_before) / line_cost(c.w.units));
+    c.item0 = s_before + static_cast<int64_t>(c.h) * line_cost(c.w.units);
+    return clip(c) || next(c);
   };
 
   if (warp >= kDecWarps) {
@@ -266,8 +288,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     int64_t q = 0;
     bool ok = true;
     Cursor c;
-    start(c);
-    do {
+    for (bool more = start(c); more && ok; more = next(c)) {
       const int32_t ub = c.w.t0 / kUnit;
       const int32_t* row = a.table + c.b * a.ld_table;
       // table entries of 32 boxes at a time, one a lane
@@ -314,7 +335,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           bulk_load(sd + kUnit * 4, a.c.vs + so, box * 4, bar_full(slot));
         }
       }
-    } while (ok && next(c));
+    }
     // no copy may still be landing in shared memory when the CTA exits
     for (int64_t i = q > C::kStages ? q - C::kStages : 0; i < q; ++i)
       if (!mbar_wait_bounded(bar_full(static_cast<int>(i % C::kStages)), static_cast<uint32_t>((i / C::kStages) & 1),
@@ -341,38 +362,44 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   __shared__ int s_last;
   bool ok = true;
   int64_t q = 0;
+  // the rows grp * 8 + g of an item's queries, this lane's elements; fetched while the item before ends
+  uint4 raw[NG][KC][2];
+  auto fetch = [&](const Cursor& c) {
+#pragma unroll
+    for (int grp = 0; grp < NG; ++grp) {
+      const int r = grp * 8 + g, i = r / a.group;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (c.w.row0 + i) * a.q_st +
+                                                        (c.h * a.group + r - i * a.group) * a.q_sh + 16 * t);
+#pragma unroll
+      for (int h = 0; h < KC; ++h) {
+        raw[grp][h][0] = raw[grp][h][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < c.w.q_len * a.group) {
+          raw[grp][h][0] = __ldg(src + 8 * h);
+          raw[grp][h][1] = __ldg(src + 8 * h + 1);
+        }
+      }
+    }
+  };
+  constexpr bool kAhead = NG <= 2;           // (no registers left for it otherwise)
   Cursor c;
-  start(c);
-  bool more = true;
+  bool more = start(c);
+  if (more && kAhead) fetch(c);
   while (more) {
     const SeqWork w = c.w;
     const int rows = w.q_len * a.group;
+    if (!kAhead) fetch(c);
     // ---- queries: rows grp * 8 + g, f16 after scaling by a power of two
     uint32_t qf[NG][KC * 4][2];
     float cq[NG][2];
 #pragma unroll
     for (int grp = 0; grp < NG; ++grp) {
-      const int r = grp * 8 + g;
-      uint4 raw[KC][2];
       float amax = 0.f;
-#pragma unroll
-      for (int h = 0; h < KC; ++h) {
-        raw[h][0] = raw[h][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) {
-          const int i = r / a.group;
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + (w.row0 + i) * a.q_st +
-                                                            (c.h * a.group + r - i * a.group) * a.q_sh +
-                                                            16 * (t + 4 * h));
-          raw[h][0] = __ldg(src);
-          raw[h][1] = __ldg(src + 1);
-        }
-      }
       float f[KC][16];
 #pragma unroll
       for (int h = 0; h < KC; ++h)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint4& u = raw[h][i >> 2];
+          const uint4& u = raw[grp][h][i >> 2];
           const uint32_t x = (i & 3) == 0 ? u.x : (i & 3) == 1 ? u.y : (i & 3) == 2 ? u.z : u.w;
           f[h][2 * i] = __uint_as_float(x << 16);
           f[h][2 * i + 1] = __uint_as_float(x & 0xFFFF0000u);
@@ -414,47 +441,76 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       for (int j = 0; j < DT; ++j) acc[grp][j][0] = acc[grp][j][1] = acc[grp][j][2] = acc[grp][j][3] = 0.f;
     }
     const int32_t ub = w.t0 / kUnit;
-    for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
-      const int slot = static_cast<int>(q % C::kStages);
-      if (ok) {
-        const bool in = mbar_wait_bounded(bar_full(slot), static_cast<uint32_t>((q / C::kStages) & 1), p.wait_limit);
-        ok = __all_sync(0xffffffffu, in);
-        if (!ok && lane == 0) report_failure(a.err, kDevTimeoutEpilogue);
-      }
-      const int32_t base = (ub + k) * kUnit + warp * 16;
-      if (ok && base < w.t1 && base + 16 > w.t0) {
-        const uint8_t* kst = smem + slot * C::kStageBytes + warp * 16 * D;
-        const uint8_t* vst = kst + C::kCodes;
-        const float* sc = reinterpret_cast<const float*>(smem + C::kOffScale) + slot * C::kScaleFloats + warp * 16;
-        const bool edge = base < full_lo || base + 16 > full_hi;
-        float ks[2] = {sc[pg], sc[pg + 8]}, lv[2] = {lg2(sc[kUnit + pg]), lg2(sc[kUnit + pg + 8])};
-        // ---- scores
-        float s[NG][4];
+    // 16 tokens of this warp in each of NU units (stages q ..), whose chains of dependent steps overlap
+    auto process = [&](auto nu, int32_t k) {
+      constexpr int NU = decltype(nu)::value;
+      int32_t base[NU];
+      const uint8_t *kst[NU], *vst[NU];
+      float ks[NU][2], lv[NU][2];
+      bool edge = false;
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp) s[grp][0] = s[grp][1] = s[grp][2] = s[grp][3] = 0.f;
+      for (int u = 0; u < NU; ++u) {
+        const int slot = static_cast<int>((q + u) % C::kStages);
+        base[u] = (ub + k + u) * kUnit + warp * 16;
+        kst[u] = smem + slot * C::kStageBytes + warp * 16 * D;
+        vst[u] = kst[u] + C::kCodes;
+        const float* sc = reinterpret_cast<const float*>(smem + C::kOffScale) + slot * C::kScaleFloats + warp * 16;
+        edge |= base[u] < full_lo || base[u] + 16 > full_hi;
+        ks[u][0] = sc[pg];
+        ks[u][1] = sc[pg + 8];
+        lv[u][0] = lg2(sc[kUnit + pg]);
+        lv[u][1] = lg2(sc[kUnit + pg + 8]);
+      }
+      // ---- scores
+      float s[NU][NG][4];
+      {
+        float part[NU][NG][KC][4];
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+            for (int h = 0; h < KC; ++h)
+              part[u][grp][h][0] = part[u][grp][h][1] = part[u][grp][h][2] = part[u][grp][h][3] = 0.f;
 #pragma unroll
         for (int h = 0; h < KC; ++h) {
-          const uint4 ka = *reinterpret_cast<const uint4*>(kst + chunk_off<D>(pg, t + 4 * h));
-          const uint4 kb = *reinterpret_cast<const uint4*>(kst + chunk_off<D>(pg + 8, t + 4 * h));
-          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+          uint4 ka[NU], kb[NU];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t a0, a1, a2, a3;
-            e4m3x4_to_f16(wa[i], a0, a2);
-            e4m3x4_to_f16(wb[i], a1, a3);
-#pragma unroll
-            for (int grp = 0; grp < NG; ++grp)
-              mma_f16_16x8x16(s[grp], a0, a1, a2, a3, qf[grp][h * 4 + i][0], qf[grp][h * 4 + i][1]);
+          for (int u = 0; u < NU; ++u) {
+            ka[u] = *reinterpret_cast<const uint4*>(kst[u] + chunk_off<D>(pg, t + 4 * h));
+            kb[u] = *reinterpret_cast<const uint4*>(kst[u] + chunk_off<D>(pg + 8, t + 4 * h));
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+              const uint32_t wa = i == 0 ? ka[u].x : i == 1 ? ka[u].y : i == 2 ? ka[u].z : ka[u].w;
+              const uint32_t wb = i == 0 ? kb[u].x : i == 1 ? kb[u].y : i == 2 ? kb[u].z : kb[u].w;
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(wa, a0, a2);
+              e4m3x4_to_f16(wb, a1, a3);
+#pragma unroll
+              for (int grp = 0; grp < NG; ++grp)
+                mma_f16_16x8x16(part[u][grp][h], a0, a1, a2, a3, qf[grp][h * 4 + i][0], qf[grp][h * 4 + i][1]);
+            }
         }
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp)
+        for (int u = 0; u < NU; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[grp][i] = s[grp][i] * ks[i >> 1] * cq[grp][i & 1];
-        if (edge) {
-          const int32_t j0 = base + pg;
-          if (j0 < w.t0 || j0 >= w.t1) lv[0] = 0.f;              // whatever an unused place holds
-          if (j0 + 8 < w.t0 || j0 + 8 >= w.t1) lv[1] = 0.f;
+          for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float v = part[u][grp][0][i];
+              if constexpr (KC == 2) v += part[u][grp][1][i];
+              s[u][grp][i] = v * ks[u][i >> 1] * cq[grp][i & 1];
+            }
+      }
+      if (edge) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+          const int32_t j0 = base[u] + pg;
+          if (j0 < w.t0 || j0 >= w.t1) lv[u][0] = 0.f;              // whatever an unused place holds
+          if (j0 + 8 < w.t0 || j0 + 8 >= w.t1) lv[u][1] = 0.f;
 #pragma unroll
           for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
@@ -462,103 +518,136 @@ __global__ void __launch_bounds__(kDecThreads, 1)
               const int r = grp * 8 + 2 * t + e;
               int32_t lo, hi;
               seen_range(a, w.kv_len, w.pos0 + r / a.group, lo, hi);
-              if (j0 < lo || j0 >= hi) s[grp][e] = -INFINITY;
-              if (j0 + 8 < lo || j0 + 8 >= hi) s[grp][2 + e] = -INFINITY;
+              if (j0 < lo || j0 >= hi) s[u][grp][e] = -INFINITY;
+              if (j0 + 8 < lo || j0 + 8 >= hi) s[u][grp][2 + e] = -INFINITY;
             }
         }
-        // ---- move the references when a score passes its limit
-        bool need = false;
+      }
+      // ---- move the references when a score passes its limit
+      float top[NG][2], topv[NG][2];
+      bool need = false;
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp)
+      for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            need |= fmaxf(s[grp][e], s[grp][2 + e]) > m[grp][e] + kLag ||
-                    fmaxf(s[grp][e] + lv[0], s[grp][2 + e] + lv[1]) > mv[grp][e] + kLag;
-        if (__any_sync(0xffffffffu, need)) {
+        for (int e = 0; e < 2; ++e) {
+          top[grp][e] = topv[grp][e] = -INFINITY;
 #pragma unroll
-          for (int grp = 0; grp < NG; ++grp) {
-            float fe[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float mn = fmaxf(m[grp][e], max_over_g(fmaxf(s[grp][e], s[grp][2 + e])));
-              const float vn = fmaxf(mv[grp][e], max_over_g(fmaxf(s[grp][e] + lv[0], s[grp][2 + e] + lv[1])));
-              l[grp][e] *= ex2(m[grp][e] - mn);
-              fe[e] = ex2(mv[grp][e] - vn);
-              m[grp][e] = mn;
-              mv[grp][e] = vn;
-            }
-#pragma unroll
-            for (int j = 0; j < DT; ++j) {
-              acc[grp][j][0] *= fe[0];
-              acc[grp][j][1] *= fe[1];
-              acc[grp][j][2] *= fe[0];
-              acc[grp][j][3] *= fe[1];
-            }
+          for (int u = 0; u < NU; ++u) {
+            top[grp][e] = fmaxf(top[grp][e], fmaxf(s[u][grp][e], s[u][grp][2 + e]));
+            topv[grp][e] = fmaxf(topv[grp][e], fmaxf(s[u][grp][e] + lv[u][0], s[u][grp][2 + e] + lv[u][1]));
           }
+          need |= top[grp][e] > m[grp][e] + kLag || topv[grp][e] > mv[grp][e] + kLag;
         }
-        // ---- weights, and the second product's operand
-        uint32_t pb[NG][2];
+      if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp) {
-          l[grp][0] += ex2(s[grp][0] - m[grp][0]) + ex2(s[grp][2] - m[grp][0]);
-          l[grp][1] += ex2(s[grp][1] - m[grp][1]) + ex2(s[grp][3] - m[grp][1]);
-          const float b0 = mv[grp][0] - kLift, b1 = mv[grp][1] - kLift;
-          pb[grp][0] = transpose8x8(pack_f16x2(ex2(s[grp][0] + (lv[0] - b0)), ex2(s[grp][1] + (lv[0] - b1))));
-          pb[grp][1] = transpose8x8(pack_f16x2(ex2(s[grp][2] + (lv[1] - b0)), ex2(s[grp][3] + (lv[1] - b1))));
+          float fe[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mn = fmaxf(m[grp][e], max_over_g(top[grp][e]));
+            const float vn = fmaxf(mv[grp][e], max_over_g(topv[grp][e]));
+            l[grp][e] *= ex2(m[grp][e] - mn);
+            fe[e] = ex2(mv[grp][e] - vn);
+            m[grp][e] = mn;
+            mv[grp][e] = vn;
+          }
+#pragma unroll
+          for (int j = 0; j < DT; ++j) {
+            acc[grp][j][0] *= fe[0];
+            acc[grp][j][1] *= fe[1];
+            acc[grp][j][2] *= fe[0];
+            acc[grp][j][3] *= fe[1];
+          }
         }
-        // ---- values: bytes of four tokens interleaved into token pairs
-        if constexpr (D == 128) {
-          uint4 vw[4];
+      }
+      // ---- weights, and the second product's operand
+      uint32_t pb[NU][NG][2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vw[i] = *reinterpret_cast<const uint4*>(vst + chunk_off<D>(v_tok[i], pg));
-          if (edge) {
+      for (int grp = 0; grp < NG; ++grp) {
+        const float b0 = mv[grp][0] - kLift, b1 = mv[grp][1] - kLift;
+        float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (base + v_tok[i] < w.t0 || base + v_tok[i] >= w.t1) vw[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int u = 0; u < NU; ++u) {
+          l0 += ex2(s[u][grp][0] - m[grp][0]) + ex2(s[u][grp][2] - m[grp][0]);
+          l1 += ex2(s[u][grp][1] - m[grp][1]) + ex2(s[u][grp][3] - m[grp][1]);
+          pb[u][grp][0] =
+              transpose8x8(pack_f16x2(ex2(s[u][grp][0] + (lv[u][0] - b0)), ex2(s[u][grp][1] + (lv[u][0] - b1))));
+          pb[u][grp][1] =
+              transpose8x8(pack_f16x2(ex2(s[u][grp][2] + (lv[u][1] - b0)), ex2(s[u][grp][3] + (lv[u][1] - b1))));
+        }
+        l[grp][0] += l0;
+        l[grp][1] += l1;
+      }
+      // ---- values: bytes of four tokens interleaved into token pairs
+      constexpr int VW = D / 32;                               // words of a token that a lane takes
+      uint32_t vw[NU][4][VW];
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(vst[u] + chunk_off<D>(v_tok[i], pg));
+            vw[u][i][0] = x.x;
+            vw[u][i][1] = x.y;
+            vw[u][i][2] = x.z;
+            vw[u][i][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(vst[u] + chunk_off<D>(v_tok[i], g >> 1) + 8 * (g & 1));
+            vw[u][i][0] = x.x;
+            vw[u][i][1] = x.y;
           }
+          if (edge && (base[u] + v_tok[i] < w.t0 || base[u] + v_tok[i] >= w.t1)) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            auto word = [&](int n) { return i == 0 ? vw[n].x : i == 1 ? vw[n].y : i == 2 ? vw[n].z : vw[n].w; };
-#pragma unroll
-            for (int hlf = 0; hlf < 2; ++hlf) {
-              const uint32_t sel = hlf ? 0x7362u : 0x5140u;
-              uint32_t a0, a1, a2, a3;
-              e4m3x4_to_f16(__byte_perm(word(0), word(1), sel), a0, a1);
-              e4m3x4_to_f16(__byte_perm(word(2), word(3), sel), a2, a3);
-#pragma unroll
-              for (int grp = 0; grp < NG; ++grp)
-                mma_f16_16x8x16(acc[grp][2 * i + hlf], a0, a1, a2, a3, pb[grp][0], pb[grp][1]);
-            }
+            for (int e = 0; e < VW; ++e) vw[u][i][e] = 0u;
           }
+        }
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int i = 0; i < VW; ++i)
+#pragma unroll
+          for (int hlf = 0; hlf < 2; ++hlf) {
+            const uint32_t sel = hlf ? 0x7362u : 0x5140u;
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16(__byte_perm(vw[u][0][i], vw[u][1][i], sel), a0, a1);
+            e4m3x4_to_f16(__byte_perm(vw[u][2][i], vw[u][3][i], sel), a2, a3);
+#pragma unroll
+            for (int grp = 0; grp < NG; ++grp)
+              mma_f16_16x8x16(acc[grp][2 * i + hlf], a0, a1, a2, a3, pb[u][grp][0], pb[u][grp][1]);
+          }
+    };
+    for (int32_t k = c.k0; k < c.k1;) {
+      const int n = C::kAtOnce == 2 && k + 1 < c.k1 ? 2 : 1;
+      for (int u = 0; u < n && ok; ++u) {
+        const bool in = mbar_wait_bounded(bar_full(static_cast<int>((q + u) % C::kStages)),
+                                          static_cast<uint32_t>(((q + u) / C::kStages) & 1), p.wait_limit);
+        ok = __all_sync(0xffffffffu, in);
+        if (!ok && lane == 0) report_failure(a.err, kDevTimeoutEpilogue);
+      }
+      const int32_t base = (ub + k) * kUnit + warp * 16;
+      const bool live0 = base < w.t1 && base + 16 > w.t0, live1 = base + kUnit < w.t1 && base + kUnit + 16 > w.t0;
+      if (ok) {
+        if (C::kAtOnce == 2 && n == 2 && live0 && live1) {
+          process(std::integral_constant<int, C::kAtOnce>{}, k);
         } else {
-          uint2 vw[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            vw[i] = *reinterpret_cast<const uint2*>(vst + chunk_off<D>(v_tok[i], g >> 1) + 8 * (g & 1));
-          if (edge) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (base + v_tok[i] < w.t0 || base + v_tok[i] >= w.t1) vw[i] = make_uint2(0u, 0u);
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            auto word = [&](int n) { return i == 0 ? vw[n].x : vw[n].y; };
-#pragma unroll
-            for (int hlf = 0; hlf < 2; ++hlf) {
-              const uint32_t sel = hlf ? 0x7362u : 0x5140u;
-              uint32_t a0, a1, a2, a3;
-              e4m3x4_to_f16(__byte_perm(word(0), word(1), sel), a0, a1);
-              e4m3x4_to_f16(__byte_perm(word(2), word(3), sel), a2, a3);
-#pragma unroll
-              for (int grp = 0; grp < NG; ++grp)
-                mma_f16_16x8x16(acc[grp][2 * i + hlf], a0, a1, a2, a3, pb[grp][0], pb[grp][1]);
-            }
+          if (live0) process(std::integral_constant<int, 1>{}, k);
+          if (n == 2 && live1) {
+            ++q;
+            process(std::integral_constant<int, 1>{}, k + 1);
+            --q;
           }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_empty(slot));
+      if (lane == 0)
+        for (int u = 0; u < n; ++u) mbar_arrive(bar_empty(static_cast<int>((q + u) % C::kStages)));
+      q += n;
+      k += n;
     }
+
+    Cursor nx = c;
+    more = next(nx);
+    if (more && kAhead) fetch(nx);
 
     // ---- the warps' parts of the item, added in warp order, a group of 8 rows at a time
     const bool whole = c.k0 == 0 && c.k1 == w.units;
@@ -620,8 +709,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
               a.lse[(w.row0 + i) * a.heads + head] = lse2 * 0.6931471805599453f;
           }
         } else {
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) part_o[r * D + lane * (D / 32) + e] = o[e];
+          if constexpr (D == 128)
+            *reinterpret_cast<float4*>(part_o + r * D + lane * 4) = make_float4(o[0], o[1], o[2], o[3]);
+          else *reinterpret_cast<float2*>(part_o + r * D + lane * 2) = make_float2(o[0], o[1]);
           if (lane == 0) part_o[kRows * D + r] = lse2;
         }
       }
@@ -629,8 +719,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (!whole) {
       // ---- the last CTA of the item to arrive adds the parts in CTA order
       const int64_t i0 = c.item0, i1 = c.item0 + w.units;
-      const int c_first = static_cast<int>(((i0 + 1) * ctas - 1) / total);
-      const int c_last = static_cast<int>((i1 * ctas - 1) / total);
+      const int c_first = share_of(i0, total, ctas);
+      const int c_last = share_of(i1 - 1, total, ctas);
       __threadfence();
       named_bar_sync(1, kDecWarps * 32);
       if (tid == 0) {
@@ -641,11 +731,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       named_bar_sync(1, kDecWarps * 32);
       if (s_last) {
         __threadfence();
+        // the first CTA's part is its last segment, unless the item begins with its share
+        const int first_slot = 2 * c_first + (share_begin(c_first, total, ctas) < i0 ? 1 : 0);
         auto slot_of = [&](int cc) -> const float* {
-          const int64_t cu0 = cc * total / ctas;
-          return p.partials + static_cast<int64_t>(2 * cc + (i0 <= cu0 ? 0 : 1)) * kRows * (D + 1);
+          return p.partials + static_cast<int64_t>(cc == c_first ? first_slot : 2 * cc) * kRows * (D + 1);
         };
         for (int r = warp; r < rows; r += kDecWarps) {
+          // log2 sums and weights a lane each; the parts' loads sixteen at a time
           float top = -INFINITY;
           for (int cc = c_first + lane; cc <= c_last; cc += 32) top = fmaxf(top, __ldcg(slot_of(cc) + kRows * D + r));
 #pragma unroll
@@ -654,12 +746,25 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           float sum = 0.f, o[D / 32];
 #pragma unroll
           for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-          for (int cc = c_first; cc <= c_last; ++cc) {
-            const float* src = slot_of(cc);
-            const float wgt = ex2(__ldcg(src + kRows * D + r) - ref);
-            sum += wgt;
+          for (int c0 = c_first; c0 <= c_last; c0 += 32) {
+            const float wl = c0 + lane <= c_last ? ex2(__ldcg(slot_of(c0 + lane) + kRows * D + r) - ref) : 0.f;
+            const int n = c_last - c0 + 1 < 32 ? c_last - c0 + 1 : 32;
+            for (int j0 = 0; j0 < n; j0 += 16) {
+              using Vec = typename std::conditional<D == 128, float4, float2>::type;
+              Vec v[16];
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) o[e] = fmaf(__ldcg(src + r * D + lane * (D / 32) + e), wgt, o[e]);
+              for (int j = 0; j < 16; ++j)
+                v[j] = __ldcg(reinterpret_cast<const Vec*>(slot_of(c0 + (j0 + j < n ? j0 + j : n - 1)) + r * D) + lane);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float wgt = __shfl_sync(0xffffffffu, wl, (j0 + j) & 31);
+                if (j0 + j >= n) wgt = 0.f;
+                sum += wgt;
+                const float* x = reinterpret_cast<const float*>(&v[j]);
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) o[e] = fmaf(x[e], wgt, o[e]);
+              }
+            }
           }
           const float inv = sum > 0.f ? 1.f / sum : 0.f;
           const int i = r / a.group, head = c.h * a.group + r - i * a.group;
@@ -675,7 +780,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
       }
     }
-    more = next(c);
+    c = nx;
   }
 }
 

@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (tid == 0) {
       s_total = total;
       s_ctas = static_cast<int>(ctas);
-      s_u0 = blockIdx.x * total / ctas;
-      s_u1 = (blockIdx.x + 1) * total / ctas;
+      s_u0 = share_begin(blockIdx.x, total, ctas);
+      s_u1 = share_begin(blockIdx.x + 1, total, ctas);
     }
     __syncthreads();
   }
@@ -958,8 +958,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       } else {
         part_lse[t * kTile + r] = lse2;
         const int64_t i0 = c.item0, i1 = c.item0 + c.n, total = s_total, ctas = s_ctas;
-        const int c_first = static_cast<int>(((i0 + 1) * ctas - 1) / total);
-        const int c_last = static_cast<int>((i1 * ctas - 1) / total);
+        const int c_first = share_of(i0, total, ctas);
+        const int c_last = share_of(i1 - 1, total, ctas);
         __threadfence();
         named_bar_sync(1 + t, kTile);
         if (r == 0) {
@@ -970,8 +970,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         named_bar_sync(1 + t, kTile);
         if (s_last[t]) {
           __threadfence();
+          // the first CTA's part is its last segment, unless the block begins with its share
+          const int first_slot = 2 * c_first + (share_begin(c_first, total, ctas) < i0 ? 1 : 0);
           auto slot_of = [&](int cta) -> const float* {
-            return p.partials + (2 * cta + (i0 <= cta * total / ctas ? 0 : 1)) * slot_floats<D>();
+            return p.partials + (cta == c_first ? first_slot : 2 * cta) * slot_floats<D>();
           };
           float best = -INFINITY;
           for (int cta = c_first; cta <= c_last; ++cta)
