@@ -12,8 +12,8 @@
 //
 // A producer warp streams units through TMA (tensor-map boxes of one page and
 // head, 128-byte swizzle, and the pages' scales by bulk copies) into a ring.
-// Eight warps take 16 tokens of a unit each and keep their own running
-// maximum, sum and output.  The tokens are the 16-row operand of
+// Teams of four warps take units in turn, 32 tokens a warp; each warp keeps its
+// own running maximum, sum and output.  The tokens are the 16-row operand of
 // mma.sync.m16n8k16 (f16, fp32 sums) and the query rows its 8 columns:
 //   S^T [16 tokens x 8 rows] = K Q^T,    O^T [D x 8 rows] += V^T P^T.
 // The e4m3 codes become f16 in registers (exact, one conversion a pair).  Slots
@@ -50,11 +50,7 @@ namespace bfp8 {
 
 namespace {
 
-constexpr int kDecWarps = 8;
 constexpr int kUnit = 128;                 // tokens of a unit
-// two warpgroups of consumers and one whose first warp produces: registers are
-// handed from the third (56 a thread) to the first two (224) of 168 at launch
-constexpr int kDecThreads = (kDecWarps + 4) * 32;
 constexpr int kItemCost = 4;               // (measured: query, joining the warps, output 5000 cycles; a unit 1340)
 constexpr int kSeqCache = 64;              // sequences whose lengths a CTA keeps in shared memory
 constexpr float kNoMax = -3.0e38f;         // running maximum before any token
@@ -67,13 +63,19 @@ struct DecCfg {
   static constexpr int kStageBytes = 2 * kCodes;
   static constexpr int kScaleFloats = 2 * kUnit;
   static constexpr int kStages = D == 128 ? 5 : 8;
-  // units a warp takes at once: two where the registers allow it
+  // Consumers: groups of four warps that take units in turn, 32 tokens a warp, as two chains of 16
+  // where the registers allow it.  A fourth warpgroup (its first warp) produces; registers are handed
+  // to the consumers (launch: 128 or 168 a thread).
+  static constexpr int kWarps = NG == 1 ? 12 : 8;
+  static constexpr int kGroups = kWarps / 4;
+  static constexpr int kThreads = (kWarps + 4) * 32;
+  static constexpr int kRegs = NG == 1 ? 152 : 224, kRegsProducer = 56;
   static constexpr int kAtOnce = NG <= 2 ? 2 : 1;
   static constexpr int kPitch = D + 4;                     // floats of a row of partials
   static constexpr int kOffScale = kStages * kStageBytes;
   static constexpr int kOffRed = kOffScale + kStages * kScaleFloats * 4;
-  static constexpr int kOffMl = kOffRed + kDecWarps * 8 * kPitch * 4;
-  static constexpr int kOffSeq = kOffMl + kDecWarps * 8 * 3 * 4;
+  static constexpr int kOffMl = kOffRed + kWarps * 8 * kPitch * 4;
+  static constexpr int kOffSeq = kOffMl + kWarps * 8 * 3 * 4;
   static constexpr int kOffBar = kOffSeq + kSeqCache * 32;
   static constexpr int kSmem = kOffBar + 2 * kStages * 8 + 64 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -169,7 +171,7 @@ struct DecodeArgs {
 };
 
 template <int D, int NG>
-__global__ void __launch_bounds__(kDecThreads, 1)
+__global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ DecodeArgs p) {
   using C = DecCfg<D, NG>;
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), kDecWarps);
+      mbar_init(bar_empty(s), 4);
     }
     fence_barrier_init();
   }
@@ -196,17 +198,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   griddep_wait();
 
   // ---- this CTA's share [u0, u1) of the line of units, and where it starts
-  __shared__ int64_t part[kDecThreads / 32];
+  __shared__ int64_t part[C::kThreads / 32];
   __shared__ int64_t s_before;
   __shared__ int s_b;
   int64_t run = 0, incl0 = 0;
   SeqWork mine{};                                      // sequence tid of the last chunk of them
-  for (int b0 = 0; b0 < a.batch; b0 += kDecThreads) {
+  for (int b0 = 0; b0 < a.batch; b0 += C::kThreads) {
     const int b = b0 + tid;
     mine.units = 0;
     if (b < a.batch) mine = seq_work(a, b, kRows);
     incl0 = block_scan(line_cost(mine.units), part);
-    if (tid == kDecThreads - 1) part[0] = incl0;
+    if (tid == C::kThreads - 1) part[0] = incl0;
     __syncthreads();
     run += part[0];
     __syncthreads();
@@ -221,18 +223,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       s_before = (incl - n) * H;
     }
   };
-  if (a.batch <= kDecThreads) {                        // the lengths are in registers
+  if (a.batch <= C::kThreads) {                        // the lengths are in registers
     locate(tid, incl0, line_cost(mine.units));
     __syncthreads();
     if (tid >= s_b && tid < a.batch && tid - s_b < kSeqCache) seqs[tid - s_b] = mine;
   } else {
     run = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kDecThreads) {
+    for (int b0 = 0; b0 < a.batch; b0 += C::kThreads) {
       const int b = b0 + tid;
       const int32_t n = b < a.batch ? line_cost(seq_work(a, b, kRows).units) : 0;
       const int64_t incl = run + block_scan(n, part);
       locate(b, incl, n);
-      if (tid == kDecThreads - 1) part[0] = incl;
+      if (tid == C::kThreads - 1) part[0] = incl;
       __syncthreads();
       run = part[0];
       __syncthreads();
@@ -277,15 +279,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     return clip(c) || next(c);
   };
 
-  if (warp >= kDecWarps) {
+  if (warp >= C::kWarps) {
     // ------------------------------------------------------------ producer
-    setmaxnreg_dec<56>();
-    if (warp > kDecWarps) return;
+    setmaxnreg_dec<C::kRegsProducer>();
+    if (warp > C::kWarps) return;
     const int page = a.c.page_size, shift = a.c.page_shift;
     const int ppu = page >= kUnit ? 1 : kUnit / page;            // boxes of a unit
     const int box = page >= kUnit ? kUnit : page;                // tokens of a box
     const uint32_t box_bytes = static_cast<uint32_t>(2 * box * D + 2 * box * 4);
-    int64_t q = 0;
+    uint32_t q = 0;
     bool ok = true;
     Cursor c;
     for (bool more = start(c); more && ok; more = next(c)) {
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       }
     }
     // no copy may still be landing in shared memory when the CTA exits
-    for (int64_t i = q > C::kStages ? q - C::kStages : 0; i < q; ++i)
+    for (uint32_t i = q > C::kStages ? q - C::kStages : 0; i < q; ++i)
       if (!mbar_wait_bounded(bar_full(static_cast<int>(i % C::kStages)), static_cast<uint32_t>((i / C::kStages) & 1),
                              p.wait_limit)) {
         if (lane == 0) report_failure(a.err, kDevTimeoutTail);
@@ -347,7 +349,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
 
   // ------------------------------------------------------------- consumers
-  setmaxnreg_inc<224>();
+  setmaxnreg_inc<C::kRegs>();
+  const int team = warp >> 2, wq = warp & 3;         // units team, team + kGroups .. ; 32 tokens of each
   const int g = lane >> 2, t = lane & 3;
   const int pg = slot_token<D>(g);
   // value chunk and tokens of this lane
@@ -357,11 +360,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   constexpr int DT = D / 16;                 // 16-element tiles of the output
   float* red = reinterpret_cast<float*>(smem + C::kOffRed);
   float* red_m = reinterpret_cast<float*>(smem + C::kOffMl);
-  float* red_l = red_m + kDecWarps * 8;
-  float* red_v = red_l + kDecWarps * 8;
+  float* red_l = red_m + C::kWarps * 8;
+  float* red_v = red_l + C::kWarps * 8;
   __shared__ int s_last;
   bool ok = true;
-  int64_t q = 0;
+  uint32_t q = 0;
   // the rows grp * 8 + g of an item's queries, this lane's elements; fetched while the item before ends
   uint4 raw[NG][KC][2];
   auto fetch = [&](const Cursor& c) {
@@ -441,8 +444,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       for (int j = 0; j < DT; ++j) acc[grp][j][0] = acc[grp][j][1] = acc[grp][j][2] = acc[grp][j][3] = 0.f;
     }
     const int32_t ub = w.t0 / kUnit;
-    // 16 tokens of this warp in each of NU units (stages q ..), whose chains of dependent steps overlap
-    auto process = [&](auto nu, int32_t k) {
+    // NU times 16 tokens from `first` of this warp's 32 of a unit, whose chains of dependent steps overlap
+    auto process = [&](auto nu, int32_t k, int first) {
       constexpr int NU = decltype(nu)::value;
       int32_t base[NU];
       const uint8_t *kst[NU], *vst[NU];
@@ -450,11 +453,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       bool edge = false;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        const int slot = static_cast<int>((q + u) % C::kStages);
-        base[u] = (ub + k + u) * kUnit + warp * 16;
-        kst[u] = smem + slot * C::kStageBytes + warp * 16 * D;
+        const int slot = static_cast<int>(q % C::kStages), at = wq * 32 + first + 16 * u;
+        base[u] = (ub + k) * kUnit + at;
+        kst[u] = smem + slot * C::kStageBytes + at * D;
         vst[u] = kst[u] + C::kCodes;
-        const float* sc = reinterpret_cast<const float*>(smem + C::kOffScale) + slot * C::kScaleFloats + warp * 16;
+        const float* sc = reinterpret_cast<const float*>(smem + C::kOffScale) + slot * C::kScaleFloats + at;
         edge |= base[u] < full_lo || base[u] + 16 > full_hi;
         ks[u][0] = sc[pg];
         ks[u][1] = sc[pg + 8];
@@ -616,33 +619,26 @@ __global__ void __launch_bounds__(kDecThreads, 1)
               mma_f16_16x8x16(acc[grp][2 * i + hlf], a0, a1, a2, a3, pb[u][grp][0], pb[u][grp][1]);
           }
     };
-    for (int32_t k = c.k0; k < c.k1;) {
-      const int n = C::kAtOnce == 2 && k + 1 < c.k1 ? 2 : 1;
-      for (int u = 0; u < n && ok; ++u) {
-        const bool in = mbar_wait_bounded(bar_full(static_cast<int>((q + u) % C::kStages)),
-                                          static_cast<uint32_t>(((q + u) / C::kStages) & 1), p.wait_limit);
+    for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
+      if (static_cast<int>(q % C::kGroups) != team) continue;
+      const int slot = static_cast<int>(q % C::kStages);
+      if (ok) {
+        const bool in = mbar_wait_bounded(bar_full(slot), (q / C::kStages) & 1u, p.wait_limit);
         ok = __all_sync(0xffffffffu, in);
         if (!ok && lane == 0) report_failure(a.err, kDevTimeoutEpilogue);
       }
-      const int32_t base = (ub + k) * kUnit + warp * 16;
-      const bool live0 = base < w.t1 && base + 16 > w.t0, live1 = base + kUnit < w.t1 && base + kUnit + 16 > w.t0;
-      if (ok) {
-        if (C::kAtOnce == 2 && n == 2 && live0 && live1) {
-          process(std::integral_constant<int, C::kAtOnce>{}, k);
+      const int32_t base = (ub + k) * kUnit + wq * 32;
+      if (ok && base < w.t1 && base + 32 > w.t0) {
+        if constexpr (C::kAtOnce == 2) {
+          process(std::integral_constant<int, 2>{}, k, 0);
         } else {
-          if (live0) process(std::integral_constant<int, 1>{}, k);
-          if (n == 2 && live1) {
-            ++q;
-            process(std::integral_constant<int, 1>{}, k + 1);
-            --q;
-          }
+#pragma unroll 1
+          for (int first = 0; first < 32; first += 16)
+            if (base + first < w.t1 && base + first + 16 > w.t0) process(std::integral_constant<int, 1>{}, k, first);
         }
       }
       __syncwarp();
-      if (lane == 0)
-        for (int u = 0; u < n; ++u) mbar_arrive(bar_empty(static_cast<int>((q + u) % C::kStages)));
-      q += n;
-      k += n;
+      if (lane == 0) mbar_arrive(bar_empty(slot));
     }
 
     Cursor nx = c;
@@ -656,7 +652,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const int vchunk = D == 128 ? 16 * pg : 8 * g;         // first output element of this lane
 #pragma unroll
     for (int grp = 0; grp < NG; ++grp) {
-      named_bar_sync(1, kDecWarps * 32);
+      named_bar_sync(1, C::kWarps * 32);
       const float l0 = sum_over_g(l[grp][0]), l1 = sum_over_g(l[grp][1]);
       if (g == 0) {
         red_m[warp * 8 + 2 * t] = m[grp][0];
@@ -675,15 +671,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         *reinterpret_cast<float4*>(r1 + 2 * j) =
             make_float4(acc[grp][j][1], acc[grp][j][3], acc[grp][j + 1][1], acc[grp][j + 1][3]);
       }
-      named_bar_sync(1, kDecWarps * 32);
+      named_bar_sync(1, C::kWarps * 32);
       const int r = grp * 8 + warp;                        // warp w finishes row w of the group
-      if (r < rows) {
+      if (warp < 8 && r < rows) {
         float top = kNoMax, sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kDecWarps; ++i) top = fmaxf(top, red_m[i * 8 + warp]);
-        float f[kDecWarps];
+        for (int i = 0; i < C::kWarps; ++i) top = fmaxf(top, red_m[i * 8 + warp]);
+        float f[C::kWarps];
 #pragma unroll
-        for (int i = 0; i < kDecWarps; ++i) {
+        for (int i = 0; i < C::kWarps; ++i) {
           f[i] = ex2(red_m[i * 8 + warp] - top);
           sum += red_l[i * 8 + warp] * f[i];
         }
@@ -693,7 +689,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kDecWarps; ++i) {
+        for (int i = 0; i < C::kWarps; ++i) {
           const float ci = ex2(red_v[i * 8 + warp] - kLift - top) * inv;
           const float* src = red + (i * 8 + warp) * C::kPitch + lane * (D / 32);
 #pragma unroll
@@ -722,13 +718,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const int c_first = share_of(i0, total, ctas);
       const int c_last = share_of(i1 - 1, total, ctas);
       __threadfence();
-      named_bar_sync(1, kDecWarps * 32);
+      named_bar_sync(1, C::kWarps * 32);
       if (tid == 0) {
         const int n = atomicAdd(p.counters + c_first, 1);
         s_last = n == c_last - c_first;
         if (s_last) p.counters[c_first] = 0;
       }
-      named_bar_sync(1, kDecWarps * 32);
+      named_bar_sync(1, C::kWarps * 32);
       if (s_last) {
         __threadfence();
         // the first CTA's part is its last segment, unless the item begins with its share
@@ -736,7 +732,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         auto slot_of = [&](int cc) -> const float* {
           return p.partials + static_cast<int64_t>(cc == c_first ? first_slot : 2 * cc) * kRows * (D + 1);
         };
-        for (int r = warp; r < rows; r += kDecWarps) {
+        for (int r = warp; r < rows; r += C::kWarps) {
           // log2 sums and weights a lane each; the parts' loads sixteen at a time
           float top = -INFINITY;
           for (int cc = c_first + lane; cc <= c_last; cc += 32) top = fmaxf(top, __ldcg(slot_of(cc) + kRows * D + r));
@@ -793,7 +789,7 @@ cudaError_t launch_decode_ng(const CUtensorMap& k, const CUtensorMap& v, const D
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kDecThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
