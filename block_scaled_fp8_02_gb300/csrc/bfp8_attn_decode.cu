@@ -52,7 +52,7 @@ namespace {
 
 constexpr int kUnit = 128;                 // tokens of a unit
 constexpr int kItemCost = 4;               // (measured: query, joining the warps, output 5000 cycles; a unit 1340)
-constexpr int kSeqCache = 64;              // sequences whose lengths a CTA keeps in shared memory
+constexpr int kSeqCache = 32;              // sequences whose lengths a CTA keeps in shared memory
 constexpr float kNoMax = -3.0e38f;         // running maximum before any token
 constexpr float kLag = 8.f;                // how far scores may exceed the running maximum
 constexpr float kLift = 7.f;               // weighted values are 2^(x + log2 vs - mv + kLift) <= 2^15
@@ -62,7 +62,7 @@ struct DecCfg {
   static constexpr int kCodes = kUnit * D;                 // K or V of a unit
   static constexpr int kStageBytes = 2 * kCodes;
   static constexpr int kScaleFloats = 2 * kUnit;
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 6 : 12;
   // Consumers: groups of four warps that take units in turn, 32 tokens a warp, as two chains of 16
   // where the registers allow it.  A fourth warpgroup (its first warp) produces; registers are handed
   // to the consumers (launch: 128 or 168 a thread).
@@ -71,11 +71,15 @@ struct DecCfg {
   static constexpr int kThreads = (kWarps + 4) * 32;
   static constexpr int kRegs = NG == 1 ? 152 : 224, kRegsProducer = 56;
   static constexpr int kAtOnce = NG <= 2 ? 2 : 1;
+  // a slot always belongs to the same team, which waits for each of its phases in turn: a wait by parity
+  // cannot tell a phase from the one two further on
+  static_assert(kStages % kGroups == 0, "slots belong to teams");
   static constexpr int kPitch = D + 4;                     // floats of a row of partials
+  static constexpr int kJoin = 4;                          // rows whose warps' parts are joined at once
   static constexpr int kOffScale = kStages * kStageBytes;
   static constexpr int kOffRed = kOffScale + kStages * kScaleFloats * 4;
-  static constexpr int kOffMl = kOffRed + kWarps * 8 * kPitch * 4;
-  static constexpr int kOffSeq = kOffMl + kWarps * 8 * 3 * 4;
+  static constexpr int kOffMl = kOffRed + kWarps * kJoin * kPitch * 4;
+  static constexpr int kOffSeq = kOffMl + kWarps * kJoin * 3 * 4;
   static constexpr int kOffBar = kOffSeq + kSeqCache * 32;
   static constexpr int kSmem = kOffBar + 2 * kStages * 8 + 64 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -360,8 +364,8 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
   constexpr int DT = D / 16;                 // 16-element tiles of the output
   float* red = reinterpret_cast<float*>(smem + C::kOffRed);
   float* red_m = reinterpret_cast<float*>(smem + C::kOffMl);
-  float* red_l = red_m + C::kWarps * 8;
-  float* red_v = red_l + C::kWarps * 8;
+  float* red_l = red_m + C::kWarps * C::kJoin;
+  float* red_v = red_l + C::kWarps * C::kJoin;
   __shared__ int s_last;
   bool ok = true;
   uint32_t q = 0;
@@ -645,43 +649,48 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
     more = next(nx);
     if (more && kAhead) fetch(nx);
 
-    // ---- the warps' parts of the item, added in warp order, a group of 8 rows at a time
+    // ---- the warps' parts of the item, added in warp order, four rows at a time
     const bool whole = c.k0 == 0 && c.k1 == w.units;
     const int slot_id = 2 * blockIdx.x + (c.item0 + c.k0 == u0 ? 0 : 1);
     float* part_o = p.partials + static_cast<int64_t>(slot_id) * kRows * (D + 1);
     const int vchunk = D == 128 ? 16 * pg : 8 * g;         // first output element of this lane
 #pragma unroll
-    for (int grp = 0; grp < NG; ++grp) {
+    for (int part4 = 0; part4 < 2 * NG; ++part4) {
+      const int grp = part4 >> 1, hf = part4 & 1;          // rows 8 grp + 4 hf ..: those of lanes t = 2 hf, 2 hf + 1
+      if (part4 * C::kJoin >= rows) break;
       named_bar_sync(1, C::kWarps * 32);
       const float l0 = sum_over_g(l[grp][0]), l1 = sum_over_g(l[grp][1]);
-      if (g == 0) {
-        red_m[warp * 8 + 2 * t] = m[grp][0];
-        red_m[warp * 8 + 2 * t + 1] = m[grp][1];
-        red_l[warp * 8 + 2 * t] = l0;
-        red_l[warp * 8 + 2 * t + 1] = l1;
-        red_v[warp * 8 + 2 * t] = mv[grp][0];
-        red_v[warp * 8 + 2 * t + 1] = mv[grp][1];
-      }
-      float* r0 = red + (warp * 8 + 2 * t) * C::kPitch + vchunk;
-      float* r1 = r0 + C::kPitch;
+      if ((t >> 1) == hf) {
+        const int at = warp * C::kJoin + 2 * (t & 1);
+        if (g == 0) {
+          red_m[at] = m[grp][0];
+          red_m[at + 1] = m[grp][1];
+          red_l[at] = l0;
+          red_l[at + 1] = l1;
+          red_v[at] = mv[grp][0];
+          red_v[at + 1] = mv[grp][1];
+        }
+        float* r0 = red + at * C::kPitch + vchunk;
+        float* r1 = r0 + C::kPitch;
 #pragma unroll
-      for (int j = 0; j < DT; j += 2) {
-        *reinterpret_cast<float4*>(r0 + 2 * j) =
-            make_float4(acc[grp][j][0], acc[grp][j][2], acc[grp][j + 1][0], acc[grp][j + 1][2]);
-        *reinterpret_cast<float4*>(r1 + 2 * j) =
-            make_float4(acc[grp][j][1], acc[grp][j][3], acc[grp][j + 1][1], acc[grp][j + 1][3]);
+        for (int j = 0; j < DT; j += 2) {
+          *reinterpret_cast<float4*>(r0 + 2 * j) =
+              make_float4(acc[grp][j][0], acc[grp][j][2], acc[grp][j + 1][0], acc[grp][j + 1][2]);
+          *reinterpret_cast<float4*>(r1 + 2 * j) =
+              make_float4(acc[grp][j][1], acc[grp][j][3], acc[grp][j + 1][1], acc[grp][j + 1][3]);
+        }
       }
       named_bar_sync(1, C::kWarps * 32);
-      const int r = grp * 8 + warp;                        // warp w finishes row w of the group
-      if (warp < 8 && r < rows) {
+      const int r = part4 * C::kJoin + warp;               // warp w finishes row w of the four
+      if (warp < C::kJoin && r < rows) {
         float top = kNoMax, sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < C::kWarps; ++i) top = fmaxf(top, red_m[i * 8 + warp]);
+        for (int i = 0; i < C::kWarps; ++i) top = fmaxf(top, red_m[i * C::kJoin + warp]);
         float f[C::kWarps];
 #pragma unroll
         for (int i = 0; i < C::kWarps; ++i) {
-          f[i] = ex2(red_m[i * 8 + warp] - top);
-          sum += red_l[i * 8 + warp] * f[i];
+          f[i] = ex2(red_m[i * C::kJoin + warp] - top);
+          sum += red_l[i * C::kJoin + warp] * f[i];
         }
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const float lse2 = sum > 0.f ? top + log2f(sum) : -INFINITY;
@@ -690,8 +699,8 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
         for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
 #pragma unroll
         for (int i = 0; i < C::kWarps; ++i) {
-          const float ci = ex2(red_v[i * 8 + warp] - kLift - top) * inv;
-          const float* src = red + (i * 8 + warp) * C::kPitch + lane * (D / 32);
+          const float ci = ex2(red_v[i * C::kJoin + warp] - kLift - top) * inv;
+          const float* src = red + (i * C::kJoin + warp) * C::kPitch + lane * (D / 32);
 #pragma unroll
           for (int e = 0; e < D / 32; ++e) o[e] = fmaf(src[e], ci, o[e]);
         }
