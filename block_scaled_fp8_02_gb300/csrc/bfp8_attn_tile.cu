@@ -22,8 +22,9 @@
 // weights collects P 2^-lv, a tile's sum at a time.  Where a tile's value scales
 // differ by more than 2^11 its tokens' own log2 scales join the exponents instead.
 //
-// As in the kernel for few rows, the tiles of all blocks form one line that the
-// persistent CTAs share equally; a block cut by a border leaves fp32 partial
+// As in the kernel for few rows, the tiles of all blocks form one line (with
+// kBlockCost places behind each block's for the time that a block costs besides)
+// that the persistent CTAs share equally; a block cut by a border leaves fp32 partial
 // rows in the workspace and the last CTA to arrive adds them in CTA order.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -50,6 +51,7 @@ constexpr int kBlockRows = 2 * kTile;
 // 208 and 88 a thread after they are handed around.
 constexpr int kTileThreads = 384;
 constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpConv = 10, kConvWarps = 2;
+constexpr int kBlockCost = 8;              // (measured: a block's queries, first tiles, output 36000 cycles; a tile 4000)
 constexpr int kSeqChunk = 2048;            // sequences whose tile counts are held at once
 constexpr int kKStages = 3, kVStages = 2, kFStages = 2, kScSlots = 4;
 constexpr float kNoMax = -3.0e38f;
@@ -180,6 +182,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Orders later uses of the registers after the preceding wait.
 __device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
@@ -258,7 +271,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const SeqBlocks w = seq_blocks(a, b0 + i);
       int64_t v = 0;
       int32_t t0, t1;
-      for (int rb = lane; rb < w.blocks; rb += 32) v += block_tiles(a, w, rb, t0, t1);
+      for (int rb = lane; rb < w.blocks; rb += 32) v += block_tiles(a, w, rb, t0, t1) + kBlockCost;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (lane == 0) cnt[i] = v;
@@ -342,12 +355,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     c.n = block_tiles(a, c.w, c.rb, c.t0, c.t1);
   };
-  auto clip = [&](Cursor& c) {
+  auto clip = [&](Cursor& c) {                  // false: only the block's end lies in the share
     c.k0 = static_cast<int32_t>(s_u0 > c.item0 ? s_u0 - c.item0 : 0);
     c.k1 = static_cast<int32_t>(c.item0 + c.n < s_u1 ? c.n : s_u1 - c.item0);
+    return c.k0 < c.k1;
   };
   Cursor& c = reinterpret_cast<Cursor*>(smem + C::kOffCur)[warp];
-  auto start = [&]() {
+  auto advance = [&](Cursor& c) {               // false: the share is done
+    do {
+      c.item0 += c.n + kBlockCost;
+      if (c.item0 >= s_u1) return false;
+      step_block(c);
+    } while (!clip(c));
+    return true;
+  };
+  auto start = [&]() -> bool {
+    int more = 0;
     if (lane == 0) {
       c.b = s_b;
       c.w = seq_blocks(a, c.b);
@@ -355,25 +378,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       c.h = 0;
       c.item0 = s_before;
       c.n = block_tiles(a, c.w, 0, c.t0, c.t1);
-      while (c.item0 + c.n <= s_u0) {
-        c.item0 += c.n;
+      while (c.item0 + c.n + kBlockCost <= s_u0) {
+        c.item0 += c.n + kBlockCost;
         step_block(c);
       }
-      clip(c);
+      more = clip(c) || advance(c);
     }
+    more = __shfl_sync(0xffffffffu, more, 0);
     __syncwarp();
+    return more != 0;
   };
-  auto next = [&]() -> bool {                   // false: the share is done
+  auto next = [&]() -> bool {
     __syncwarp();
     int more = 0;
-    if (lane == 0) {
-      c.item0 += c.n;
-      if (c.item0 < s_u1) {
-        step_block(c);
-        clip(c);
-        more = 1;
-      }
-    }
+    if (lane == 0) more = advance(c);
     more = __shfl_sync(0xffffffffu, more, 0);
     __syncwarp();
     return more != 0;
@@ -472,8 +490,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int box = page >= kTile ? kTile : page;
       uint32_t q = 0, pending = 0;                      // loads begun; a tile whose scales wait
       int32_t p_tok = 0, p_t0 = 0, p_t1 = 0;
-      start();
-      do {
+      for (bool more = start(); more; more = next() && ok) {
         const int32_t ub = c.t0 / kTile, t0 = c.t0, t1 = c.t1, h = c.h, k1 = c.k1;
         const int32_t* row = a.table + c.b * a.ld_table;
         int32_t cached = -1, entry = 0;
@@ -532,7 +549,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tma_load_4d(sbase + static_cast<uint32_t>(C::kOffV + vs * C::kK + lane * box * D), &tmV, bar(bVf + vs), 0,
                         off, h, pg);
         }
-      } while (next() && ok);
+      }
       if (pending) scales(q - 1, p_tok, p_t0, p_t1);
       // no copy may still be landing when the CTA exits (after a failure: bounded waits all the same)
       auto drain = [&](int b0, int stages) {
@@ -576,8 +593,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       };
       uint32_t q = 0, done = 0;                  // stages are counted in 32 bits: at most 2^30 tokens an item
       uint32_t item = 0;
-      start();
-      do {
+      for (bool more_blocks = start(); more_blocks; more_blocks = next()) {
         const int32_t n = c.k1 - c.k0;
         if (lane == 0 && ok) {
           wait1(bQ, item & 1);
@@ -614,7 +630,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           ++item;
         }
-      } while (next());
+      }
       // every commit has arrived before the CTA exits
       if (lane == 0) {
         for (uint32_t i = done > kFStages ? done - kFStages : 0; i < done; ++i)
@@ -628,8 +644,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int cw = warp - kWarpConv, c8 = lane & 7, rsub = lane >> 3;
       constexpr int CH = D / 16;                        // 16-code chunks of a row
       uint32_t q = 0;
-      start();
-      do {
+      for (bool more = start(); more; more = next()) {
         for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
           const int sl = static_cast<int>(q % kScSlots), vs = static_cast<int>(q % kVStages),
                     fs = static_cast<int>(q % kFStages);
@@ -690,7 +705,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_arrive(bar(bSe + sl));
           }
         }
-      } while (next());
+      }
     }
   } else {
     // --------------------------------------------------------------- softmax
@@ -701,8 +716,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t tO = tS - t * 128 + C::kColO + t * 128;
     uint32_t q = 0;
     uint32_t item = 0;                                // blocks done
-    start();
-    bool more = true;
+    bool more = start();
     while (more) {
       // ---- this row's query, as two e4m3 rows
       const int64_t R = static_cast<int64_t>(c.rb) * kBlockRows + t * kTile + r;
@@ -758,7 +772,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bQ + t));
-      int32_t lo = 0, hi = 0;
+      // (rows past the last token see everything: their scores are computed beside the others' and
+      // dropped, and must not make tiles look masked)
+      int32_t lo = 0, hi = 0x7FFFFFFF;
       if (live) seen_range(a, c.w.kv_len, c.w.pos0 + i, lo, hi);
 
       float m = kNoMax, l = 0.f;
@@ -814,9 +830,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         };
         wait_all(bS + t, q & 1, kDevTimeoutEpilogue);
         tc_fence_after();
-        if (odd) {
-          // few tiles: masked scores become -inf, and a wide tile's take their tokens' own scales
-          // (its ks are ones), in tensor memory
+        if (odd && !wide) {
+          // masked scores become -inf, in tensor memory
+#pragma unroll 1
+          for (int g = 0; g < kTile / 32; ++g) {
+            uint32_t o[32];
+            tmem_ld32(tS + 32 * g, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+            const int32_t f = from - 32 * g, e1 = to - 32 * g;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = e >= f && e < e1 ? o[e] : 0xFF800000u;
+            tmem_st32(tS + 32 * g, o);
+          }
+          tmem_wait_st();
+        } else if (odd) {
+          // a wide tile: its scores take their tokens' own scales too (its ks are ones)
           const float* kr = reinterpret_cast<const float*>(smem + C::kOffRaw) + sl * 2 * kTile;
           const float* dl = reinterpret_cast<const float*>(smem + C::kOffDl) + sl * kTile;
           float top = -INFINITY;
@@ -830,7 +859,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int e = 0; e < 16; ++e) {
               const int j = 16 * g + e;
               float v = __uint_as_float(o[e]);
-              if (wide) v = fmaf(v * kr[j], cq, dl[j]);
+              v = fmaf(v * kr[j], cq, dl[j]);
               v = j >= from && j < to ? v : -INFINITY;
               top = fmaxf(top, v);
               o[e] = __float_as_uint(v);
@@ -838,7 +867,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tmem_st16(tS + 16 * g, o);
           }
           tmem_wait_st();
-          if (wide) {
+          {
             // its weights are summed here, by the maximum that the pass below then need not move
             if (__any_sync(0xffffffffu, top + lv > m + kLag)) move_max(top + lv, 0);
             const float* iv = reinterpret_cast<const float*>(smem + C::kOffIv) + sl * kTile;
