@@ -17,9 +17,12 @@
 // converting V, one for the MMAs, and one for TMA and the tiles' scales.
 //
 // Scores x are in powers of two.  A tile's values share the scale 2^lv, which
-// joins the exponent: P = 2^(x + lv - mv + 7) with mv a running maximum of x + lv
-// that may lag by up to 8 (then O and the sum are rescaled), and the sum of the
-// weights collects P 2^-lv, a tile's sum at a time.  Where a tile's value scales
+// joins the exponent: P = 2^(x + lv - mv + 7) with mv a running maximum of x + lv,
+// and the sum of the weights collects P 2^-lv, 64 columns' sum at a time.  mv may
+// lag for as long as 64 weights sum to 2^15 at most, which every f16 holds; only
+// where they pass that is the chunk's maximum looked for, O and the sum
+// rescaled and the chunk done again.  So a tile takes no pass for its maximum:
+// of the softmax's time a row (800 cycles beside another warp) that was 140.  Where a tile's value scales
 // differ by more than 2^11 its tokens' own log2 scales join the exponents instead.
 //
 // As in the kernel for few rows, the tiles of all blocks form one line (with
@@ -56,7 +59,8 @@ constexpr int kSeqChunk = 2048;            // sequences whose tile counts are he
 constexpr int kKStages = 3, kVStages = 2, kFStages = 2, kScSlots = 4;
 constexpr float kNoMax = -3.0e38f;
 constexpr float kLag = 8.f;
-constexpr float kLift = 7.f;               // P <= 2^15
+constexpr float kLift = 7.f;               // a weight at the running maximum is 2^7
+constexpr float kMost = 32768.f;           // sum of 64 weights up to which the maximum may lag: each fits f16
 constexpr int kVUp = 6;                    // values are scaled up by 2^6 in f16: 448 * 2^6 < 65504
 constexpr float kWide = 0x1p-11f;          // below this ratio of value scales a tile takes the other path
 
@@ -192,6 +196,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
+}
+// One lane of the warp, the same every time.  Where a branch hangs on it the compiler knows that one thread runs
+// and keeps an MMA's operands in uniform registers; on lane == 0 it cannot, and an MMA took so many instructions
+// that the softmax warps' held it up: 16 MMAs beside warps that never stop issuing 4177 cycles, with this 1246.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Orders later uses of the registers after the preceding wait.
@@ -565,7 +577,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       drain(bVf, kVStages);
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------- MMA
-      // the whole warp walks; its first lane waits and issues
+      // the whole warp walks; one lane waits and issues
       const uint32_t idS = idesc_e4m3_f32(128, 128), idO = idesc_f16_bmn(128, D);
       auto wait1 = [&](int i, uint32_t parity) {
         if (ok && !mbar_wait_bounded(bar(i), parity, p.wait_limit)) {
@@ -595,7 +607,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       uint32_t item = 0;
       for (bool more_blocks = start(); more_blocks; more_blocks = next()) {
         const int32_t n = c.k1 - c.k0;
-        if (lane == 0 && ok) {
+        if (elect_one()) {
           wait1(bQ, item & 1);
           wait1(bQ + 1, item & 1);
           wait1(bKf + static_cast<int>(q % kKStages), ph(q, kKStages));
@@ -632,7 +644,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       // every commit has arrived before the CTA exits
-      if (lane == 0) {
+      if (elect_one()) {
         for (uint32_t i = done > kFStages ? done - kFStages : 0; i < done; ++i)
           mbar_wait_bounded(bar(bFe + static_cast<int>(i % kFStages)), ph(i, kFStages), p.wait_limit);
         for (uint32_t i = done > kKStages ? done - kKStages : 0; i < done; ++i)
@@ -674,16 +686,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int u = 0; u < 4; ++u) {
               const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) e4m3x4_to_f16(ww[e], o[u][2 * e], o[u][2 * e + 1]);
+              for (int e = 0; e < 4; ++e)                 // unused places may hold anything
+                e4m3x4_to_f16(r[u].x == 0u ? 0u : ww[e], o[u][2 * e], o[u][2 * e + 1]);
             }
             // code * rh + (code * rl): one f16 rounding of the product, and 2^-22 of it
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                o[u][e] = hfma2(o[u][e], r[u].x, hmul2(o[u][e], r[u].y));
-                if (r[u].x == 0u) o[u][e] = 0u;         // unused places may hold anything
-              }
+              for (int e = 0; e < 8; ++e) o[u][e] = hfma2(o[u][e], r[u].x, hmul2(o[u][e], r[u].y));
             // two 16-byte chunks of the row's 64-column half; lanes of the second half store them in
             // the other order, so that a quarter-warp's stores fall on different banks
             const int half = ch >> 2, c0 = 2 * (ch & 3), f0 = half & 1;
@@ -789,16 +799,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int32_t from = lo - (ub + k) * kTile, to = hi - (ub + k) * kTile;
         const bool odd = wide || __any_sync(0xffffffffu, from > 0 || to < kTile);
         const float cc = wide ? 1.f : cq;
-        uint64_t sum[2] = {0, 0};
-        // moves the running maximum to `top` where it lags too far, `chunks` of this tile's weights being stored already
+        // moves the running maximum to `top`, `chunks` of this tile's weights being stored already
         auto move_max = [&](float top, int chunks) {
           const float mn = fmaxf(m, top);
           const float f = ex2(m - mn);
           m = mn;
           l *= f;
-          const uint64_t f2 = pack_u32x2(__float_as_uint(f), __float_as_uint(f));
-          sum[0] = mul_f32x2(sum[0], f2);
-          sum[1] = mul_f32x2(sum[1], f2);
           if (chunks > 0) {
             tmem_wait_st();
 #pragma unroll 1
@@ -885,59 +891,67 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             l += ws;
           }
         }
-        // ---- one pass, 64 columns at a time (a load takes some 30 cycles): key scales, the running maximum
-        // (moved when the chunk passes it by more than kLag), weights.  Few live registers: with a
-        // whole row in them the compiler had none left to overlap anything (2000 cycles a row against
-        // 700 for this arithmetic alone)
+        // ---- 64 columns at a time: key scales, weights by the maximum so far, their sum, and once more by the
+        // chunk's own maximum if that lagged too far.  A loop, and few live registers: with a whole row in them
+        // the compiler had none left to overlap anything, and the two chunks written out took 13% longer, the
+        // instruction cache being what four kinds of warps wait for most
         const uint64_t cc2 = pack_u32x2(__float_as_uint(cc), __float_as_uint(cc));
 #pragma unroll 1
         for (int g = 0; g < kTile / 64; ++g) {
-          uint32_t sr[2][32];
-          tmem_ld32(tS + 64 * g, sr[0]);
-          tmem_ld32(tS + 64 * g + 32, sr[1]);
-          tmem_wait_ld();
-          reg_fence32(sr[0]);
-          reg_fence32(sr[1]);
-          uint64_t y[32];
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          bool look = k == k0 && g == 0, sure = false;    // look for the maximum first; the weights fit
+          uint32_t nw[32];
+          float part;
+          while (true) {
+            if (__builtin_expect(look, 0)) {
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int g1 = 4 * g; g1 < 4 * g + 4; ++g1) {
+                uint32_t o[16];
+                tmem_ld16(tS + 16 * g1, o);
+                tmem_wait_ld();
+                reg_fence16(o);
+                const float* kr = reinterpret_cast<const float*>(ks2) + 16 * g1;
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const ulonglong2 kv = ks2[16 * g + e / 2];
-            const int c0 = 2 * e % 32;
-            y[e] = mul_f32x2(pack_u32x2(sr[e / 16][c0], sr[e / 16][c0 + 1]), kv.x);
-            y[e + 1] = mul_f32x2(pack_u32x2(sr[e / 16][c0 + 2], sr[e / 16][c0 + 3]), kv.y);
-          }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float e0, e1;
-            unpack_f32x2(y[e], e0, e1);
-            mx[e & 3] = max3(mx[e & 3], e0, e1);
-          }
-          const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), cc, lv);
-          if (__any_sync(0xffffffffu, top > m + kLag)) move_max(top, 2 * g);
-          const float off = lv - m + kLift;
-          const uint64_t off2 = pack_u32x2(__float_as_uint(off), __float_as_uint(off));
-          float w[64];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) unpack_f32x2(fma_f32x2(y[e], cc2, off2), w[2 * e], w[2 * e + 1]);
-#pragma unroll
-          for (int e = 0; e < 64; ++e) w[e] = ex2(w[e]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int j = 32 * h + 2 * e;
-              pk[e] = pack_f16x2(w[j], w[j + 1]);
-              sum[e & 1] = add_f32x2(sum[e & 1], pack_u32x2(__float_as_uint(w[j]), __float_as_uint(w[j + 1])));
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, __uint_as_float(o[e]) * kr[e]);
+              }
+              move_max(fmaf(top, cc, lv), 2 * g);
+              sure = true;
             }
-            tmem_st16(tS + 32 * g + 16 * h, pk);
+            uint32_t sr[2][32];
+            tmem_ld32(tS + 64 * g, sr[0]);
+            tmem_ld32(tS + 64 * g + 32, sr[1]);
+            tmem_wait_ld();
+            reg_fence32(sr[0]);
+            reg_fence32(sr[1]);
+            const float off = lv - m + kLift;
+            const uint64_t off2 = pack_u32x2(__float_as_uint(off), __float_as_uint(off));
+            float w[64];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const ulonglong2 kv = ks2[16 * g + e / 2];
+              const int c0 = 2 * e % 32;
+              const uint64_t y0 = mul_f32x2(pack_u32x2(sr[e / 16][c0], sr[e / 16][c0 + 1]), kv.x),
+                             y1 = mul_f32x2(pack_u32x2(sr[e / 16][c0 + 2], sr[e / 16][c0 + 3]), kv.y);
+              unpack_f32x2(fma_f32x2(y0, cc2, off2), w[2 * e], w[2 * e + 1]);
+              unpack_f32x2(fma_f32x2(y1, cc2, off2), w[2 * e + 2], w[2 * e + 3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 64; ++e) w[e] = ex2(w[e]);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              nw[e] = pack_f16x2(w[2 * e], w[2 * e + 1]);
+              sum[e & 1] = add_f32x2(sum[e & 1], pack_u32x2(__float_as_uint(w[2 * e]), __float_as_uint(w[2 * e + 1])));
+            }
+            float s0, s1;
+            unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
+            part = s0 + s1;
+            if (__builtin_expect(sure || __all_sync(0xffffffffu, part <= kMost), 1)) break;
+            look = true;
           }
-        }
-        if (!wide) {
-          float s0, s1;
-          unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
-          l = fmaf(s0 + s1, info.y, l);
+          if (!wide) l = fmaf(part, info.y, l);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) tmem_st16(tS + 32 * g + 16 * h, reinterpret_cast<const uint32_t(&)[16]>(nw[16 * h]));
         }
         tmem_wait_st();
         tc_fence_before();
