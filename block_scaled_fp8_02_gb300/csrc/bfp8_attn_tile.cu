@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const bool more = k + 1 < n;
             const int fs = static_cast<int>(q % kFStages), kn = static_cast<int>((q + 1) % kKStages);
             wait1(bFf + fs, ph(q, kFStages));
+            if (more) wait1(bKf + kn, ph(q + 1, kKStages));
 #pragma unroll 1
             for (int t = 0; t < 2; ++t) {
               if (!wait1(bP + t, q & 1)) break;
@@ -630,7 +631,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               pv(t, fs, k == 0);
               if (t == 1) mma_commit(bar(bFe + fs));
               if (more) {
-                if (t == 0 && !wait1(bKf + kn, ph(q + 1, kKStages))) break;
                 qk(t, kn);
                 mma_commit(bar(bS + t));
                 if (t == 1) mma_commit(bar(bKe + kn));
