@@ -25,6 +25,14 @@
 // of the softmax's time a row (800 cycles beside another warp) that was 140.  Where a tile's value scales
 // differ by more than 2^11 its tokens' own log2 scales join the exponents instead.
 //
+// A pair of 128 x 128 tiles (two query tiles over 128 tokens) takes 3600 cycles
+// against 2090 of the MMAs alone: a query tile's scores wait for its weights, which
+// stand in their place, so that its softmax (1630 cycles, and 480 until the last
+// of its four warps has finished) and its MMAs (1050) take turns, and the other
+// tile's turns fill what gaps they can.  4096 tokens of 64 / 8 heads of 128 at a
+// context of 16384: 1.73 ms, 1110 TFLOP/s (4 D flop a score; the queries' second
+// part not counted), 0.59 of the measured bf16 rate.
+//
 // As in the kernel for few rows, the tiles of all blocks form one line (with
 // kBlockCost places behind each block's for the time that a block costs besides)
 // that the persistent CTAs share equally; a block cut by a border leaves fp32 partial
@@ -50,15 +58,16 @@ constexpr int kTile = 128;                 // tokens of a tile, rows of a query 
 constexpr int kBlockRows = 2 * kTile;
 // 8 softmax warps, one for the MMAs, one for TMA and the tiles' scales, two that
 // convert V.  Three warpgroups and no more: the compiler plans for the registers
-// that a thread has at launch (168), and with 128 the softmax ran at half speed.
+// that a thread has at launch (168); with 128, and four warps converting, a chunk
+// took 11% longer.
 // 208 and 88 a thread after they are handed around.
 constexpr int kTileThreads = 384;
 constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpConv = 10, kConvWarps = 2;
-constexpr int kBlockCost = 8;              // (measured: a block's queries, first tiles, output 36000 cycles; a tile 4000)
+constexpr int kBlockCost = 8;              // (a block's queries, first tiles, output 20000-36000 cycles, a tile's pair 3600;
+                                           // 5 to 10 time alike, 12 is 3% slower on a mixed batch)
 constexpr int kSeqChunk = 2048;            // sequences whose tile counts are held at once
 constexpr int kKStages = 3, kVStages = 2, kFStages = 2, kScSlots = 4;
 constexpr float kNoMax = -3.0e38f;
-constexpr float kLag = 8.f;
 constexpr float kLift = 7.f;               // a weight at the running maximum is 2^7
 constexpr float kMost = 32768.f;           // sum of 64 weights up to which the maximum may lag: each fits f16
 constexpr int kVUp = 6;                    // values are scaled up by 2^6 in f16: 448 * 2^6 < 65504
@@ -121,13 +130,13 @@ __device__ __forceinline__ SeqBlocks seq_blocks(const AttnArgs& a, int b) {
 // Tokens [t0, t1) that some row of block rb sees, and its tiles.
 __device__ __forceinline__ int32_t block_tiles(const AttnArgs& a, const SeqBlocks& w, int rb, int32_t& t0,
                                                int32_t& t1) {
-  const int64_t r0 = static_cast<int64_t>(rb) * kBlockRows;
-  const int32_t i0 = static_cast<int32_t>(r0 / a.group);
-  int64_t i1 = (r0 + kBlockRows - 1) / a.group;
+  const uint32_t r0 = static_cast<uint32_t>(rb) * kBlockRows, group = static_cast<uint32_t>(a.group);   // < 2^32: 2^24 tokens, 128 heads
+  const int32_t i0 = static_cast<int32_t>(r0 / group);
+  int32_t i1 = static_cast<int32_t>((r0 + kBlockRows - 1) / group);
   if (i1 > w.q_len - 1) i1 = w.q_len - 1;
   int32_t lo, hi, x;
   seen_range(a, w.kv_len, w.pos0 + i0, lo, x);
-  seen_range(a, w.kv_len, w.pos0 + static_cast<int32_t>(i1), x, hi);
+  seen_range(a, w.kv_len, w.pos0 + i1, x, hi);
   t0 = lo;
   t1 = hi;
   return hi > lo ? (hi + kTile - 1) / kTile - lo / kTile : 1;
@@ -239,10 +248,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             bFe = bFf + kFStages, bRf = bFe + kFStages, bSf = bRf + kScSlots, bSe = bSf + kScSlots,
             bQ = bSe + kScSlots, bS = bQ + 2, bP = bS + 2, bO = bP + 2;
   __shared__ uint32_t s_tmem;
-  __shared__ int64_t s_before, s_total;
+  __shared__ int64_t s_item0, s_total;
   __shared__ int64_t s_u0, s_u1;                 // this CTA's share of the line of s_total tiles
   __shared__ int s_ctas;
-  __shared__ int s_b;
+  __shared__ int s_b, s_h, s_rb;                 // where the share begins
   __shared__ int s_last[2];
 
   if (tid == 0) {
@@ -324,6 +333,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int n = a.batch <= kSeqChunk ? a.batch : count_chunk(b0);
     if (warp == 0) {
       const int64_t u0 = s_u0;
+      int64_t mine = 0, first = 0;               // the sequence with u0: a head's places, its first place
+      int hit = -1;
       for (int i0 = 0; i0 < n; i0 += 32) {
         const int64_t own = i0 + lane < n ? cnt[i0 + lane] : 0;
         int64_t v = own;
@@ -333,11 +344,38 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (lane >= o) v += t;
         }
         const int64_t before = (run + v - own) * H;
-        if (own > 0 && before <= u0 && u0 < before + own * H) {
-          s_b = b0 + i0 + lane;
-          s_before = before;
+        const uint32_t here = __ballot_sync(0xffffffffu, own > 0 && before <= u0 && u0 < before + own * H);
+        if (here != 0u) {
+          const int at = __ffs(here) - 1;
+          hit = b0 + i0 + at;
+          mine = __shfl_sync(0xffffffffu, own, at);
+          first = __shfl_sync(0xffffffffu, before, at);
         }
         run += __shfl_sync(0xffffffffu, v, 31);
+      }
+      if (hit >= 0) {
+        // its head by a division, the head's block by adding up the blocks before it, 32 at a time (walking
+        // there block by block cost a chunk of 4096 tokens 160 us)
+        const SeqBlocks w = seq_blocks(a, hit);
+        const int h = static_cast<int>((u0 - first) / mine);
+        int64_t place = first + h * mine;
+        for (int rb0 = 0; rb0 < w.blocks; rb0 += 32) {
+          int32_t t0, t1;
+          const int64_t own = rb0 + lane < w.blocks ? block_tiles(a, w, rb0 + lane, t0, t1) + kBlockCost : 0;
+          int64_t v = own;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += t;
+          }
+          if (own > 0 && place + v - own <= u0 && u0 < place + v) {
+            s_b = hit;
+            s_h = h;
+            s_rb = rb0 + lane;
+            s_item0 = place + v - own;
+          }
+          place += __shfl_sync(0xffffffffu, v, 31);
+        }
       }
     }
     __syncthreads();
@@ -386,14 +424,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (lane == 0) {
       c.b = s_b;
       c.w = seq_blocks(a, c.b);
-      c.rb = 0;
-      c.h = 0;
-      c.item0 = s_before;
-      c.n = block_tiles(a, c.w, 0, c.t0, c.t1);
-      while (c.item0 + c.n + kBlockCost <= s_u0) {
-        c.item0 += c.n + kBlockCost;
-        step_block(c);
-      }
+      c.rb = s_rb;
+      c.h = s_h;
+      c.item0 = s_item0;
+      c.n = block_tiles(a, c.w, c.rb, c.t0, c.t1);
       more = clip(c) || advance(c);
     }
     more = __shfl_sync(0xffffffffu, more, 0);
@@ -875,7 +909,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tmem_wait_st();
           {
             // its weights are summed here, by the maximum that the pass below then need not move
-            if (__any_sync(0xffffffffu, top + lv > m + kLag)) move_max(top + lv, 0);
+            if (__any_sync(0xffffffffu, top + lv > m)) move_max(top + lv, 0);
             const float* iv = reinterpret_cast<const float*>(smem + C::kOffIv) + sl * kTile;
             const float off = lv - m + kLift;
             float ws = 0.f;

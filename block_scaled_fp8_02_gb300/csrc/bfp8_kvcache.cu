@@ -9,9 +9,10 @@
 // sums; places that do not fill a block of 256 threads share it with the next
 // tokens, those beyond it are the grid's second dimension.  Bound by memory:
 // write 2 bytes in and 1 + 4 / head_dim out an element (bf16), read the other
-// way round; reading 65536 tokens of 8 heads of 128 runs at 0.91 of the measured
-// HBM rate, writing is held up by the arithmetic that makes every code the
-// correctly rounded quotient's.
+// way round; reading 65536 tokens of 8 heads of 128 takes 65 us, 0.92 of the
+// measured copy rate, writing 8192 of them 16.6 us, 0.45 of it, held up by the
+// arithmetic that makes every code the correctly rounded quotient's (11 million
+// warp instructions, of which the two conversions a pair are the dearest).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
