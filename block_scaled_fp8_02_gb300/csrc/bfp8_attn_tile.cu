@@ -25,13 +25,14 @@
 // of the softmax's time a row (800 cycles beside another warp) that was 140.  Where a tile's value scales
 // differ by more than 2^11 its tokens' own log2 scales join the exponents instead.
 //
-// A pair of 128 x 128 tiles (two query tiles over 128 tokens) takes 3600 cycles
+// A pair of 128 x 128 tiles (two query tiles over 128 tokens) takes 3450 cycles
 // against 2090 of the MMAs alone: a query tile's scores wait for its weights, which
 // stand in their place, so that its softmax (1630 cycles, and 480 until the last
 // of its four warps has finished) and its MMAs (1050) take turns, and the other
 // tile's turns fill what gaps they can.  4096 tokens of 64 / 8 heads of 128 at a
-// context of 16384: 1.73 ms, 1110 TFLOP/s (4 D flop a score; the queries' second
-// part not counted), 0.59 of the measured bf16 rate.
+// context of 16384: 1.49 ms, 1290 TFLOP/s (4 D flop a score; the queries' second
+// part not counted), 0.68 of the measured bf16 rate.  A block costs 15000 cycles
+// besides (queries, first scores, output).
 //
 // As in the kernel for few rows, the tiles of all blocks form one line (with
 // kBlockCost places behind each block's for the time that a block costs besides)
@@ -63,7 +64,7 @@ constexpr int kBlockRows = 2 * kTile;
 // 208 and 88 a thread after they are handed around.
 constexpr int kTileThreads = 384;
 constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpConv = 10, kConvWarps = 2;
-constexpr int kBlockCost = 8;              // (a block's queries, first tiles, output 20000-36000 cycles, a tile's pair 3600;
+constexpr int kBlockCost = 8;              // (places of a block besides its tiles' pairs (3450 cycles): 15000 cycles, more where parts are joined;
                                            // 5 to 10 time alike, 12 is 3% slower on a mixed batch)
 constexpr int kSeqChunk = 2048;            // sequences whose tile counts are held at once
 constexpr int kKStages = 3, kVStages = 2, kFStages = 2, kScSlots = 4;
@@ -874,11 +875,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           // masked scores become -inf, in tensor memory
 #pragma unroll 1
           for (int g = 0; g < kTile / 32; ++g) {
+            const int32_t f = from - 32 * g, e1 = to - 32 * g;
+            if (!__any_sync(0xffffffffu, f > 0 || e1 < 32)) continue;
             uint32_t o[32];
             tmem_ld32(tS + 32 * g, o);
             tmem_wait_ld();
             reg_fence32(o);
-            const int32_t f = from - 32 * g, e1 = to - 32 * g;
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = e >= f && e < e1 ? o[e] : 0xFF800000u;
             tmem_st32(tS + 32 * g, o);
@@ -1058,30 +1060,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const float ref = best == -INFINITY ? 0.f : best;
           float sum = 0.f;
 #pragma unroll 1
-          for (int g = 0; g < D / 32; ++g) {
-            float o[32];
+          for (int g = 0; g < D / 64; ++g) {         // 64 columns' loads in flight
+            float o[64];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            for (int e = 0; e < 64; ++e) o[e] = 0.f;
             sum = 0.f;
+#pragma unroll 1
             for (int cta = c_first; cta <= c_last; ++cta) {
               const float* src = slot_of(cta);
               const float w = ex2(__ldcg(src + kBlockRows * D + t * kTile + r) - ref);
               sum += w;
+              float4 v[16];
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                    src + ((t * (D / 4) + 8 * g + e / 4) * kTile + r) * 4));
-                o[e] = fmaf(v.x, w, o[e]);
-                o[e + 1] = fmaf(v.y, w, o[e + 1]);
-                o[e + 2] = fmaf(v.z, w, o[e + 2]);
-                o[e + 3] = fmaf(v.w, w, o[e + 3]);
+              for (int e = 0; e < 16; ++e)
+                v[e] = __ldcg(reinterpret_cast<const float4*>(src + ((t * (D / 4) + 16 * g + e) * kTile + r) * 4));
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                o[4 * e] = fmaf(v[e].x, w, o[4 * e]);
+                o[4 * e + 1] = fmaf(v[e].y, w, o[4 * e + 1]);
+                o[4 * e + 2] = fmaf(v[e].z, w, o[4 * e + 2]);
+                o[4 * e + 3] = fmaf(v[e].w, w, o[4 * e + 3]);
               }
             }
             const float is = sum > 0.f ? 1.f / sum : 0.f;
             if (live && ok) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                st_global_v4(dst + 32 * g + e, pack_bf16x2(o[e] * is, o[e + 1] * is),
+              for (int e = 0; e < 64; e += 8)
+                st_global_v4(dst + 64 * g + e, pack_bf16x2(o[e] * is, o[e + 1] * is),
                              pack_bf16x2(o[e + 2] * is, o[e + 3] * is), pack_bf16x2(o[e + 4] * is, o[e + 5] * is),
                              pack_bf16x2(o[e + 6] * is, o[e + 7] * is));
             }
