@@ -148,13 +148,17 @@ extern "C" bfp8_status bfp8_paged_attention(const bfp8_attention_args* p, const 
   int32_t* counters = static_cast<int32_t*>(workspace);
   char* partials = static_cast<char*>(workspace) + kCounterHeaderBytes;
   cudaError_t e = cudaSuccess;
-  if (a.group <= kFewRows)
-    e = launch_attn_decode(mk, mv, a, groups, sms, counters, reinterpret_cast<float*>(partials), cs);
-  else
-    a.few_rows = 0;
-  if (e == cudaSuccess && has_many(a.group, p->max_q_len))
+  // Can a sequence be short enough for the kernel for few rows?  Not if the others at their longest leave this
+  // one too many tokens (always so for a single chunk): then its launch is saved.
+  const bool many = has_many(a.group, p->max_q_len);
+  const bool few = a.group <= kFewRows &&
+                   (!many || p->total_q <= static_cast<int64_t>(p->batch - 1) * p->max_q_len + a.few_rows / a.group);
+  if (!few) a.few_rows = 0;
+  if (many)
     e = launch_attn_tile(mk, mv, a, sms, counters + sms,
                          reinterpret_cast<float*>(partials + few_bytes(a.group, a.c.dim, p->max_q_len, sms)), cs);
+  if (e == cudaSuccess && few)
+    e = launch_attn_decode(mk, mv, a, groups, sms, counters, reinterpret_cast<float*>(partials), many, cs);
   if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
   return set_last_error(BFP8_OK, "");
 }

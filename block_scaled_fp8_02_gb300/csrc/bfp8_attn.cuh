@@ -79,10 +79,11 @@ __device__ __forceinline__ int share_of(int64_t u, int64_t total, int64_t ctas) 
 // The kernel for few rows a sequence (bfp8_attn_decode.cu): `groups` (1, 2 or 4)
 // eights of rows, `ctas` persistent CTAs, counters[ctas] zero.
 // k, v: tensor maps [dim, token, head, page] of bytes, boxes of min(page_size, 128) tokens.
+// behind: the launch before it in the stream is launch_attn_tile's of the same call; the two run beside each other.
 int attn_decode_groups(int64_t rows);
 size_t attn_decode_partial_bytes(int groups, int dim, int ctas);
 cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int groups, int ctas,
-                               int32_t* counters, float* partials, cudaStream_t stream);
+                               int32_t* counters, float* partials, bool behind, cudaStream_t stream);
 
 // The kernel for more rows (bfp8_attn_tile.cu); counters[2 * ctas] zero.
 size_t attn_tile_partial_bytes(int dim, int ctas);

@@ -177,6 +177,7 @@ struct DecodeArgs {
   int32_t* counters;          // one a CTA, zero between calls
   float* partials;            // two slots a CTA: NG * 8 rows of D floats, then their log2 sums
   unsigned long long wait_limit;
+  int32_t behind;             // launched right behind the other kernel, for the same call
 };
 
 template <int D, int NG>
@@ -204,7 +205,9 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
     fence_barrier_init();
   }
   griddep_launch_dependents();
-  griddep_wait();
+  // Behind the other kernel this one starts once all of its CTAs have passed their wait, on what SMs it leaves,
+  // needs nothing of it and only must not be done before it.
+  if (!p.behind) griddep_wait();
 
   // ---- this CTA's share [u0, u1) of the line of units, and where it starts
   __shared__ int64_t part[C::kThreads / 32];
@@ -224,7 +227,10 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
   }
   const int64_t total = run * H;
   const int64_t ctas = total < gridDim.x ? total : gridDim.x;
-  if (blockIdx.x >= ctas) return;                      // whole CTA: nothing is in flight yet
+  if (blockIdx.x >= ctas) {                            // whole CTA: nothing is in flight yet
+    if (p.behind) griddep_wait();
+    return;
+  }
   const int64_t u0 = share_begin(blockIdx.x, total, ctas), u1 = share_begin(blockIdx.x + 1, total, ctas);
   auto locate = [&](int b, int64_t incl, int32_t n) {
     if (n > 0 && (incl - n) * H <= u0 && u0 < incl * H) {
@@ -792,6 +798,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
     }
     c = nx;
   }
+  if (p.behind) griddep_wait();
 }
 
 template <int D, int NG>
@@ -823,12 +830,13 @@ size_t attn_decode_partial_bytes(int groups, int dim, int ctas) {
 }
 
 cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int groups, int ctas,
-                               int32_t* counters, float* partials, cudaStream_t stream) {
+                               int32_t* counters, float* partials, bool behind, cudaStream_t stream) {
   DecodeArgs p;
   p.a = a;
   p.counters = counters;
   p.partials = partials;
   p.wait_limit = 1ull << 31;
+  p.behind = behind;
   if (a.c.dim == 128) {
     switch (groups) {
       case 1: return launch_decode_ng<128, 1>(k, v, p, ctas, stream);

@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     fence_barrier_init();
   }
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();                  // after the wait: what starts behind this needs no wait of its own
 
   // ---- this CTA's share of the line of tiles: the tiles of each sequence and
   // kv head, a warp a sequence, in the operands' space; then one warp adds up
