@@ -249,10 +249,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             bFe = bFf + kFStages, bRf = bFe + kFStages, bSf = bRf + kScSlots, bSe = bSf + kScSlots,
             bQ = bSe + kScSlots, bS = bQ + 2, bP = bS + 2, bO = bP + 2;
   __shared__ uint32_t s_tmem;
-  __shared__ int64_t s_item0, s_total;
+  __shared__ int64_t s_total;
   __shared__ int64_t s_u0, s_u1;                 // this CTA's share of the line of s_total tiles
   __shared__ int s_ctas;
-  __shared__ int s_b, s_h, s_rb;                 // where the share begins
+  __shared__ Cursor s_first;                     // the block in which the share begins
   __shared__ int s_last[2];
 
   if (tid == 0) {
@@ -284,6 +284,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   griddep_wait();
   griddep_launch_dependents();                  // after the wait: what starts behind this needs no wait of its own
 
+  // the page table is looked at once the share is known: into the cache with it (no more than a line a thread)
+  {
+    const int64_t at = static_cast<int64_t>(tid) * 32;
+    if (at < static_cast<int64_t>(a.batch - 1) * a.ld_table + 1)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table + at));
+  }
   // ---- this CTA's share of the line of tiles: the tiles of each sequence and
   // kv head, a warp a sequence, in the operands' space; then one warp adds up
   int64_t* cnt = reinterpret_cast<int64_t*>(smem);
@@ -361,7 +367,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int h = static_cast<int>((u0 - first) / mine);
         int64_t place = first + h * mine;
         for (int rb0 = 0; rb0 < w.blocks; rb0 += 32) {
-          int32_t t0, t1;
+          int32_t t0 = 0, t1 = 0;
           const int64_t own = rb0 + lane < w.blocks ? block_tiles(a, w, rb0 + lane, t0, t1) + kBlockCost : 0;
           int64_t v = own;
 #pragma unroll
@@ -370,10 +376,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (lane >= o) v += t;
           }
           if (own > 0 && place + v - own <= u0 && u0 < place + v) {
-            s_b = hit;
-            s_h = h;
-            s_rb = rb0 + lane;
-            s_item0 = place + v - own;
+            s_first.item0 = place + v - own;
+            s_first.w = w;
+            s_first.b = hit;
+            s_first.h = h;
+            s_first.rb = rb0 + lane;
+            s_first.n = static_cast<int32_t>(own) - kBlockCost;
+            s_first.t0 = t0;
+            s_first.t1 = t1;
           }
           place += __shfl_sync(0xffffffffu, v, 31);
         }
@@ -423,12 +433,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto start = [&]() -> bool {
     int more = 0;
     if (lane == 0) {
-      c.b = s_b;
-      c.w = seq_blocks(a, c.b);
-      c.rb = s_rb;
-      c.h = s_h;
-      c.item0 = s_item0;
-      c.n = block_tiles(a, c.w, c.rb, c.t0, c.t1);
+      c = s_first;
       more = clip(c) || advance(c);
     }
     more = __shfl_sync(0xffffffffu, more, 0);
@@ -577,7 +582,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           ++q;                                          // its copies are in flight
           if (pending) scales(q - 2, p_tok, p_t0, p_t1);
-          pending = 1;
+          pending = q > 1;
           p_tok = tok;
           p_t0 = t0;
           p_t1 = t1;
@@ -595,6 +600,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (live)
             tma_load_4d(sbase + static_cast<uint32_t>(C::kOffV + vs * C::kK + lane * box * D), &tmV, bar(bVf + vs), 0,
                         off, h, pg);
+          if (q == 1) scales(0, tok, t0, t1);           // the first tile's are waited for
         }
       }
       if (pending) scales(q - 1, p_tok, p_t0, p_t1);
