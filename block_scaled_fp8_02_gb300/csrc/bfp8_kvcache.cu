@@ -10,7 +10,7 @@
 // tokens, those beyond it are the grid's second dimension.  Bound by memory:
 // write 2 bytes in and 1 + 4 / head_dim out an element (bf16), read the other
 // way round; reading 65536 tokens of 8 heads of 128 takes 65 us, 0.92 of the
-// measured copy rate, writing 8192 of them 16.6 us, 0.45 of it, held up by the
+// measured copy rate, writing 8192 of them 15.6 us, 0.48 of it, held up by the
 // arithmetic that makes every code the correctly rounded quotient's (11 million
 // warp instructions, of which the two conversions a pair are the dearest).
 #include <cuda_bf16.h>
@@ -29,10 +29,11 @@ namespace bfp8 {
 namespace {
 
 constexpr int kThreads = 256;
-// Tokens of a thread whose loads are issued together, with four blocks a SM
-// resident: writing 8192 tokens of 8 heads of 128, 16.8 us with two against 18.9
-// with four on three blocks; reading 65536, 65.7 with four against 78.1 with two.
-constexpr int kWriteTokens = 2, kReadTokens = 4, kBlocksPerSm = 4;
+// Tokens that a reading thread's loads are issued for together, with four blocks a SM
+// resident: 65536 tokens of 8 heads of 128, 65.1 us with four against 78.1 with
+// two.  Writing takes one at a time: 8192 tokens 15.6 us against 16.6 with two (and 18.9
+// with four), 16.5 with five blocks; there the arithmetic is what counts.
+constexpr int kReadTokens = 4, kBlocksPerSm = 4;
 
 // The places of a token: nkv x heads x (dim / 16), shared out as above.
 struct Places {
@@ -70,35 +71,27 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv_write_kernel(const 
   const int64_t step = static_cast<int64_t>(gridDim.x) * a.pl.tokens;
   griddep_launch_dependents();
   griddep_wait();
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.pl.tokens; t0 < a.T; t0 += step * kWriteTokens) {
-    Raw8<kF32> x[kWriteTokens][2];
-    int64_t slot[kWriteTokens];
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.pl.tokens; t0 < a.T; t0 += step) {
+    const int64_t t = t0 + ti;
+    const bool ok = mine && t < a.T;
+    const int64_t slot = ok ? __ldg(a.slots + t) : -1;
+    Raw8<kF32> x[2];
 #pragma unroll
-    for (int u = 0; u < kWriteTokens; ++u) {
-      const int64_t t = t0 + u * step + ti;
-      const bool ok = mine && t < a.T;
-      slot[u] = ok ? __ldg(a.slots + t) : -1;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) x[u][i].load(src + (ok ? t : 0) * st + 8 * i, a.vec, ok ? 8 : 0);
+    for (int i = 0; i < 2; ++i) x[i].load(src + (ok ? t : 0) * st + 8 * i, a.vec, ok ? 8 : 0);
+    float v[16];
+    x[0].get(reinterpret_cast<float(&)[8]>(v[0]));
+    x[1].get(reinterpret_cast<float(&)[8]>(v[8]));
+    float scale;
+    uint32_t w[4];
+    quant16<LPR, kUe8m0>(v, scale, w);
+    if (slot < 0) continue;
+    if (slot >= nslots) {
+      report_failure(a.err, kDevBadCacheIndex);
+      continue;
     }
-#pragma unroll
-    for (int u = 0; u < kWriteTokens; ++u) {
-      if (t0 + u * step >= a.T) break;                // whole blocks
-      float v[16];
-      x[u][0].get(reinterpret_cast<float(&)[8]>(v[0]));
-      x[u][1].get(reinterpret_cast<float(&)[8]>(v[8]));
-      float scale;
-      uint32_t w[4];
-      quant16<LPR, kUe8m0>(v, scale, w);
-      if (slot[u] < 0) continue;
-      if (slot[u] >= nslots) {
-        report_failure(a.err, kDevBadCacheIndex);
-        continue;
-      }
-      const int64_t page = slot[u] >> a.c.page_shift, o = slot[u] & (a.c.page_size - 1);
-      *reinterpret_cast<uint4*>(q + page * a.c.st_page + o * a.c.st_tok) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (li == 0) s[page * a.c.ss_page + o] = scale;
-    }
+    const int64_t page = slot >> a.c.page_shift, o = slot & (a.c.page_size - 1);
+    *reinterpret_cast<uint4*>(q + page * a.c.st_page + o * a.c.st_tok) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (li == 0) s[page * a.c.ss_page + o] = scale;
   }
 }
 
