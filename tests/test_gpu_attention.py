@@ -272,3 +272,23 @@ def test_one_weight_beside_a_long_tail(dev):
                                            torch.tensor([0, m], dtype=torch.int32, device=dev),
                                            torch.tensor([n], dtype=torch.int32, device=dev), m, n, return_lse=True)
         check_attention(out, lse, attention_ref(q, kq, vq, ks, vs, table, [0, m], [n], D ** -0.5))
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,max_q", [([40, 40], [90, 300], None), ([40, 39, 1], [300, 90, 77], None),
+                                                  ([40], [300], 64), ([1, 40, 0], [500, 41, 9], 200), ([2, 5], [9, 300], None)])
+@pytest.mark.parametrize("Hq,H", [(8, 1), (6, 2), (33, 1)])
+def test_batches_that_may_or_may_not_hold_short_sequences(dev, q_lens, kv_lens, max_q, Hq, H):
+    """From batches whose token count leaves no room for a short sequence to ones with nothing else."""
+    _run(dev, q_lens, kv_lens, Hq, H, 64, 16, max_q=max_q)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,window", [([1200], [1300], 0), ([1, 1100, 60], [400, 1100, 700], 0),
+                                                   ([1150, 1, 1], [1500, 900, 2], 300)])
+def test_more_blocks_than_lanes(dev, q_lens, kv_lens, window):
+    """A head's blocks of 256 rows pass 32: shares begin anywhere among them."""
+    _run(dev, q_lens, kv_lens, 8, 1, 64, 32, window=window)
+
+
+def test_more_sequences_than_are_counted_at_once(dev):
+    n = 2060
+    _run(dev, [2] * n, [2 + i % 5 for i in range(n)], 17, 1, 64, 16)
