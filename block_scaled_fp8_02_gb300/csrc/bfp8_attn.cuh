@@ -76,7 +76,7 @@ __device__ __forceinline__ int share_of(int64_t u, int64_t total, int64_t ctas) 
   return static_cast<int>(((u + 1) * ctas - 1) / total);
 }
 
-// The kernel for few rows a sequence (bfp8_attn_decode.cu): `groups` (1, 2 or 4)
+// The kernel for few rows a sequence (bfp8_attn_decode.cu): `groups` (1 to 4)
 // eights of rows, `ctas` persistent CTAs, counters[ctas] zero.
 // k, v: tensor maps [dim, token, head, page] of bytes, boxes of min(page_size, 128) tokens.
 // behind: the launch before it in the stream is launch_attn_tile's of the same call; the two run beside each other.

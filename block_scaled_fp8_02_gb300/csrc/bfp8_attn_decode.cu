@@ -12,7 +12,7 @@
 //
 // A producer warp streams units through TMA (tensor-map boxes of one page and
 // head, 128-byte swizzle, and the pages' scales by bulk copies) into a ring.
-// Teams of four warps take units in turn, 32 tokens a warp; each warp keeps its
+// Teams of four warps take units in turn (or, past 16 rows, share the rows), 32 tokens a warp; each warp keeps its
 // own running maximum, sum and output.  The tokens are the 16-row operand of
 // mma.sync.m16n8k16 (f16, fp32 sums) and the query rows its 8 columns:
 //   S^T [16 tokens x 8 rows] = K Q^T,    O^T [D x 8 rows] += V^T P^T.
@@ -62,23 +62,25 @@ constexpr float kNoMax = -3.0e38f;         // running maximum before any token
 constexpr float kLag = 8.f;                // how far scores may exceed the running maximum
 constexpr float kLift = 7.f;               // weighted values are 2^(x + log2 vs - mv + kLift) <= 2^15
 
-template <int D, int NG>
+template <int D, int NG, int RT>
 struct DecCfg {
   static constexpr int kCodes = kUnit * D;                 // K or V of a unit
   static constexpr int kStageBytes = 2 * kCodes;
   static constexpr int kScaleFloats = 2 * kUnit;
   static constexpr int kStages = D == 128 ? 6 : 12;
-  // Consumers: groups of four warps that take units in turn, 32 tokens a warp, as two chains of 16
-  // where the registers allow it.  A fourth warpgroup (its first warp) produces; registers are handed
-  // to the consumers (launch: 128 or 168 a thread).
+  // Consumers: teams of four warps, 32 tokens a warp, as two chains of 16.  Up to 16 rows (NG eights of
+  // them in a warp) the teams take units in turn (RT = 1); more rows than a warp's registers hold are shared out
+  // and RT teams work on every unit (one warp with 32 rows spilled: 16 sequences of 4 tokens at 8192,
+  // 64 / 8 heads of 128, took 167 us against 103).  The last warpgroup's first warp produces; registers are handed to the consumers
+  // (launch: 128 or 168 a thread).
   static constexpr int kWarps = NG == 1 ? 12 : 8;
   static constexpr int kGroups = kWarps / 4;
   static constexpr int kThreads = (kWarps + 4) * 32;
   static constexpr int kRegs = NG == 1 ? 152 : 224, kRegsProducer = 56;
-  static constexpr int kAtOnce = NG <= 2 ? 2 : 1;
   // a slot always belongs to the same team, which waits for each of its phases in turn: a wait by parity
   // cannot tell a phase from the one two further on
-  static_assert(kStages % kGroups == 0, "slots belong to teams");
+  static_assert(kStages % kGroups == 0 && (RT == 1 || RT == kGroups), "slots belong to teams, or to all");
+  static constexpr int kParts = RT == 1 ? kWarps : 4;      // warps whose parts make up a row
   static constexpr int kPitch = D + 4;                     // floats of a row of partials
   static constexpr int kJoin = 4;                          // rows whose warps' parts are joined at once
   static constexpr int kOffScale = kStages * kStageBytes;
@@ -180,12 +182,12 @@ struct DecodeArgs {
   int32_t behind;             // launched right behind the other kernel, for the same call
 };
 
-template <int D, int NG>
-__global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
+template <int D, int NG, int RT>
+__global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ DecodeArgs p) {
-  using C = DecCfg<D, NG>;
-  constexpr int kRows = NG * 8;
+  using C = DecCfg<D, NG, RT>;
+  constexpr int kRows = NG * 8 * RT;
   const AttnArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
   // aligned by an offset: the compiler has to see that this is shared memory
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), 4);
+      mbar_init(bar_empty(s), 4 * RT);
     }
     fence_barrier_init();
   }
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
   // ------------------------------------------------------------- consumers
   setmaxnreg_inc<C::kRegs>();
   const int team = warp >> 2, wq = warp & 3;         // units team, team + kGroups .. ; 32 tokens of each
+  const int row0 = RT == 1 ? 0 : team * 8 * NG;      // first row of this team
   const int g = lane >> 2, t = lane & 3;
   const int pg = slot_token<D>(g);
   // value chunk and tokens of this lane
@@ -380,12 +383,12 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
   __shared__ int s_last;
   bool ok = true;
   uint32_t q = 0;
-  // the rows grp * 8 + g of an item's queries, this lane's elements; fetched while the item before ends
+  // the rows row0 + grp * 8 + g of an item's queries, this lane's elements; fetched while the item before ends
   uint4 raw[NG][KC][2];
   auto fetch = [&](const Cursor& c) {
 #pragma unroll
     for (int grp = 0; grp < NG; ++grp) {
-      const int r = grp * 8 + g, i = r / a.group;
+      const int r = row0 + grp * 8 + g, i = r / a.group;
       const uint4* src = reinterpret_cast<const uint4*>(a.q + (c.w.row0 + i) * a.q_st +
                                                         (c.h * a.group + r - i * a.group) * a.q_sh + 16 * t);
 #pragma unroll
@@ -398,15 +401,13 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
       }
     }
   };
-  constexpr bool kAhead = NG <= 2;           // (no registers left for it otherwise)
   Cursor c;
   bool more = start(c);
-  if (more && kAhead) fetch(c);
+  if (more) fetch(c);
   while (more) {
     const SeqWork w = c.w;
     const int rows = w.q_len * a.group;
-    if (!kAhead) fetch(c);
-    // ---- queries: rows grp * 8 + g, f16 after scaling by a power of two
+    // ---- queries: rows row0 + grp * 8 + g, f16 after scaling by a power of two
     uint32_t qf[NG][KC * 4][2];
     float cq[NG][2];
 #pragma unroll
@@ -459,16 +460,16 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
       for (int j = 0; j < DT; ++j) acc[grp][j][0] = acc[grp][j][1] = acc[grp][j][2] = acc[grp][j][3] = 0.f;
     }
     const int32_t ub = w.t0 / kUnit;
-    // NU times 16 tokens from `first` of this warp's 32 of a unit, whose chains of dependent steps overlap
-    auto process = [&](auto nu, int32_t k, int first) {
-      constexpr int NU = decltype(nu)::value;
+    // this warp's 32 tokens of a unit as NU times 16, whose chains of dependent steps overlap
+    auto process = [&](int32_t k) {
+      constexpr int NU = 2;
       int32_t base[NU];
       const uint8_t *kst[NU], *vst[NU];
       float ks[NU][2], lv[NU][2];
       bool edge = false;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        const int slot = static_cast<int>(q % C::kStages), at = wq * 32 + first + 16 * u;
+        const int slot = static_cast<int>(q % C::kStages), at = wq * 32 + 16 * u;
         base[u] = (ub + k) * kUnit + at;
         kst[u] = smem + slot * C::kStageBytes + at * D;
         vst[u] = kst[u] + C::kCodes;
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
           for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int r = grp * 8 + 2 * t + e;
+              const int r = row0 + grp * 8 + 2 * t + e;
               int32_t lo, hi;
               seen_range(a, w.kv_len, w.pos0 + r / a.group, lo, hi);
               if (j0 < lo || j0 >= hi) s[u][grp][e] = -INFINITY;
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
           }
     };
     for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
-      if (static_cast<int>(q % C::kGroups) != team) continue;
+      if (RT == 1 && static_cast<int>(q % C::kGroups) != team) continue;
       const int slot = static_cast<int>(q % C::kStages);
       if (ok) {
         const bool in = mbar_wait_bounded(bar_full(slot), (q / C::kStages) & 1u, p.wait_limit);
@@ -644,13 +645,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
       }
       const int32_t base = (ub + k) * kUnit + wq * 32;
       if (ok && base < w.t1 && base + 32 > w.t0) {
-        if constexpr (C::kAtOnce == 2) {
-          process(std::integral_constant<int, 2>{}, k, 0);
-        } else {
-#pragma unroll 1
-          for (int first = 0; first < 32; first += 16)
-            if (base + first < w.t1 && base + first + 16 > w.t0) process(std::integral_constant<int, 1>{}, k, first);
-        }
+        process(k);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_empty(slot));
@@ -658,7 +653,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
 
     Cursor nx = c;
     more = next(nx);
-    if (more && kAhead) fetch(nx);
+    if (more) fetch(nx);
 
     // ---- the warps' parts of the item, added in warp order, four rows at a time
     const bool whole = c.k0 == 0 && c.k1 == w.units;
@@ -692,16 +687,18 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
         }
       }
       named_bar_sync(1, C::kWarps * 32);
-      const int r = part4 * C::kJoin + warp;               // warp w finishes row w of the four
-      if (warp < C::kJoin && r < rows) {
+      // warp w (of a team with its own rows: of its own) finishes row w of the four
+      const int w4 = RT == 1 ? warp : wq, w0 = RT == 1 ? 0 : team * 4;
+      const int r = row0 + part4 * C::kJoin + w4;
+      if (w4 < C::kJoin && r < rows) {
         float top = kNoMax, sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < C::kWarps; ++i) top = fmaxf(top, red_m[i * C::kJoin + warp]);
-        float f[C::kWarps];
+        for (int i = 0; i < C::kParts; ++i) top = fmaxf(top, red_m[(w0 + i) * C::kJoin + w4]);
+        float f[C::kParts];
 #pragma unroll
-        for (int i = 0; i < C::kWarps; ++i) {
-          f[i] = ex2(red_m[i * C::kJoin + warp] - top);
-          sum += red_l[i * C::kJoin + warp] * f[i];
+        for (int i = 0; i < C::kParts; ++i) {
+          f[i] = ex2(red_m[(w0 + i) * C::kJoin + w4] - top);
+          sum += red_l[(w0 + i) * C::kJoin + w4] * f[i];
         }
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const float lse2 = sum > 0.f ? top + log2f(sum) : -INFINITY;
@@ -709,9 +706,9 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < C::kWarps; ++i) {
-          const float ci = ex2(red_v[i * C::kJoin + warp] - kLift - top) * inv;
-          const float* src = red + (i * C::kJoin + warp) * C::kPitch + lane * (D / 32);
+        for (int i = 0; i < C::kParts; ++i) {
+          const float ci = ex2(red_v[(w0 + i) * C::kJoin + w4] - kLift - top) * inv;
+          const float* src = red + ((w0 + i) * C::kJoin + w4) * C::kPitch + lane * (D / 32);
 #pragma unroll
           for (int e = 0; e < D / 32; ++e) o[e] = fmaf(src[e], ci, o[e]);
         }
@@ -801,11 +798,11 @@ __global__ void __launch_bounds__((DecCfg<D, NG>::kThreads), 1)
   if (p.behind) griddep_wait();
 }
 
-template <int D, int NG>
+template <int D, int NG, int RT>
 cudaError_t launch_decode_ng(const CUtensorMap& k, const CUtensorMap& v, const DecodeArgs& p, int ctas,
                              cudaStream_t stream) {
-  using C = DecCfg<D, NG>;
-  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using C = DecCfg<D, NG, RT>;
+  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NG, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -818,12 +815,12 @@ cudaError_t launch_decode_ng(const CUtensorMap& k, const CUtensorMap& v, const D
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, NG>, k, v, p);
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, NG, RT>, k, v, p);
 }
 
 }  // namespace
 
-int attn_decode_groups(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+int attn_decode_groups(int64_t rows) { return rows <= 32 ? static_cast<int>((rows + 7) / 8) : 4; }
 
 size_t attn_decode_partial_bytes(int groups, int dim, int ctas) {
   return static_cast<size_t>(2) * ctas * groups * 8 * (dim + 1) * sizeof(float);
@@ -839,15 +836,17 @@ cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const
   p.behind = behind;
   if (a.c.dim == 128) {
     switch (groups) {
-      case 1: return launch_decode_ng<128, 1>(k, v, p, ctas, stream);
-      case 2: return launch_decode_ng<128, 2>(k, v, p, ctas, stream);
-      default: return launch_decode_ng<128, 4>(k, v, p, ctas, stream);
+      case 1: return launch_decode_ng<128, 1, 1>(k, v, p, ctas, stream);
+      case 2: return launch_decode_ng<128, 2, 1>(k, v, p, ctas, stream);
+      case 3: return launch_decode_ng<128, 1, 3>(k, v, p, ctas, stream);
+      default: return launch_decode_ng<128, 2, 2>(k, v, p, ctas, stream);
     }
   }
   switch (groups) {
-    case 1: return launch_decode_ng<64, 1>(k, v, p, ctas, stream);
-    case 2: return launch_decode_ng<64, 2>(k, v, p, ctas, stream);
-    default: return launch_decode_ng<64, 4>(k, v, p, ctas, stream);
+    case 1: return launch_decode_ng<64, 1, 1>(k, v, p, ctas, stream);
+    case 2: return launch_decode_ng<64, 2, 1>(k, v, p, ctas, stream);
+    case 3: return launch_decode_ng<64, 1, 3>(k, v, p, ctas, stream);
+    default: return launch_decode_ng<64, 2, 2>(k, v, p, ctas, stream);
   }
 }
 

@@ -22,7 +22,7 @@ bfp8_status set_last_errorf(bfp8_status st, const char* fmt, ...);
 // The current device if it is one the library runs on: its SM count and the
 // address of its failure word.
 bfp8_status device_for_call(int* sms, int** err);
-// The driver's tensor-map encoder (tiled, 128- or 64-byte swizzle by
+// The CUDA driver's tensor-map encoder (tiled, 128- or 64-byte swizzle by
 // `swizzle_bytes`, zero fill): `rank` dims of bytes, strides of dims 1.. in
 // bytes.
 bfp8_status encode_bytes_tiled(CUtensorMap* map, const void* ptr, int rank, const uint64_t* dims,
