@@ -201,7 +201,7 @@ cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t stream) {
                           : rmsnorm_quant_long_kernel<kF32, kUe8m0>;
   // as many blocks as are resident, asked for once a kernel and size
   static std::atomic<int> resident[4][33];
-  std::atomic<int>& known = resident[nc / 2 + (nc == 4)][threads / 32];
+  std::atomic<int>& known = resident[nc == 4 ? 3 : nc][threads / 32];
   int per_sm = known.load(std::memory_order_relaxed);
   if (per_sm == 0) {
     const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
