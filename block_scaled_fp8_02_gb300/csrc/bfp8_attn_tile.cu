@@ -940,7 +940,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tmem_wait_st();
           {
             // its weights are summed here, by the maximum that the pass below then need not move
-            if (__any_sync(0xffffffffu, top + lv > m)) move_max(top + lv, 0);
+            if (__any_sync(0xffffffffu, live && top + lv > m)) move_max(top + lv, 0);
             const float* iv = reinterpret_cast<const float*>(smem + C::kOffIv) + sl * kTile;
             const float off = lv - m + kLift;
             float ws = 0.f;
@@ -1011,7 +1011,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             float s0, s1;
             unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
             part = s0 + s1;
-            if (__builtin_expect(sure || __all_sync(0xffffffffu, part <= kMost), 1)) break;
+            // (rows past the last token see whatever unused places hold: they have no say, or that would show in the
+            // others' roundings)
+            if (__builtin_expect(sure || __all_sync(0xffffffffu, !live || part <= kMost), 1)) break;
             look = true;
           }
           if (!wide) l = fmaf(part, info.y, l);

@@ -292,3 +292,32 @@ def test_more_blocks_than_lanes(dev, q_lens, kv_lens, window):
 def test_more_sequences_than_are_counted_at_once(dev):
     n = 2060
     _run(dev, [2] * n, [2 + i % 5 for i in range(n)], 17, 1, 64, 16)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_other_sequences_nans_leave_no_trace(dev, D):
+    """Every other sequence's keys are NaN: the rest come out bit for bit as beside ordinary ones, although their last
+    tiles are not full and their row blocks have rows to spare, which see what the tiles before left there."""
+    n, page, g = 600, 16, torch.Generator().manual_seed(5)      # (pages end inside a tile's halves)
+    kv_lens = [256 if i % 2 == 0 else 168 for i in range(n)]
+    pages = sum((m + page - 1) // page for m in kv_lens)
+    kq, ks, vq, vs = make_cache(pages, 1, page, D, g, 0.5)
+    table = torch.zeros(n, 16, dtype=torch.int32)
+    at = 0
+    spoilt = kq.view(torch.uint8).clone()
+    for i, m in enumerate(kv_lens):
+        c = (m + page - 1) // page
+        table[i, :c] = torch.arange(at, at + c)
+        if i % 2 == 0:
+            spoilt[at:at + c] = 0x7F
+        at += c
+    q = torch.randn(n * 5, 8, D, generator=g).bfloat16().to(dev)
+    cu = (torch.arange(n + 1) * 5).int().to(dev)
+    outs = []
+    for codes in (kq, spoilt.view(torch.float8_e4m3fn)):
+        cache = bf.KVCache(codes.to(dev), vq.to(dev), ks.to(dev), vs.to(dev))
+        out, lse = bf.bfp8_paged_attention(q, cache, table.to(dev), cu, torch.tensor(kv_lens, dtype=torch.int32, device=dev),
+                                           5, 256, return_lse=True)
+        outs.append((out.view(n, 5, 8, D)[1::2], lse.view(n, 5, 8)[1::2]))
+    assert torch.isfinite(outs[0][0].float()).all()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
