@@ -134,7 +134,9 @@ extern "C" bfp8_status bfp8_paged_attention(const bfp8_attention_args* p, const 
   a.batch = p->batch;
   a.max_q = p->max_q_len;
   a.causal = p->causal;
-  a.window = p->window;
+  // A window past every distance hides nothing.  Positions begin at -max_q_len (more new tokens than context), so
+  // without this p - window + 1 would leave 32 bits for the widest windows.
+  a.window = p->window > p->max_kv_len + p->max_q_len ? 0 : p->window;
   a.scale = p->softmax_scale;
   const int groups = few_groups(a.group, p->max_q_len);
   a.few_rows = groups * 8;

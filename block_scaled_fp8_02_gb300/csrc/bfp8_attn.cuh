@@ -27,7 +27,7 @@ struct AttnArgs {
   int32_t batch;
   int32_t max_q;
   int32_t causal;
-  int32_t window;
+  int32_t window;               // 0: none; at most max_kv + max_q
   int32_t few_rows;             // sequences of at most this many rows (new tokens x group) go to the kernel for few
   float scale;
   CacheView c;
@@ -53,7 +53,7 @@ __device__ __forceinline__ SeqLens seq_lens(const AttnArgs& a, int b) {
   return s;
 }
 
-// Tokens [lo, hi) that the new token at position p sees.
+// Tokens [lo, hi) that the new token at position p sees (p >= -max_q, window <= max_kv + max_q < 2^31 - max_q).
 __device__ __forceinline__ void seen_range(const AttnArgs& a, int32_t kv_len, int32_t p, int32_t& lo,
                                            int32_t& hi) {
   hi = a.causal ? p + 1 : kv_len;
