@@ -36,7 +36,8 @@ EXPORTS = ("bfp8_group_quant", "bfp8_group_quant_ex", "bfp8_scale_ceil_ue8m0", "
            "bfp8_version", "bfp8_gemm_noalloc", "bfp8_gemm_grouped",
            "bfp8_gemm_grouped_workspace_size", "bfp8_gemm_fused", "bfp8_gemm_fused_workspace_size",
            "bfp8_linear", "bfp8_linear_workspace_size", "bfp8_rmsnorm_quant", "bfp8_kv_cache_write",
-           "bfp8_kv_cache_read", "bfp8_paged_attention", "bfp8_paged_attention_workspace_size")
+           "bfp8_kv_cache_read", "bfp8_paged_attention", "bfp8_paged_attention_workspace_size",
+           "bfp8_stream_capture_id")
 
 
 class BFP8Error(RuntimeError):
@@ -165,6 +166,8 @@ def lib():
             L.bfp8_paged_attention.argtypes = [P, P, P, sz, P]
             L.bfp8_paged_attention_workspace_size.restype = i32
             L.bfp8_paged_attention_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
+            L.bfp8_stream_capture_id.restype = i32
+            L.bfp8_stream_capture_id.argtypes = [P, ctypes.POINTER(ctypes.c_ulonglong)]
             _lib = L
     return _lib
 
@@ -281,6 +284,18 @@ def _as_layout(As: torch.Tensor, M: int, G: int):
 
 
 _ws_cache: dict[tuple[int, int], torch.Tensor] = {}
+# (device, stream) -> (capture, buffer allocated in it); buffers of _ws_cache that a graph holds the address of
+_ws_graph: dict[tuple[int, int], tuple[int, torch.Tensor]] = {}
+_ws_held: dict[int, torch.Tensor] = {}
+
+
+def _capture_id(stream, sp: int) -> int:
+    """The number of the graph capture that the stream is in, 0 outside of any."""
+    if stream is None and not torch.cuda.is_current_stream_capturing():
+        return 0
+    n = ctypes.c_ulonglong(0)
+    _check(lib().bfp8_stream_capture_id(sp, ctypes.byref(n)), "bfp8_stream_capture_id")
+    return int(n.value)
 
 
 def workspace_for(nbytes: int, device: torch.device, stream=None) -> torch.Tensor:
@@ -292,24 +307,45 @@ def workspace_for(nbytes: int, device: torch.device, stream=None) -> torch.Tenso
     without ordering between them get separate buffers.  A new buffer is
     allocated and zeroed on that stream, so its zeroing is ordered before the
     calls that use it, and a replaced buffer is only ever reused by later work
-    on the same stream (the caching allocator's stream-ordered reuse)."""
+    on the same stream (the caching allocator's stream-ordered reuse).
+
+    A call that is being captured gets the stream's buffer if that is large
+    enough, which is then kept for good: the graph holds its address.  Otherwise
+    it gets a buffer of this capture's own, zeroed by a node of the graph, which
+    no call outside the capture is given (it is zero only when the graph runs)."""
     idx = device.index if device.index is not None else torch.cuda.current_device()
     sp = _stream_ptr(stream)
     ws = _ws_cache.get((idx, sp))
+    capture = _capture_id(stream, sp)
+    if capture:
+        if ws is not None and ws.numel() >= nbytes:
+            _ws_held[ws.data_ptr()] = ws
+            return ws
+        born, ws = _ws_graph.get((idx, sp), (0, None))
+        if born != capture:
+            ws = None
     if ws is None or ws.numel() < nbytes:
         s = stream if isinstance(stream, torch.cuda.Stream) else (
             torch.cuda.current_stream(device) if stream is None else
             torch.cuda.ExternalStream(sp, device=device))
         with torch.cuda.stream(s):
             ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _ws_cache[(idx, sp)] = ws
+        if capture:
+            _ws_graph[(idx, sp)] = (capture, ws)
+        else:
+            _ws_cache[(idx, sp)] = ws
     return ws
 
 
 def drop_workspaces() -> None:
     """Forget every cached workspace (after a kernel gave up on a wait, one may
-    hold non-zero stream-K counters)."""
+    hold non-zero stream-K counters).  Those that captured graphs use stay and
+    are zeroed, with the device idle before and after."""
     _ws_cache.clear()
+    for ws in _ws_held.values():
+        torch.cuda.synchronize(ws.device)
+        ws.zero_()
+        torch.cuda.synchronize(ws.device)
 
 
 def bfp8_gemm_workspace_size(M: int, N: int, K: int, options=None,
@@ -743,7 +779,7 @@ def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
     if workspace is None:
         need = _attention_workspace(dev, Hq, H, D, max_q_len)
         workspace = _ws_cache.get((dev.index, sp))
-        if workspace is None or workspace.numel() < need:
+        if workspace is None or workspace.numel() < need or _capture_id(stream, sp):
             workspace = workspace_for(need, dev, stream)
         ws_bytes = workspace.numel()
     else:

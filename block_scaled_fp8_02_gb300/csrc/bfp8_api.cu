@@ -1114,6 +1114,21 @@ bfp8_status bfp8_device_status(int* code, int clear) {
   return ok();
 }
 
+bfp8_status bfp8_stream_capture_id(void* stream, unsigned long long* id) {
+  if (!id) return fail(BFP8_ERR_INVALID_ARG, "id is null");
+  *id = 0;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long n = 0;
+  const cudaError_t e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &n);
+  if (e == cudaErrorStreamCaptureImplicit) {       // the null stream beside another's capture: not part of it
+    cudaGetLastError();
+    return ok();
+  }
+  if (e != cudaSuccess) return fail(BFP8_ERR_CUDA, "capture state of the stream: %s", cudaGetErrorString(e));
+  if (status == cudaStreamCaptureStatusActive) *id = n;
+  return ok();
+}
+
 bfp8_status bfp8_selftest_bounded_wait(uint64_t limit_cycles, uint64_t* elapsed, void* stream) {
   DevInfo d;
   bfp8_status st = current_device(&d, nullptr);

@@ -601,6 +601,12 @@ const char* bfp8_status_string(int status);
  * zero it before reusing it. */
 bfp8_status bfp8_device_status(int* code, int clear);
 
+/* The number of the graph capture that `stream` is part of, 0 when it is not
+ * capturing.  For callers that keep workspaces: a buffer that a captured call
+ * was given has to outlive the graph, and one that was allocated and zeroed
+ * within a capture is zero only when that graph runs. */
+bfp8_status bfp8_stream_capture_id(void* stream, unsigned long long* id);
+
 /* Self-test of the bounded wait every kernel uses: launches one warp that
  * waits on a shared-memory barrier nothing ever arrives on, giving up after
  * `limit_cycles` SM cycles.  Synchronises the stream and returns
