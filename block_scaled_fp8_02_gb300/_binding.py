@@ -601,10 +601,9 @@ def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
 
 
 def _col_major_scales(M: int, G: int, ld: int, dev) -> torch.Tensor:
-    """[M, G] fp32 with strides (1, ld), whose columns the GEMM copies whole.  The last column's ld - M <= 3 floats
-    past the tensor's end need no room of their own: ld is a multiple of 4, so the columns end on 16 bytes, and an
-    allocation that holds 4 bytes of a 16-byte line holds the line.  (A view of a padded buffer costs 4 us.)"""
-    return torch.empty_strided((M, G), (1, ld), dtype=torch.float32, device=dev)
+    """[M, G] fp32 with strides (1, ld) over a buffer of G * ld floats, whose columns the GEMM copies whole."""
+    s = torch.empty_strided((ld, G), (1, ld), dtype=torch.float32, device=dev)
+    return s if ld == M else s.as_strided_((M, G), (1, ld))      # (half the time of a view)
 
 
 def bfp8_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None, residual: torch.Tensor | None = None,
