@@ -700,8 +700,9 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
           f[i] = ex2(red_m[(w0 + i) * C::kJoin + w4] - top);
           sum += red_l[(w0 + i) * C::kJoin + w4] * f[i];
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const float lse2 = sum > 0.f ? top + log2f(sum) : -INFINITY;
+        // zero only where nothing is seen; a NaN stays one
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
         float o[D / 32];
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
@@ -779,7 +780,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
               }
             }
           }
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const int i = r / a.group, head = c.h * a.group + r - i * a.group;
           __nv_bfloat16* dst = a.out + (w.row0 + i) * a.o_st + head * a.o_sh + lane * (D / 32);
           if (ok) {
@@ -788,7 +789,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
             else *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
             if (a.lse != nullptr && lane == 0)
               a.lse[(w.row0 + i) * a.heads + head] =
-                  sum > 0.f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                  sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
           }
         }
       }

@@ -1032,8 +1032,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // ---- output rows
       wait_all(bO + t, item & 1, kDevTimeoutEpilogue);
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f ? m - kLift + log2f(l) : -INFINITY;
+      // zero only where nothing is seen; a NaN stays one
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse2 = l == 0.f ? -INFINITY : m - kLift + log2f(l);
       const bool whole = c.k0 == 0 && c.k1 == c.n;
       const int slot_id = 2 * blockIdx.x + (c.item0 + c.k0 == s_u0 ? 0 : 1);
       float* part = p.partials + slot_id * slot_floats<D>();
@@ -1113,7 +1114,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 o[4 * e + 3] = fmaf(v[e].w, w, o[4 * e + 3]);
               }
             }
-            const float is = sum > 0.f ? 1.f / sum : 0.f;
+            const float is = sum == 0.f ? 0.f : 1.f / sum;
             if (live && ok) {
 #pragma unroll
               for (int e = 0; e < 64; e += 8)
@@ -1123,7 +1124,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
           if (live && ok && a.lse != nullptr)
-            a.lse[(c.w.row0 + i) * a.heads + head] = sum > 0.f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+            a.lse[(c.w.row0 + i) * a.heads + head] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
         }
       }
       tc_fence_before();                       // O and S are read: the next block may overwrite them

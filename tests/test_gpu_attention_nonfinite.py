@@ -1,0 +1,63 @@
+"""What is not finite stays with the rows that see it: NaN and infinities among the keys, values, scales and queries."""
+import pytest
+import torch
+
+import block_scaled_fp8_02_gb300 as bf
+from attn_ref import attention_ref, check_attention, make_cache, make_table
+from block_scaled_fp8_02_gb300 import build as bfbuild
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def dev():
+    bfbuild.build()
+    assert torch.cuda.is_available()
+    return torch.device("cuda:0")
+
+
+def _inputs(q_lens, kv_lens, Hq, H, D, page, seed):
+    g = torch.Generator().manual_seed(seed)
+    pages = sum((n + page - 1) // page for n in kv_lens) + 1
+    kq, ks, vq, vs = make_cache(pages, H, page, D, g)
+    table = make_table(kv_lens, page, pages, g)
+    cu = [0]
+    for m in q_lens:
+        cu.append(cu[-1] + m)
+    q = torch.randn(cu[-1], Hq, D, generator=g).bfloat16()
+    return q, kq, ks, vq, vs, table, cu
+
+
+def _attend(dev, q, kq, ks, vq, vs, table, cu, q_lens, kv_lens, causal=True, window=0):
+    cache = bf.KVCache(*(t.to(dev) for t in (kq, vq, ks, vs)))
+    out, lse = bf.bfp8_paged_attention(q.to(dev), cache, table.to(dev), torch.tensor(cu, dtype=torch.int32, device=dev),
+                                       torch.tensor(kv_lens, dtype=torch.int32, device=dev), max(q_lens), max(kv_lens),
+                                       causal=causal, window=window, return_lse=True)
+    torch.cuda.synchronize()
+    assert bf.bfp8_device_status(clear=True) == 0
+    return out.cpu(), lse.cpu()
+
+
+def _rows(ref, keep):
+    return tuple(t[keep] for t in ref)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [700, 33]), ([4, 3], [129, 2]), ([8], [4000]), ([150], [120]),
+                                            ([300], [900])])
+@pytest.mark.parametrize("value", [NAN])
+@pytest.mark.parametrize("D", [64, 128])
+def test_queries_that_are_not_finite(dev, q_lens, kv_lens, value, D):
+    """They spoil their own row and head, and not even that where the row sees no token."""
+    Hq, H = 8, 2
+    q, kq, ks, vq, vs, table, cu = _inputs(q_lens, kv_lens, Hq, H, D, 32, 11)
+    ref = attention_ref(q, kq, vq, ks, vs, table, cu, kv_lens, D ** -0.5)
+    hit = torch.zeros(cu[-1], Hq, dtype=torch.bool)
+    hit[0, 3] = hit[cu[1] // 2, 0] = hit[-1, 7] = True
+    bad = q.clone()
+    bad[..., 5] = torch.where(hit, torch.tensor(value, dtype=q.dtype), q[..., 5])
+    out, lse = _attend(dev, bad, kq, ks, vq, vs, table, cu, q_lens, kv_lens)
+    clean = ~hit | torch.isinf(ref[1])
+    check_attention(out[clean], lse[clean], _rows(ref, clean))
+    assert torch.isnan(out[~clean]).all() and torch.isnan(lse[~clean]).all()
