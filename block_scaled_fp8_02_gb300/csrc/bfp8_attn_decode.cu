@@ -441,7 +441,8 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
           qf[grp][h * 4 + i][0] = pack_f16x2(f[h][4 * i] * f1 * f2, f[h][4 * i + 1] * f1 * f2);
           qf[grp][h * 4 + i][1] = pack_f16x2(f[h][4 * i + 2] * f1 * f2, f[h][4 * i + 3] * f1 * f2);
         }
-      const float back = a.scale * 1.4426950408889634f * d1 * d2;
+      // (an infinite query: every score a NaN, also where all products happen to be of one sign)
+      const float back = e > 127 ? __uint_as_float(0x7FFFFFFFu) : a.scale * 1.4426950408889634f * d1 * d2;
       cq[grp][0] = __shfl_sync(0xffffffffu, back, 8 * t);
       cq[grp][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }

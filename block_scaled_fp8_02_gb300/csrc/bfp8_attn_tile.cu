@@ -797,6 +797,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int32_t i = static_cast<int32_t>(R / a.group);
       const int head = c.h * a.group + static_cast<int>(R - static_cast<int64_t>(i) * a.group);
       const bool live = i < c.w.q_len;
+      // (rows past the last token see everything: their scores are computed beside the others' and
+      // dropped, and must not make tiles look masked)
+      int32_t lo = 0, hi = 0x7FFFFFFF;
+      if (live) seen_range(a, c.w.kv_len, c.w.pos0 + i, lo, hi);
       float cq;
       {
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (c.w.row0 + (live ? i : 0)) * a.q_st + head * a.q_sh);
@@ -821,6 +825,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         cq = fmaxf(fabsf(a.scale) * 1.4426950408889634f * d1 * d2, 1.2e-38f);
         if (a.scale < 0.f) f1 = -f1;
         if (a.scale == 0.f) f1 = 0.f;
+        // e4m3 holds no infinity: the factor carries it, as a NaN, unless the row sees nothing
+        if (ex > 127 && lo < hi) cq = __uint_as_float(0x7FFFFFFFu);
         uint8_t* qh = smem + C::kOffQ + 2 * t * C::kQ;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
@@ -846,10 +852,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bQ + t));
-      // (rows past the last token see everything: their scores are computed beside the others' and
-      // dropped, and must not make tiles look masked)
-      int32_t lo = 0, hi = 0x7FFFFFFF;
-      if (live) seen_range(a, c.w.kv_len, c.w.pos0 + i, lo, hi);
 
       float m = kNoMax, l = 0.f;
       const int32_t ub = c.t0 / kTile, k0 = c.k0, k1 = c.k1;

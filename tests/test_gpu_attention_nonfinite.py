@@ -8,7 +8,7 @@ from block_scaled_fp8_02_gb300 import build as bfbuild
 
 pytestmark = pytest.mark.gpu
 
-NAN = float("nan")
+NAN, INF = float("nan"), float("inf")
 
 
 @pytest.fixture(scope="module")
@@ -46,7 +46,7 @@ def _rows(ref, keep):
 
 @pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [700, 33]), ([4, 3], [129, 2]), ([8], [4000]), ([150], [120]),
                                             ([300], [900])])
-@pytest.mark.parametrize("value", [NAN])
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
 @pytest.mark.parametrize("D", [64, 128])
 def test_queries_that_are_not_finite(dev, q_lens, kv_lens, value, D):
     """They spoil their own row and head, and not even that where the row sees no token."""
