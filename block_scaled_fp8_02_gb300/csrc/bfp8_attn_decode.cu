@@ -198,8 +198,10 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
   SeqWork* seqs = reinterpret_cast<SeqWork*>(smem + C::kOffSeq);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.c.heads;
+  __shared__ uint32_t s_spoilt[2];            // rows to become NaN, of the item at hand and the next
 
   if (tid == 0) {
+    s_spoilt[0] = s_spoilt[1] = 0;
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar_full(s), 1);
       mbar_init(bar_empty(s), 4 * RT);
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
   float* red_v = red_l + C::kWarps * C::kJoin;
   __shared__ int s_last;
   bool ok = true;
-  uint32_t q = 0;
+  uint32_t q = 0, item = 0;
   // the rows row0 + grp * 8 + g of an item's queries, this lane's elements; fetched while the item before ends
   uint4 raw[NG][KC][2];
   auto fetch = [&](const Cursor& c) {
@@ -462,12 +464,14 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
     }
     const int32_t ub = w.t0 / kUnit;
     // this warp's 32 tokens of a unit as NU times 16, whose chains of dependent steps overlap
-    auto process = [&](int32_t k) {
+    // (tokens that every row sees have a copy of their own, without the masks: 16 sequences of 3 tokens at 8192, 64 / 8
+    // heads of 128, 88 us against 96 in one; 16 of 4 102 against 103.5; batches of one token 105 against 107)
+    auto process = [&](int32_t k, auto masked) {
+      constexpr bool edge = decltype(masked)::value;
       constexpr int NU = 2;
       int32_t base[NU];
       const uint8_t *kst[NU], *vst[NU];
       float ks[NU][2], lv[NU][2];
-      bool edge = false;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         const int slot = static_cast<int>(q % C::kStages), at = wq * 32 + 16 * u;
@@ -475,7 +479,6 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
         kst[u] = smem + slot * C::kStageBytes + at * D;
         vst[u] = kst[u] + C::kCodes;
         const float* sc = reinterpret_cast<const float*>(smem + C::kOffScale) + slot * C::kScaleFloats + at;
-        edge |= base[u] < full_lo || base[u] + 16 > full_hi;
         ks[u][0] = sc[pg];
         ks[u][1] = sc[pg + 8];
         lv[u][0] = lg2(sc[kUnit + pg]);
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
               s[u][grp][i] = v * ks[u][i >> 1] * cq[grp][i & 1];
             }
       }
-      if (edge) {
+      if constexpr (edge) {
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
           const int32_t j0 = base[u] + pg;
@@ -636,6 +639,30 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
               mma_f16_16x8x16(acc[grp][2 * i + hlf], a0, a1, a2, a3, pb[u][grp][0], pb[u][grp][1]);
           }
     };
+    // A value that is not finite must not reach rows that do not see its token, not even with a weight of zero.  Among
+    // tokens that only some rows see (this warp's from .. to) it is taken out of the stage, and the rows that see it
+    // are noted: they become NaN when the parts are joined.  (Teams that share a unit may each find it.)
+    auto take_out = [&](int slot, int32_t first, int32_t from, int32_t to) {
+      constexpr int kLanes = D / 16;                           // of a token
+#pragma unroll 1
+      for (int32_t j = from + lane / kLanes; j < to; j += 32 / kLanes) {
+        uint4* x = reinterpret_cast<uint4*>(smem + slot * C::kStageBytes + C::kCodes + chunk_off<D>(j - first, lane % kLanes));
+        float* vs = reinterpret_cast<float*>(smem + C::kOffScale) + slot * C::kScaleFloats + kUnit + (j - first);
+        const uint4 w4 = *x;
+        const bool scale = *vs >= 0.f && *vs < INFINITY;
+        if ((nan_codes(w4.x) | nan_codes(w4.y) | nan_codes(w4.z) | nan_codes(w4.w)) != 0u || !scale) {
+          *x = make_uint4(without_nan_codes(w4.x), without_nan_codes(w4.y), without_nan_codes(w4.z), without_nan_codes(w4.w));
+          if (!scale) *vs = 0.f;
+          fence_proxy_async_smem();                            // (the stage's next contents come by TMA)
+          for (int r = 0; r < rows; ++r) {
+            int32_t lo, hi;
+            seen_range(a, w.kv_len, w.pos0 + r / a.group, lo, hi);
+            if (j >= lo && j < hi) atomicOr(&s_spoilt[item & 1], 1u << r);
+          }
+        }
+      }
+      __syncwarp();
+    };
     for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
       if (RT == 1 && static_cast<int>(q % C::kGroups) != team) continue;
       const int slot = static_cast<int>(q % C::kStages);
@@ -646,7 +673,16 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
       }
       const int32_t base = (ub + k) * kUnit + wq * 32;
       if (ok && base < w.t1 && base + 32 > w.t0) {
-        process(k);
+        if (base >= full_lo && base + 32 <= full_hi) {
+          process(k, std::false_type{});
+        } else {
+          const int32_t first = (ub + k) * kUnit, from = base > w.t0 ? base : w.t0, to = base + 32 < w.t1 ? base + 32 : w.t1;
+          // (where a window leaves tokens on both sides, all of the warp's are looked at)
+          const bool low = w.t0 < full_lo && from < full_lo;
+          if (low || (full_hi < w.t1 && to > full_hi))
+            take_out(slot, first, low || from > full_hi ? from : full_hi, to);
+          process(k, std::true_type{});
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_empty(slot));
@@ -666,6 +702,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
       const int grp = part4 >> 1, hf = part4 & 1;          // rows 8 grp + 4 hf ..: those of lanes t = 2 hf, 2 hf + 1
       if (part4 * C::kJoin >= rows) break;
       named_bar_sync(1, C::kWarps * 32);
+      if (part4 == 0 && tid == 0) s_spoilt[(item + 1) & 1] = 0;      // the item before is read, the next not begun
       const float l0 = sum_over_g(l[grp][0]), l1 = sum_over_g(l[grp][1]);
       if ((t >> 1) == hf) {
         const int at = warp * C::kJoin + 2 * (t & 1);
@@ -702,7 +739,8 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
           sum += red_l[(w0 + i) * C::kJoin + w4] * f[i];
         }
         // zero only where nothing is seen; a NaN stays one
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (s_spoilt[item & 1] >> r & 1u) inv = __uint_as_float(0x7FFFFFFFu);
         const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
         float o[D / 32];
 #pragma unroll
@@ -796,6 +834,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
       }
     }
     c = nx;
+    ++item;
   }
   if (p.behind) griddep_wait();
 }

@@ -44,6 +44,49 @@ def _rows(ref, keep):
     return tuple(t[keep] for t in ref)
 
 
+KINDS = ["value code", "value scale inf", "value scale nan", "key code", "key scale nan", "key scale inf"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,n", [(4, 200), (6, 131), (8, 300)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 50), (False, 60)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_bad_token(dev, kind, m, n, causal, window, D):
+    """Token j of the second sequence, kv head 0, is spoilt: among the new tokens, which earlier rows do not see, and
+    just before them, which a window hides from later rows.  Rows that see it get no finite output (all elements but
+    those of a finite part of the value), rows that do not, other heads and the other sequence their usual one."""
+    Hq, H, page = 8, 2, 16
+    g4 = Hq // H
+    q_lens, kv_lens = [3, m], [150, n]
+    for j in (n - (m + 1) // 2, n - m - 20):
+        q, kq, ks, vq, vs, table, cu = _inputs(q_lens, kv_lens, Hq, H, D, page, 1000 * m + j)
+        ref = attention_ref(q, kq, vq, ks, vs, table, cu, kv_lens, D ** -0.5, causal, window)
+        pg, o = int(table[1, j // page]), j % page
+        bad = [t.clone() for t in (kq.view(torch.uint8), ks, vq.view(torch.uint8), vs)]
+        if kind.endswith("code"):
+            bad[0 if kind[0] == "k" else 2][pg, 0, o, 17] = 0x7F
+        else:
+            bad[1 if kind[0] == "k" else 3][pg, 0, o] = INF if kind.endswith("inf") else NAN
+        f8 = torch.float8_e4m3fn
+        out, lse = _attend(dev, q, bad[0].view(f8), bad[1], bad[2].view(f8), bad[3], table, cu, q_lens, kv_lens, causal, window)
+        p = torch.arange(n - m, n)
+        sees = ((j <= p) if causal else torch.ones(m, dtype=torch.bool)) & ((j > p - window) if window else True)
+        clean = torch.ones(cu[-1], Hq, dtype=torch.bool)
+        clean[cu[1]:, :g4] = ~sees[:, None]
+        check_attention(out[clean], lse[clean], _rows(ref, clean))
+        if kind == "key scale inf":               # a score of minus infinity is a weight of zero
+            continue
+        spoilt = out[~clean]
+        assert torch.isnan(spoilt[:, 17]).all()
+        if kind != "value code":
+            assert not torch.isfinite(spoilt).any()
+        if kind.startswith("key"):
+            assert torch.isnan(lse[~clean]).all()
+        else:
+            got, want = lse[~clean].double(), ref[1][~clean]
+            assert ((got - want).abs() <= 2.0 ** -17 * ref[3][~clean] + 2.0 ** -19 * (1 + want.abs())).all()
+
+
 @pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [700, 33]), ([4, 3], [129, 2]), ([8], [4000]), ([150], [120]),
                                             ([300], [900])])
 @pytest.mark.parametrize("value", [NAN, INF, -INF])
