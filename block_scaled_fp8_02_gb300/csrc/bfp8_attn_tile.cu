@@ -68,6 +68,7 @@ constexpr int kBlockCost = 8;              // (places of a block besides its til
                                            // 5 to 10 time alike, 12 is 3% slower on a mixed batch)
 constexpr int kSeqChunk = 2048;            // sequences whose tile counts are held at once
 constexpr int kKStages = 3, kVStages = 2, kFStages = 2, kScSlots = 4;
+constexpr int kBadSlots = 8;               // > blocks in flight: the loader is at most kScSlots tiles ahead
 constexpr float kNoMax = -3.0e38f;
 constexpr float kLift = 7.f;               // a weight at the running maximum is 2^7
 constexpr float kMost = 32768.f;           // sum of 64 weights up to which the maximum may lag: each fits f16
@@ -90,7 +91,8 @@ struct TileCfg {
   static constexpr int kOffDl = kOffRv + kScSlots * kTile * 8;   // wide tiles: log2 vs - lv
   static constexpr int kOffIv = kOffDl + kScSlots * kTile * 4;   // wide tiles: 1 / vs
   static constexpr int kOffInfo = kOffIv + kScSlots * kTile * 4; // lv, 2^-lv, wide
-  static constexpr int kOffCur = kOffInfo + kScSlots * 16;       // a cursor a warp
+  static constexpr int kOffBad = kOffInfo + kScSlots * 16;       // a flag a block
+  static constexpr int kOffCur = kOffBad + kBadSlots * 4;        // a cursor a warp
   static constexpr int kOffBar = kOffCur + (kTileThreads / 32) * 80;
   static constexpr int kBars = 2 * kKStages + 2 * kVStages + 2 * kFStages + 3 * kScSlots + 8;
   static constexpr int kSmem = kOffBar + kBars * 8 + 64 + 1024;
@@ -128,16 +130,16 @@ __device__ __forceinline__ SeqBlocks seq_blocks(const AttnArgs& a, int b) {
   w.blocks = rows > a.few_rows ? static_cast<int32_t>((rows + kBlockRows - 1) / kBlockRows) : 0;
   return w;
 }
-// Tokens [t0, t1) that some row of block rb sees, and its tiles.
+// Tokens [t0, t1) that some row of block rb sees, [f0, f1) that every row sees, and its tiles.
 __device__ __forceinline__ int32_t block_tiles(const AttnArgs& a, const SeqBlocks& w, int rb, int32_t& t0,
-                                               int32_t& t1) {
+                                               int32_t& t1, int32_t& f0, int32_t& f1) {
   const uint32_t r0 = static_cast<uint32_t>(rb) * kBlockRows, group = static_cast<uint32_t>(a.group);   // < 2^32: 2^24 tokens, 128 heads
   const int32_t i0 = static_cast<int32_t>(r0 / group);
   int32_t i1 = static_cast<int32_t>((r0 + kBlockRows - 1) / group);
   if (i1 > w.q_len - 1) i1 = w.q_len - 1;
-  int32_t lo, hi, x;
-  seen_range(a, w.kv_len, w.pos0 + i0, lo, x);
-  seen_range(a, w.kv_len, w.pos0 + i1, x, hi);
+  int32_t lo, hi;
+  seen_range(a, w.kv_len, w.pos0 + i0, lo, f1);
+  seen_range(a, w.kv_len, w.pos0 + i1, f0, hi);
   t0 = lo;
   t1 = hi;
   return hi > lo ? (hi + kTile - 1) / kTile - lo / kTile : 1;
@@ -147,6 +149,83 @@ __device__ __forceinline__ int32_t block_tiles(const AttnArgs& a, const SeqBlock
 // tokens at 8192, 40 rows each: 132 us against 152 with the empty tile computed beside it).
 __device__ __forceinline__ int block_query_tiles(const AttnArgs& a, const SeqBlocks& w, int rb) {
   return static_cast<int64_t>(w.q_len) * a.group - static_cast<int64_t>(rb) * kBlockRows > kTile ? 2 : 1;
+}
+
+struct Cursor {
+  int64_t item0;
+  SeqBlocks w;
+  int32_t b, h, rb;
+  int32_t n, k0, k1;
+  int32_t t0, t1;             // tokens that some row sees
+  int32_t f0, f1;             // ... that every row sees
+  uint32_t blk;               // blocks of the share before it
+};
+static_assert(sizeof(Cursor) <= 80, "space of a warp's cursor");
+
+// What is not finite among a block's scales and values must not reach rows that do not see its token, not even as
+// 0 x NaN.  It is taken out where the tiles are made ready; a flag says so, and only then the block's rows look, at their
+// end, at the tokens that they see.  (Looked for tile by tile in the softmax it cost 8% of a chunk, and any more
+// instructions in the converters' or the loader's loops much the same.)
+// What spoils the row that sees tokens [lo, hi) of the block's sequence: 1 a key scale, 2 a value.
+template <int D>
+__device__ __noinline__ uint32_t bad_of_row(const AttnArgs& a, const Cursor& c, int32_t lo, int32_t hi) {
+  uint32_t kinds = 0;
+  for (int32_t j = lo; j < hi; ++j) {
+    const int32_t page = a.table[c.b * a.ld_table + (j >> a.c.page_shift)];
+    if (page < 0 || page >= a.c.num_pages) continue;
+    const int off = j & (a.c.page_size - 1);
+    const int64_t so = page * a.c.ss_page + c.h * a.c.ss_head + off;
+    const float ks = a.c.ks[so];
+    if (ks != ks) kinds |= 1u;
+    if (!(a.c.vs[so] < INFINITY)) kinds |= 2u;
+    if (j >= c.f0 && j < c.f1) continue;                       // a NaN code there is in the product
+    const uint4* v = reinterpret_cast<const uint4*>(a.c.v + page * a.c.st_page + c.h * a.c.st_head + off * a.c.st_tok);
+    for (int e = 0; e < D / 16; ++e)
+      if ((nan_codes(v[e].x) | nan_codes(v[e].y) | nan_codes(v[e].z) | nan_codes(v[e].w)) != 0u) kinds |= 2u;
+  }
+  return kinds;
+}
+
+// Readies converter cw's rows of a tile of values (a warp): rows outside [z0, z1) hold no token and become zero (they
+// may hold anything); rows outside [p0, p1) are not seen by every query row and lose their NaN codes.  Were there any?
+template <int D>
+__device__ __forceinline__ bool prepare_rows_here(uint8_t* tile, int cw, const Cursor& c, int32_t k) {
+  const int32_t tok0 = (c.t0 / kTile + k) * kTile, z0 = c.t0 - tok0, z1 = c.t1 - tok0, p0 = min(c.f0 - tok0, kTile), p1 = c.f1 - tok0;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kGroup = kRows * kConvWarps;
+  const int lane = threadIdx.x & 31, ch = lane % kLanes, r0 = cw * kRows + lane / kLanes;
+  // (rows kGroup apart have the same swizzle)
+  uint8_t* at = tile + (D == 128 ? (ch ^ (r0 & 7)) << 4 : (ch ^ ((r0 >> 1) & 3)) << 4);
+  uint32_t any = 0;
+  auto row = [&](int r) {
+    uint4* x = reinterpret_cast<uint4*>(at + r * D);
+    if (r < z0 || r >= z1) {
+      *x = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      const uint4 w = *x;
+      const uint32_t f = nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
+      if (f != 0u)
+        *x = make_uint4(without_nan_codes(w.x), without_nan_codes(w.y), without_nan_codes(w.z), without_nan_codes(w.w));
+      any |= f;
+    }
+  };
+#pragma unroll 1
+  for (int r = r0; r < p0; r += kGroup) row(r);
+#pragma unroll 1
+  for (int r = r0 + (p1 > r0 ? (p1 - r0 + kGroup - 1) / kGroup * kGroup : 0); r < kTile; r += kGroup) row(r);
+  __syncwarp();
+  return any != 0u;
+}
+
+// Out of the way of the loop's instructions with heads of 128 (a chunk of 4096 at 16384 1438 us, 1466 inlined), inlined with
+// heads of 64 (8 chunks of 512: 100 us, 103 called).
+template <int D>
+__device__ __noinline__ bool prepare_rows_called(uint8_t* tile, int cw, const Cursor& c, int32_t k) {
+  return prepare_rows_here<D>(tile, cw, c, k);
+}
+template <int D>
+__device__ __forceinline__ bool prepare_rows(uint8_t* tile, int cw, const Cursor& c, int32_t k) {
+  if constexpr (D == 128) return prepare_rows_called<D>(tile, cw, c, k);
+  else return prepare_rows_here<D>(tile, cw, c, k);
 }
 
 // MMAs whose descriptors come as low words (start address >> 4 and leading
@@ -228,15 +307,6 @@ __device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i])::"memory");
 }
 
-struct Cursor {
-  int64_t item0;
-  SeqBlocks w;
-  int32_t b, h, rb;
-  int32_t n, k0, k1;
-  int32_t t0, t1;
-};
-static_assert(sizeof(Cursor) <= 80, "space of a warp's cursor");
-
 template <int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -304,8 +374,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int i = warp; i < n; i += kTileThreads / 32) {
       const SeqBlocks w = seq_blocks(a, b0 + i);
       int64_t v = 0;
-      int32_t t0, t1;
-      for (int rb = lane; rb < w.blocks; rb += 32) v += block_tiles(a, w, rb, t0, t1) + kBlockCost;
+      int32_t t0, t1, f0, f1;
+      for (int rb = lane; rb < w.blocks; rb += 32) v += block_tiles(a, w, rb, t0, t1, f0, f1) + kBlockCost;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (lane == 0) cnt[i] = v;
@@ -373,8 +443,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int h = static_cast<int>((u0 - first) / mine);
         int64_t place = first + h * mine;
         for (int rb0 = 0; rb0 < w.blocks; rb0 += 32) {
-          int32_t t0 = 0, t1 = 0;
-          const int64_t own = rb0 + lane < w.blocks ? block_tiles(a, w, rb0 + lane, t0, t1) + kBlockCost : 0;
+          int32_t t0 = 0, t1 = 0, f0 = 0, f1 = 0;
+          const int64_t own = rb0 + lane < w.blocks ? block_tiles(a, w, rb0 + lane, t0, t1, f0, f1) + kBlockCost : 0;
           int64_t v = own;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -390,6 +460,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             s_first.n = static_cast<int32_t>(own) - kBlockCost;
             s_first.t0 = t0;
             s_first.t1 = t1;
+            s_first.f0 = f0;
+            s_first.f1 = f1;
+            s_first.blk = 0;
           }
           place += __shfl_sync(0xffffffffu, v, 31);
         }
@@ -411,6 +484,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // in the line.  Each warp has one in shared memory, kept by its first lane:
   // the loops over tiles need their registers for other things.
   auto step_block = [&](Cursor& c) {            // the block after (b, h, rb)
+    ++c.blk;
     if (++c.rb == c.w.blocks) {
       c.rb = 0;
       if (++c.h == H) {
@@ -420,7 +494,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         } while (c.w.blocks == 0);
       }
     }
-    c.n = block_tiles(a, c.w, c.rb, c.t0, c.t1);
+    c.n = block_tiles(a, c.w, c.rb, c.t0, c.t1, c.f0, c.f1);
   };
   auto clip = [&](Cursor& c) {                  // false: only the block's end lies in the share
     c.k0 = static_cast<int32_t>(s_u0 > c.item0 ? s_u0 - c.item0 : 0);
@@ -428,6 +502,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     return c.k0 < c.k1;
   };
   Cursor& c = reinterpret_cast<Cursor*>(smem + C::kOffCur)[warp];
+  uint32_t* const bad_blocks = reinterpret_cast<uint32_t*>(smem + C::kOffBad);
   auto advance = [&](Cursor& c) {               // false: the share is done
     do {
       c.item0 += c.n + kBlockCost;
@@ -479,29 +554,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // --------------------------------------------- TMA and the tiles' scales
       // scales of tile q as the softmax and the converters take them, from the raw ones; run one
       // tile after their load, before anything that waits for the tile's consumers
-      auto scales = [&](uint32_t q, int32_t tok0, int32_t t0, int32_t t1) {
+      auto scales = [&](uint32_t q, int32_t tok0, int32_t t0, int32_t t1, uint32_t blk) {
         const int sl = static_cast<int>(q % kScSlots);
         wait_all(bRf + sl, ph(q, kScSlots), kDevTimeoutEpilogue);
         const int32_t tok = tok0 + lane * 4;
         const float4 kr = *reinterpret_cast<const float4*>(smem + C::kOffRaw + (sl * 2 * kTile + lane * 4) * 4);
         const float4 vr = *reinterpret_cast<const float4*>(smem + C::kOffRaw + ((sl * 2 + 1) * kTile + lane * 4) * 4);
         float ks[4] = {kr.x, kr.y, kr.z, kr.w}, vs[4] = {vr.x, vr.y, vr.z, vr.w};
-        bool live[4];
+        bool bad = false;
         float top = 0.f, low = 3.0e38f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          live[e] = tok + e >= t0 && tok + e < t1;
-          if (!live[e]) vs[e] = 0.f;
+          const bool live = tok + e >= t0 && tok + e < t1, finite = vs[e] < INFINITY;
+          bad |= live && (ks[e] != ks[e] || !finite);
           // masked scores are -inf before the key scale: it must not be zero or NaN
-          ks[e] = live[e] ? fmaxf(ks[e], 1.2e-38f) : 1.f;
+          ks[e] = live ? fmaxf(ks[e], 1.2e-38f) : 1.f;
+          if (!live || !finite) vs[e] = 0.f;
           top = fmaxf(top, vs[e]);
-          if (live[e]) low = fminf(low, vs[e]);
+          if (live) low = fminf(low, vs[e]);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-        }
+        if (bad) bad_blocks[blk % kBadSlots] = 1u;
+        // (not negative: ordered as their bits are; with shuffles a mixed batch took 3% longer)
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+        low = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(low)));
         // vref = 2^E >= top; values are held as code * (vs / vref) * 2^kVUp, so 2^lv = vref 2^-kVUp
         uint32_t bits = (__float_as_uint(top) + 0x7FFFFFu) & 0xFF800000u;
         if (bits < 0x10000000u) bits = 0x10000000u;                    // 2^-95: an all-zero tile
@@ -548,10 +623,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int box = page >= kTile ? kTile : page;
       uint32_t q = 0, pending = 0;                      // loads begun; a tile whose scales wait
       int32_t p_tok = 0, p_t0 = 0, p_t1 = 0;
+      uint32_t p_blk = 0;
       for (bool more = start(); more; more = next() && ok) {
         const int32_t ub = c.t0 / kTile, t0 = c.t0, t1 = c.t1, h = c.h, k1 = c.k1;
         const int32_t* row = a.table + c.b * a.ld_table;
         int32_t cached = -1, entry = 0;
+        const uint32_t blk = c.blk;
+        if (lane == 0) bad_blocks[blk % kBadSlots] = 0u;        // (its last user is kBadSlots blocks back)
         for (int32_t k = c.k0; k < k1 && ok; ++k) {
           const int32_t tok = (ub + k) * kTile;
           const int32_t first = tok / box;
@@ -587,11 +665,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             bulk_load(sd + kTile * 4, a.c.vs + so, box * 4, bar(bRf + sc));
           }
           ++q;                                          // its copies are in flight
-          if (pending) scales(q - 2, p_tok, p_t0, p_t1);
+          if (pending) scales(q - 2, p_tok, p_t0, p_t1, p_blk);
           pending = q > 1;
           p_tok = tok;
           p_t0 = t0;
           p_t1 = t1;
+          p_blk = blk;
           wait_warp(bKe + ks, ph(q - 1, kKStages) ^ 1u, kDevTimeoutProducer);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(bar(bKf + ks), static_cast<uint32_t>(n * box * D));
@@ -606,10 +685,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (live)
             tma_load_4d(sbase + static_cast<uint32_t>(C::kOffV + vs * C::kK + lane * box * D), &tmV, bar(bVf + vs), 0,
                         off, h, pg);
-          if (q == 1) scales(0, tok, t0, t1);           // the first tile's are waited for
+          if (q == 1) scales(0, tok, t0, t1, blk);      // the first tile's are waited for
         }
       }
-      if (pending) scales(q - 1, p_tok, p_t0, p_t1);
+      if (pending) scales(q - 1, p_tok, p_t0, p_t1, p_blk);
       // no copy may still be landing when the CTA exits (after a failure: bounded waits all the same)
       auto drain = [&](int b0, int stages) {
         for (uint32_t i = q > static_cast<uint32_t>(stages) ? q - stages : 0; i < q; ++i)
@@ -709,12 +788,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       constexpr int CH = D / 16;                        // 16-code chunks of a row
       uint32_t q = 0;
       for (bool more = start(); more; more = next()) {
+        // tiles with places without a token, or tokens that only some rows see: before part0, from part1 on
+        const int32_t ub = c.t0 / kTile, part0 = (c.f0 + kTile - 1) / kTile - ub, part1 = c.f1 / kTile - ub;
         for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
           const int sl = static_cast<int>(q % kScSlots), vs = static_cast<int>(q % kVStages),
                     fs = static_cast<int>(q % kFStages);
           wait_all(bSf + sl, ph(q, kScSlots), kDevTimeoutEpilogue);
           wait_all(bVf + vs, ph(q, kVStages), kDevTimeoutEpilogue);
           wait_all(bFe + fs, ph(q, kFStages) ^ 1u, kDevTimeoutEpilogue);
+          if (__builtin_expect((k < part0 || k >= part1) && ok, 0) && prepare_rows<D>(smem + C::kOffV + vs * C::kK, cw, c, k))
+            bad_blocks[c.blk % kBadSlots] = 1u;
           const uint8_t* src = smem + C::kOffV + vs * C::kK;
           uint8_t* dst = smem + C::kOffF + fs * C::kV16;
           const uint2* rv = reinterpret_cast<const uint2*>(smem + C::kOffRv) + sl * kTile;
@@ -728,7 +811,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             uint2 r[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const int row = cw * (kTile / kConvWarps) + (i0 + u) * RPI + sub;
+              const int row = ((i0 + u) * kConvWarps + cw) * RPI + sub;     // the warps' rows in turn: both have some to ready
               w[u] = *reinterpret_cast<const uint4*>(
                   src + (D == 128 ? row * 128 + ((ch ^ (row & 7)) << 4) : row * 64 + ((ch ^ ((row >> 1) & 3)) << 4)));
               r[u] = rv[row];
@@ -738,8 +821,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int u = 0; u < 4; ++u) {
               const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e)                 // unused places may hold anything
-                e4m3x4_to_f16(r[u].x == 0u ? 0u : ww[e], o[u][2 * e], o[u][2 * e + 1]);
+              for (int e = 0; e < 4; ++e) e4m3x4_to_f16(ww[e], o[u][2 * e], o[u][2 * e + 1]);
             }
             // code * rh + (code * rl): one f16 rounding of the product, and 2^-22 of it
 #pragma unroll
@@ -751,7 +833,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int half = ch >> 2, c0 = 2 * (ch & 3), f0 = half & 1;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const int row = cw * (kTile / kConvWarps) + (i0 + u) * RPI + sub;
+              const int row = ((i0 + u) * kConvWarps + cw) * RPI + sub;
               uint8_t* drow = dst + half * C::kHalf + row * 128;
               const uint4 lo = make_uint4(o[u][0], o[u][1], o[u][2], o[u][3]),
                           hi = make_uint4(o[u][4], o[u][5], o[u][6], o[u][7]);
@@ -1035,7 +1117,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       wait_all(bO + t, item & 1, kDevTimeoutEpilogue);
       tc_fence_after();
       // zero only where nothing is seen; a NaN stays one
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float inv = l == 0.f ? 0.f : 1.f / l;
+      if (__builtin_expect(bad_blocks[c.blk % kBadSlots] != 0u, 0) && live) {
+        const uint32_t kinds = bad_of_row<D>(a, c, lo, hi);
+        if (kinds != 0u) inv = __uint_as_float(0x7FFFFFFFu);
+        if (kinds & 1u) l = inv;
+      }
       const float lse2 = l == 0.f ? -INFINITY : m - kLift + log2f(l);
       const bool whole = c.k0 == 0 && c.k1 == c.n;
       const int slot_id = 2 * blockIdx.x + (c.item0 + c.k0 == s_u0 ? 0 : 1);

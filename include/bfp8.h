@@ -459,7 +459,7 @@ bfp8_status bfp8_rmsnorm_quant(const void* x, int in_dtype, int64_t ld_x, const 
 
 /*
  * A paged cache of keys and values in e4m3, one fp32 scale per (token, kv
- * head): value = code * scale.  Token `o` of page `p`, kv head `h`:
+ * head): value = code * scale, scales not negative.  Token `o` of page `p`, kv head `h`:
  *   codes  k + p * stride_page + h * stride_head + o * stride_token, head_dim bytes
  *   scale  k_scale[p * scale_stride_page + h * scale_stride_head + o]
  * and the same offsets in v and v_scale.  A slot is p * page_size + o.
@@ -526,7 +526,8 @@ bfp8_status bfp8_kv_cache_read(const bfp8_kv_cache* cache, const int64_t* slots,
  *   S_j   = softmax_scale * q . k_j,   w = softmax(S over the tokens seen)
  *   out   = sum_j w_j v_j,   lse = log sum_j exp(S_j)   (natural logarithm)
  * A row that sees no token (q_len > kv_lens[b], an empty context) gets out = 0
- * and lse = -infinity.  Softmax and sums are fp32; the products run on the
+ * and lse = -infinity.  Queries, keys and values that are not finite reach only
+ * the rows that see them.  Softmax and sums are fp32; the products run on the
  * tensor cores from the exact bf16 queries and e4m3 codes, with the weights
  * rounded to fp16 (11 bits) for the second product.
  *   q, out   bf16 [total_q, num_heads, head_dim] with token and head strides

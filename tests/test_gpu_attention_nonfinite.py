@@ -48,7 +48,7 @@ KINDS = ["value code", "value scale inf", "value scale nan", "key code", "key sc
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("m,n", [(4, 200), (6, 131), (8, 300)])
+@pytest.mark.parametrize("m,n", [(4, 200), (6, 131), (8, 300), (40, 333), (200, 700)])
 @pytest.mark.parametrize("causal,window", [(True, 0), (True, 50), (False, 60)])
 @pytest.mark.parametrize("D", [64, 128])
 def test_one_bad_token(dev, kind, m, n, causal, window, D):
@@ -85,6 +85,25 @@ def test_one_bad_token(dev, kind, m, n, causal, window, D):
         else:
             got, want = lse[~clean].double(), ref[1][~clean]
             assert ((got - want).abs() <= 2.0 ** -17 * ref[3][~clean] + 2.0 ** -19 * (1 + want.abs())).all()
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [700, 33]), ([4, 1], [129, 5]), ([8, 2], [300, 257]), ([150], [201])])
+@pytest.mark.parametrize("D", [64, 128])
+def test_unused_places_leave_no_trace(dev, q_lens, kv_lens, D):
+    """Whatever the places past a context's end hold, the bits are the same."""
+    page = 32
+    args = _inputs(q_lens, kv_lens, 8, 2, D, page, 7)
+    q, kq, ks, vq, vs, table, cu = args
+    outs = [_attend(dev, *args, q_lens, kv_lens)]
+    for code, scale in ((0x7F, NAN), (0xFF, INF), (0x7F, -INF)):
+        bad = [t.clone() for t in (kq.view(torch.uint8), ks, vq.view(torch.uint8), vs)]
+        for b, n in enumerate(kv_lens):
+            pg, o = int(table[b, (n - 1) // page]), (n - 1) % page + 1
+            for t, x in zip(bad, (code, scale, code, scale)):
+                t[pg, :, o:] = x
+        f8 = torch.float8_e4m3fn
+        outs.append(_attend(dev, q, bad[0].view(f8), bad[1], bad[2].view(f8), bad[3], table, cu, q_lens, kv_lens))
+        assert torch.equal(outs[-1][0], outs[0][0]) and torch.equal(outs[-1][1], outs[0][1])
 
 
 @pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [700, 33]), ([4, 3], [129, 2]), ([8], [4000]), ([150], [120]),
