@@ -1,0 +1,48 @@
+"""Batches of more sequences than a CTA of the kernel for few rows has threads, and shares of more than it keeps."""
+import pytest
+import torch
+
+from block_scaled_fp8_02_gb300 import build as bfbuild
+from test_gpu_attention import _run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    bfbuild.build()
+    assert torch.cuda.is_available()
+    return torch.device("cuda:0")
+
+
+@pytest.mark.parametrize("Hq,H,D", [(8, 1, 64), (16, 1, 64), (32, 1, 64), (6, 2, 128)])
+@pytest.mark.parametrize("n", [385, 513, 1100])
+def test_many_single_tokens(dev, Hq, H, D, n):
+    """Ragged contexts, every seventh empty; a few long ones that shares cut."""
+    kv = [0 if i % 7 == 3 else 1500 if i % 251 == 0 else 1 + (i * 37) % 60 for i in range(n)]
+    _run(dev, [1] * n, kv, Hq, H, D, 16)
+
+
+def test_sequences_without_tokens_among_many(dev):
+    n = 900
+    q = [0 if i % 3 == 0 or 100 < i < 400 else 1 for i in range(n)]
+    _run(dev, q, [5 + i % 40 for i in range(n)], 8, 1, 64, 16)
+
+
+def test_shares_of_more_sequences_than_are_kept(dev):
+    n = 6000
+    _run(dev, [1] * n, [i % 3 for i in range(n)], 4, 1, 64, 16)
+
+
+@pytest.mark.parametrize("Hq,H", [(8, 1), (24, 1)])
+def test_chunks_among_many_single_tokens(dev, Hq, H):
+    """Both kernels beside each other, each with its own path for large batches."""
+    n = 700
+    q = [40 if i % 50 == 7 else 1 for i in range(n)]
+    _run(dev, q, [m + (i * 13) % 70 for i, m in enumerate(q)], Hq, H, 64, 16)
+
+
+def test_chunks_among_more_sequences_than_are_counted_at_once(dev):
+    n = 2100
+    q = [35 if i % 300 == 299 else 1 for i in range(n)]
+    _run(dev, q, [m + i % 5 for i, m in enumerate(q)], 8, 1, 64, 16)
