@@ -742,6 +742,11 @@ def bfp8_paged_attention_workspace_size(num_heads: int, num_kv_heads: int, head_
     return int(n.value)
 
 
+# From one token more than the kernel for few rows takes of any group (32 rows) the size is the same for all lengths:
+# asked for as one, or the cache below would grow by an entry for every prompt's length.
+_LONG_Q = 33
+
+
 @functools.lru_cache(maxsize=None)
 def _attention_workspace(device, num_heads: int, num_kv_heads: int, head_dim: int, max_q_len: int) -> int:
     return bfp8_paged_attention_workspace_size(num_heads, num_kv_heads, head_dim, max_q_len)
@@ -776,7 +781,7 @@ def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
     sp = _stream_of(stream)
     if workspace is None:
-        need = _attention_workspace(dev, Hq, H, D, max_q_len)
+        need = _attention_workspace(dev, Hq, H, D, min(max_q_len, _LONG_Q))
         workspace = _ws_cache.get((dev.index, sp))
         if workspace is None or workspace.numel() < need or _capture_id(stream, sp):
             workspace = workspace_for(need, dev, stream)

@@ -91,3 +91,9 @@ def test_captures_on_a_cold_stream(dev):
             s.synchronize()
             assert torch.equal(eager, want)
     assert bf.bfp8_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("Hq,H,D", [(1, 1, 64), (8, 8, 128), (64, 8, 128), (24, 8, 64), (33, 1, 128), (128, 1, 128)])
+def test_attention_workspaces_of_long_prompts_are_of_one_size(dev, Hq, H, D):
+    sizes = {bf.bfp8_paged_attention_workspace_size(Hq, H, D, n) for n in (33, 34, 100, 4096, 1 << 24)}
+    assert len(sizes) == 1
