@@ -770,7 +770,7 @@ def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
     if kv_lens.dim() != 1 or cu_q.shape != (len(kv_lens) + 1,) or not kv_lens.is_contiguous() or not cu_q.is_contiguous():
         raise ValueError("kv_lens must be a contiguous [batch] tensor and cu_q a contiguous [batch + 1] one")
     B = len(kv_lens)
-    if len(ts) != 2 or ts[0] != B or (B > 0 and tst[1] != 1):
+    if len(ts) != 2 or ts[0] != B or (B > 0 and ts[1] > 1 and tst[1] != 1):
         raise ValueError(f"block_table must be [{B}, max_pages] with unit inner stride")
     if block_table.dtype != torch.int32 or cu_q.dtype != torch.int32 or kv_lens.dtype != torch.int32:
         raise ValueError("block_table, cu_q and kv_lens must be int32")
@@ -788,9 +788,13 @@ def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
         ws_bytes = workspace.numel()
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
-    q_st, out_st = q.stride(), out.stride()
-    a = _pack_attention.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0, T, Hq, B, q_st[0], q_st[1],
-                      out_st[0], out_st[1], block_table.data_ptr(), tst[0] if B > 1 else ts[1], ts[1], max_q_len,
+    (qt, qh, _), (ot, oh, _) = q.stride(), out.stride()
+    if T == 1:                                 # the stride of an axis of one means nothing: any will do
+        qt = ot = D
+    if Hq == 1:
+        qh = oh = D
+    a = _pack_attention.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0, T, Hq, B, qt, qh,
+                      ot, oh, block_table.data_ptr(), tst[0] if B > 1 else ts[1], ts[1], max_q_len,
                       max_kv_len, cu_q.data_ptr(), kv_lens.data_ptr(), D ** -0.5 if scale is None else scale,
                       causal, window, 0)
     _check((_lib or lib()).bfp8_paged_attention(a, cache._desc, workspace.data_ptr(), ws_bytes,

@@ -1,4 +1,6 @@
 """The attention call's host side, without a device."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -27,3 +29,41 @@ def test_long_prompts_share_a_workspace_size(monkeypatch):
         with pytest.raises(LookupError):
             bf.bfp8_paged_attention(*_args(), n, 20)
     assert len(set(asked)) == 3
+
+
+@pytest.fixture
+def packed(monkeypatch):
+    """The calls' argument structures, instead of the calls."""
+    calls = []
+
+    def attention(args, desc, ws, ws_bytes, stream):
+        calls.append(dict(zip([f for f, _ in B.AttentionArgs._fields_], B._pack_attention.unpack(args))))
+        return 0
+
+    monkeypatch.setattr(B, "_lib", SimpleNamespace(bfp8_paged_attention=attention))
+    monkeypatch.setattr(B, "_stream_of", lambda stream: 0)
+    return calls
+
+
+@pytest.mark.parametrize("T,Hq", [(1, 4), (3, 1), (1, 1)])
+def test_strides_of_single_tokens_and_heads_are_free(packed, T, Hq):
+    """A slice of one has whatever stride its parent had; the library wants multiples of 8 elements, at least head_dim."""
+    D = 64
+    _, cache, table, cu, kv = _args(T=T, H=1)
+    q = torch.zeros(10 * 10 * D).bfloat16()
+    token = 3 if T == 1 else Hq * D
+    head = 5 if Hq == 1 else D
+    q, out = (torch.as_strided(q, (T, Hq, D), (token, head, 1)) for _ in range(2))
+    bf.bfp8_paged_attention(q, cache, table, cu, kv, T, 20, out=out, workspace=torch.zeros(16))
+    a = packed[0]
+    for n in ("q_stride_token", "q_stride_head", "out_stride_token", "out_stride_head"):
+        assert a[n] % 8 == 0 and a[n] >= D
+    assert T == 1 or a["q_stride_token"] == token
+    assert Hq == 1 or a["q_stride_head"] == head
+
+
+def test_a_table_of_one_page_may_be_a_column(packed):
+    q, cache, _, cu, kv = _args()
+    wide = torch.zeros(1, 4, dtype=torch.int32)
+    bf.bfp8_paged_attention(q, cache, torch.as_strided(wide, (1, 1), (4, 4)), cu, kv, 3, 16, workspace=torch.zeros(16))
+    assert packed[0]["max_pages"] == 1 and packed[0]["ld_table"] == 1

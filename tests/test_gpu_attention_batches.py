@@ -46,3 +46,18 @@ def test_chunks_among_more_sequences_than_are_counted_at_once(dev):
     n = 2100
     q = [35 if i % 300 == 299 else 1 for i in range(n)]
     _run(dev, q, [m + i % 5 for i, m in enumerate(q)], 8, 1, 64, 16)
+
+
+def test_one_token_in_a_row_of_odd_width(dev):
+    """A single token's slice of a wider row, whose stride is no multiple of 8."""
+    import block_scaled_fp8_02_gb300 as bf
+    from attn_ref import make_cache
+    g = torch.Generator().manual_seed(6)
+    kq, ks, vq, vs = make_cache(3, 2, 16, 64, g)
+    cache = bf.KVCache(*(t.to(dev) for t in (kq, vq, ks, vs)))
+    args = (cache, torch.arange(3, dtype=torch.int32, device=dev)[None], torch.tensor([0, 1], dtype=torch.int32, device=dev),
+            torch.tensor([40], dtype=torch.int32, device=dev), 1, 40)
+    wide = torch.randn(4, 8 * 64 + 3, generator=g).bfloat16().to(dev)
+    q = wide[:1, :512].view(1, 8, 64)
+    assert q.stride(0) == 515
+    assert torch.equal(bf.bfp8_paged_attention(q, *args), bf.bfp8_paged_attention(q.contiguous().clone(), *args))
