@@ -781,7 +781,7 @@ def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
     sp = _stream_of(stream)
     if workspace is None:
-        need = _attention_workspace(dev, Hq, H, D, min(max_q_len, _LONG_Q))
+        need = _attention_workspace(dev, Hq, H, D, min(max_q_len, _LONG_Q)) if T and B else 0
         workspace = _ws_cache.get((dev.index, sp))
         if workspace is None or workspace.numel() < need or _capture_id(stream, sp):
             workspace = workspace_for(need, dev, stream)

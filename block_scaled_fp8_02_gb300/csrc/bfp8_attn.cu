@@ -80,10 +80,13 @@ extern "C" bfp8_status bfp8_paged_attention(const bfp8_attention_args* p, const 
   bfp8_status st = check_cache(cache, &a.c);
   if (st != BFP8_OK) return st;
   if (!p) return bad("args is null");
-  if ((st = check_heads(p->num_heads, a.c.heads, a.c.dim, p->max_q_len)) != BFP8_OK) return st;
+  // an empty call's bounds may be zero
+  const bool empty = p->batch == 0 || p->total_q == 0;
+  if ((st = check_heads(p->num_heads, a.c.heads, a.c.dim, empty && p->max_q_len == 0 ? 1 : p->max_q_len)) != BFP8_OK)
+    return st;
   if (p->batch < 0 || p->batch > 65535 || p->total_q < 0 || p->total_q >= (int64_t{1} << 31))
     return bad("batch = %d, total_q = %lld", p->batch, (long long)p->total_q);
-  if (p->max_pages < 1 || p->ld_table < p->max_pages)
+  if (p->max_pages < (empty ? 0 : 1) || p->ld_table < p->max_pages)
     return bad("max_pages = %d, ld_table = %lld", p->max_pages, (long long)p->ld_table);
   if (p->max_kv_len < 0 || p->max_kv_len > (int64_t{1} << 30))
     return bad("max_kv_len = %lld (expected 0 .. 2^30)", (long long)p->max_kv_len);
@@ -92,7 +95,7 @@ extern "C" bfp8_status bfp8_paged_attention(const bfp8_attention_args* p, const 
   if (!std::isfinite(p->softmax_scale)) return bad("softmax_scale is not finite");
   if (p->causal != 0 && p->causal != 1) return bad("causal = %d (expected 0 or 1)", p->causal);
   if (p->window < 0) return bad("window = %d (expected >= 0)", p->window);
-  if (p->batch == 0 || p->total_q == 0) return set_last_error(BFP8_OK, "");
+  if (empty) return set_last_error(BFP8_OK, "");
   if (!p->q || !p->out || !p->block_table || !p->cu_q || !p->kv_lens)
     return bad("null pointer (q=%p out=%p block_table=%p cu_q=%p kv_lens=%p)", p->q, p->out,
                (const void*)p->block_table, (const void*)p->cu_q, (const void*)p->kv_lens);

@@ -547,7 +547,8 @@ bfp8_status bfp8_kv_cache_read(const bfp8_kv_cache* cache, const int64_t* slots,
  * Page numbers outside the cache, and lengths outside the bounds, give
  * unspecified outputs for their sequence, never a fault; page numbers are also
  * recorded as BFP8_DEV_BAD_CACHE_INDEX.  Results are deterministic.
- * batch == 0 or total_q == 0 launches nothing.
+ * batch == 0 or total_q == 0 launches nothing; max_q_len and max_pages may then
+ * be 0 too.
  */
 typedef struct {
   const void* q;

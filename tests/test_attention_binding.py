@@ -6,6 +6,7 @@ import torch
 
 import block_scaled_fp8_02_gb300 as bf
 from block_scaled_fp8_02_gb300 import _binding as B
+from block_scaled_fp8_02_gb300 import build as bfbuild
 
 
 def _args(T=3, Hq=4, H=2, D=64, pages=2, page=16):
@@ -67,3 +68,16 @@ def test_a_table_of_one_page_may_be_a_column(packed):
     wide = torch.zeros(1, 4, dtype=torch.int32)
     bf.bfp8_paged_attention(q, cache, torch.as_strided(wide, (1, 1), (4, 4)), cu, kv, 3, 16, workspace=torch.zeros(16))
     assert packed[0]["max_pages"] == 1 and packed[0]["ld_table"] == 1
+
+
+@pytest.mark.parametrize("T,batch", [(0, 1), (0, 0), (0, 3), (5, 0)])
+def test_empty_calls_with_bounds_of_zero(T, batch):
+    """The natural bounds of a batch without new tokens are zero; nothing is launched, so no device is needed."""
+    bfbuild.build()
+    q, cache, _, _, _ = _args(T=T)
+    table = torch.zeros(batch, 0, dtype=torch.int32)
+    cu, kv = torch.zeros(batch + 1, dtype=torch.int32), torch.zeros(batch, dtype=torch.int32)
+    out, lse = bf.bfp8_paged_attention(q, cache, table, cu, kv, 0, 0, return_lse=True, workspace=torch.zeros(256), stream=0)
+    assert out.shape == q.shape and lse.shape == (T, 4)
+    with pytest.raises(bf.BFP8Error):
+        bf.bfp8_paged_attention(q, cache, table, cu, kv, -1, 0, workspace=torch.zeros(256), stream=0)

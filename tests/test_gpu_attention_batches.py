@@ -58,6 +58,18 @@ def test_one_token_in_a_row_of_odd_width(dev):
     args = (cache, torch.arange(3, dtype=torch.int32, device=dev)[None], torch.tensor([0, 1], dtype=torch.int32, device=dev),
             torch.tensor([40], dtype=torch.int32, device=dev), 1, 40)
     wide = torch.randn(4, 8 * 64 + 3, generator=g).bfloat16().to(dev)
-    q = wide[:1, :512].view(1, 8, 64)
-    assert q.stride(0) == 515
+    q = torch.as_strided(wide, (1, 8, 64), (515, 64, 1))
     assert torch.equal(bf.bfp8_paged_attention(q, *args), bf.bfp8_paged_attention(q.contiguous().clone(), *args))
+
+
+def test_batches_without_new_tokens(dev):
+    """Bounds of zero, the library's own workspace; and the next call finds everything in order."""
+    import block_scaled_fp8_02_gb300 as bf
+    cache = bf.KVCache.empty(2, 2, 16, 64, dev)
+    for batch in (0, 2):
+        cu, kv = torch.zeros(batch + 1, dtype=torch.int32, device=dev), torch.zeros(batch, dtype=torch.int32, device=dev)
+        q = torch.zeros(0, 8, 64, dtype=torch.bfloat16, device=dev)
+        out, lse = bf.bfp8_paged_attention(q, cache, torch.zeros(batch, 0, dtype=torch.int32, device=dev), cu, kv, 0, 0,
+                                           return_lse=True)
+        assert out.shape == (0, 8, 64) and lse.shape == (0, 8)
+    _run(dev, [1, 3], [700, 9], 8, 2, 64, 16)
