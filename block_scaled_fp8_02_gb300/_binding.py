@@ -592,6 +592,13 @@ def _stream_of(stream) -> int:
     return _stream_ptr(stream)
 
 
+def _on(dev: torch.device, *tensors) -> None:
+    """All on one device: an address of another one (a length left on the host, say) would fault in the kernel."""
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"a tensor is on {t.device}, the others on {dev}")
+
+
 def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
     """Row stride of a tensor of the given 2-D shape with unit inner stride."""
     st = t.stride()
@@ -635,6 +642,7 @@ def bfp8_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None, residual: t
         if weight.dtype not in _IN_DTYPE or weight.shape != (K,) or not weight.is_contiguous():
             raise ValueError(f"weight must be a contiguous bfloat16 or float32 tensor of shape ({K},)")
         w_dtype, w_ptr = _IN_DTYPE[weight.dtype], weight.data_ptr()
+    _on(dev, residual, residual_out, weight)
     q = s = y = None
     if quantise:
         G = (K + 127) // 128
@@ -674,6 +682,7 @@ class KVCache:
             raise ValueError("k_scale and v_scale must be float32")
         if st[3] != 1 or ss[2] != 1 or v.stride() != st or v_scale.stride() != ss:
             raise ValueError("k and v (and the two scale tensors) must have the same strides, the inner one 1")
+        _on(k.device, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         P, H, page, D = shape
         self._desc = _pack_cache.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, page, H, D, 0,
@@ -716,6 +725,7 @@ def bfp8_kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots:
     if k.stride(2) != 1 or v.stride(2) != 1:
         raise ValueError("k and v must have unit inner stride")
     T = _check_slots(slots, k.shape[0])
+    _on(k.device, v, slots, cache.k)
     _check((_lib or lib()).bfp8_kv_cache_write(k.data_ptr(), v.data_ptr(), _IN_DTYPE[k.dtype], k.stride(0), k.stride(1),
                                      v.stride(0), v.stride(1), slots.data_ptr(), T,
                                      SCALE_UE8M0 if ue8m0 else SCALE_FP32, cache._desc,
@@ -727,6 +737,7 @@ def bfp8_kv_cache_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16
     if dtype not in _IN_DTYPE:
         raise ValueError("dtype must be bfloat16 or float32")
     T = _check_slots(slots)
+    _on(slots.device, cache.k)
     _, H, _, D = cache.k.shape
     k = torch.empty((T, H, D), dtype=dtype, device=slots.device)
     v = torch.empty((T, H, D), dtype=dtype, device=slots.device)
@@ -778,6 +789,7 @@ def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
         out = torch.empty(qs, dtype=torch.bfloat16, device=dev)
     elif out.shape != qs or out.dtype != torch.bfloat16 or out.stride(2) != 1:
         raise ValueError("out must be bfloat16, shaped like q, with unit inner stride")
+    _on(dev, cache.k, block_table, cu_q, kv_lens, out, workspace)
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
     sp = _stream_of(stream)
     if workspace is None:

@@ -81,3 +81,30 @@ def test_empty_calls_with_bounds_of_zero(T, batch):
     assert out.shape == q.shape and lse.shape == (T, 4)
     with pytest.raises(bf.BFP8Error):
         bf.bfp8_paged_attention(q, cache, table, cu, kv, -1, 0, workspace=torch.zeros(256), stream=0)
+
+
+def test_tensors_of_another_device_are_refused(packed):
+    q, cache, table, cu, kv = _args()
+    ws = torch.zeros(16)
+    bf.bfp8_paged_attention(q, cache, table, cu, kv, 3, 20, workspace=ws)
+    for i, t in ((1, table), (2, cu), (3, kv)):
+        args = [cache, table, cu, kv]
+        args[i] = t.to("meta")
+        with pytest.raises(ValueError):
+            bf.bfp8_paged_attention(q, *args, 3, 20, workspace=ws)
+    for kw in (dict(out=q.to("meta"), workspace=ws), dict(workspace=ws.to("meta"))):
+        with pytest.raises(ValueError):
+            bf.bfp8_paged_attention(q, cache, table, cu, kv, 3, 20, **kw)
+    assert len(packed) == 1
+    k, s, slots = q[:, :2].contiguous(), torch.zeros(2, 2, 16), torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        bf.KVCache(cache.k, cache.v, s, s.to("meta"))
+    for args in ((k, k.to("meta"), cache, slots), (k, k, cache, slots.to("meta"))):
+        with pytest.raises(ValueError):
+            bf.bfp8_kv_cache_write(*args)
+    with pytest.raises(ValueError):
+        bf.bfp8_kv_cache_read(cache, slots.to("meta"))
+    x = torch.zeros(3, 8)
+    for kw in (dict(weight=torch.ones(8, device="meta")), dict(weight=None, residual=x.to("meta"))):
+        with pytest.raises(ValueError):
+            bf.bfp8_rmsnorm_quant(x, **kw)
