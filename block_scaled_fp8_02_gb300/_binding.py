@@ -608,9 +608,10 @@ def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
 
 
 def _col_major_scales(M: int, G: int, ld: int, dev) -> torch.Tensor:
-    """[M, G] fp32 with strides (1, ld) over a buffer of G * ld floats, whose columns the GEMM copies whole."""
-    s = torch.empty_strided((ld, G), (1, ld), dtype=torch.float32, device=dev)
-    return s if ld == M else s.as_strided_((M, G), (1, ld))      # (half the time of a view)
+    """[M, G] fp32 with strides (1, ld), whose columns the GEMM copies in 16-byte lines.  ld - M < 4 and the columns begin on
+    lines, so the last one's line holds at least one of the tensor's floats, and CUDA memory is never handed out in
+    parts of a line.  (A slice of a buffer with the ld - M floats too costs 4 us of a small call's 15.)"""
+    return torch.empty_strided((M, G), (1, ld), dtype=torch.float32, device=dev)
 
 
 def bfp8_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None, residual: torch.Tensor | None = None,
@@ -642,7 +643,7 @@ def bfp8_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None, residual: t
         if weight.dtype not in _IN_DTYPE or weight.shape != (K,) or not weight.is_contiguous():
             raise ValueError(f"weight must be a contiguous bfloat16 or float32 tensor of shape ({K},)")
         w_dtype, w_ptr = _IN_DTYPE[weight.dtype], weight.data_ptr()
-    _on(dev, residual, residual_out, weight)
+    _on(dev, residual, residual_out if residual_out is not residual else None, weight)
     q = s = y = None
     if quantise:
         G = (K + 127) // 128

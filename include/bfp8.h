@@ -199,7 +199,11 @@ typedef struct {
  *   As   activation scales, G = ceil(K / 128) per row:
  *          as_col_major = 1: As[kb * ld_as + m], ld_as >= M; the buffer holds
  *                            G * ld_as floats (rows are copied whole, as the
- *                            [G, bfp8_scale_ld(M)] buffers of bfp8_group_quant)
+ *                            [G, bfp8_scale_ld(M)] buffers of bfp8_group_quant).
+ *                            With ld_as - M < 4 and rows that begin on 16 bytes
+ *                            it may end with the last scale: what is copied past
+ *                            that lies in the same 16-byte line, is not used, and
+ *                            is there in any CUDA allocation
  *          as_col_major = 0: As[m * ld_as + kb], ld_as >= G
  *   Bs   [ceil(N / 128), G] fp32, row-major, one scale per 128 x 128 weight tile.
  *   out  [M, N] bfloat16, row-major; each element is the fp32 accumulation of
