@@ -166,10 +166,14 @@ static_assert(sizeof(Cursor) <= 80, "space of a warp's cursor");
 // 0 x NaN.  It is taken out where the tiles are made ready; a flag says so, and only then the block's rows look, at their
 // end, at the tokens that they see.  (Looked for tile by tile in the softmax it cost 8% of a chunk, and any more
 // instructions in the converters' or the loader's loops much the same.)
-// What spoils the row that sees tokens [lo, hi) of the block's sequence: 1 a key scale, 2 a value.
+// What spoils the row that sees tokens [lo, hi) of the block's sequence among those of this CTA's tiles: 1 a key scale,
+// 2 a value.
 template <int D>
 __device__ __noinline__ uint32_t bad_of_row(const AttnArgs& a, const Cursor& c, int32_t lo, int32_t hi) {
   uint32_t kinds = 0;
+  const int32_t base = c.t0 / kTile * kTile;
+  lo = max(lo, base + c.k0 * kTile);
+  hi = min(hi, base + c.k1 * kTile);
   for (int32_t j = lo; j < hi; ++j) {
     const int32_t page = a.table[c.b * a.ld_table + (j >> a.c.page_shift)];
     if (page < 0 || page >= a.c.num_pages) continue;
