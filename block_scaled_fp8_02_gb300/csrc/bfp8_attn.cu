@@ -21,7 +21,7 @@ bfp8_status bad(const char* fmt, V... v) {
 }
 
 // Rows a kv head up to which the kernel for few rows takes a sequence: what its registers hold.  16 sequences at
-// 8192, 64 / 8 heads of 128: 103 us with 32 rows there, 132 with 40 in the other, whose 128-row tiles
+// 8192, 64 / 8 heads of 128: 100 us with 32 rows there, 118 with 40 in the other, whose 128-row tiles
 // cost the same from 33 rows to 128.
 constexpr int kFewRows = 32;
 

@@ -36,7 +36,7 @@
 //
 // Measured, 64 query over 8 kv heads of 128: 64 sequences of up to 8192 tokens
 // (558 MB of cache) 106 us, 5.3 TB/s or 0.78 of the measured copy rate; one of
-// 32768 tokens 22.9 us, of which 10.2 would be the cache's reading and the rest
+// 32768 tokens 21.9 us (25 to 29 with the host's call, back to back), of which 10.2 would be the cache's reading and the rest
 // is the launch, the first units' latency and the joining of the parts.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -71,7 +71,7 @@ struct DecCfg {
   // Consumers: teams of four warps, 32 tokens a warp, as two chains of 16.  Up to 16 rows (NG eights of
   // them in a warp) the teams take units in turn (RT = 1); more rows than a warp's registers hold are shared out
   // and RT teams work on every unit (one warp with 32 rows spilled: 16 sequences of 4 tokens at 8192,
-  // 64 / 8 heads of 128, took 167 us against 103).  The last warpgroup's first warp produces; registers are handed to the consumers
+  // 64 / 8 heads of 128, took 167 us against 103 then, 100 now).  The last warpgroup's first warp produces; registers are handed to the consumers
   // (launch: 128 or 168 a thread).
   static constexpr int kWarps = NG == 1 ? 12 : 8;
   static constexpr int kGroups = kWarps / 4;

@@ -7,7 +7,8 @@
 //   S = Q K^T   tcgen05.mma kind::f8f6f4 straight from the cache's codes.  A bf16
 //               query element (8 significant bits) is the sum of two e4m3 numbers
 //               (4 bits each) after scaling its row by a power of two, so Q is kept
-//               as two e4m3 operands and S takes two passes: exact products at the
+//               as two e4m3 operands and S takes two passes: exact products of what the
+//               operands hold (elements to 2^-17 of their row's largest) at the
 //               time of one 16-bit pass, and no conversion of K.
 //   O += P V    kind::f16: P from tensor memory, over the columns of S; V converted
 //               from e4m3 by two warps, scaled by its token's scale relative
@@ -25,13 +26,13 @@
 // of the softmax's time a row (800 cycles beside another warp) that was 140.  Where a tile's value scales
 // differ by more than 2^11 its tokens' own log2 scales join the exponents instead.
 //
-// A pair of 128 x 128 tiles (two query tiles over 128 tokens) takes 3450 cycles
+// A pair of 128 x 128 tiles (two query tiles over 128 tokens) takes 3400 cycles
 // against 2090 of the MMAs alone: a query tile's scores wait for its weights, which
 // stand in their place, so that its softmax (1630 cycles, and 480 until the last
 // of its four warps has finished) and its MMAs (1050) take turns, and the other
 // tile's turns fill what gaps they can.  4096 tokens of 64 / 8 heads of 128 at a
-// context of 16384: 1.49 ms, 1290 TFLOP/s (4 D flop a score; the queries' second
-// part not counted), 0.68 of the measured bf16 rate.  A block costs 15000 cycles
+// context of 16384: 1.42 to 1.48 ms, 1300 to 1350 TFLOP/s (4 D flop a score; the queries'
+// second part not counted), 0.68 to 0.71 of the measured bf16 rate.  A block costs 15000 cycles
 // besides (queries, first scores, output).
 //
 // As in the kernel for few rows, the tiles of all blocks form one line (with
@@ -64,7 +65,7 @@ constexpr int kBlockRows = 2 * kTile;
 // 208 and 88 a thread after they are handed around.
 constexpr int kTileThreads = 384;
 constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpConv = 10, kConvWarps = 2;
-constexpr int kBlockCost = 8;              // (places of a block besides its tiles' pairs (3450 cycles): 15000 cycles, more where parts are joined;
+constexpr int kBlockCost = 8;              // (places of a block besides its tiles' pairs (3400 cycles): 15000 cycles, more where parts are joined;
                                            // 5 to 10 time alike, 12 is 3% slower on a mixed batch)
 constexpr int kSeqChunk = 2048;            // sequences whose tile counts are held at once
 constexpr int kKStages = 3, kVStages = 2, kFStages = 2, kScSlots = 4;
@@ -146,7 +147,8 @@ __device__ __forceinline__ int32_t block_tiles(const AttnArgs& a, const SeqBlock
 }
 
 // Query tiles of row block rb that hold rows: a sequence's last block may need only the first (16 sequences of 5
-// tokens at 8192, 40 rows each: 132 us against 152 with the empty tile computed beside it).
+// tokens at 8192, 40 rows each: 132 us against 152 with the empty tile computed beside it, by events around single
+// calls; 118 now, back to back).
 __device__ __forceinline__ int block_query_tiles(const AttnArgs& a, const SeqBlocks& w, int rb) {
   return static_cast<int64_t>(w.q_len) * a.group - static_cast<int64_t>(rb) * kBlockRows > kTile ? 2 : 1;
 }

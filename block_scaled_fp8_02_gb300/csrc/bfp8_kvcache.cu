@@ -10,9 +10,10 @@
 // tokens, those beyond it are the grid's second dimension.  Bound by memory:
 // write 2 bytes in and 1 + 4 / head_dim out an element (bf16), read the other
 // way round; reading 65536 tokens of 8 heads of 128 takes 65 us, 0.92 of the
-// measured copy rate, writing 8192 of them 15.6 us, 0.48 of it, held up by the
-// arithmetic that makes every code the correctly rounded quotient's (11 million
-// warp instructions, of which the two conversions a pair are the dearest).
+// measured copy rate, writing 8192 of them 15.4 us, 0.49 of it, held up by the
+// latency of the loads of one token a thread and, beside it, by the arithmetic that
+// makes every code the correctly rounded quotient's (10 million warp instructions,
+// issue slots 47 % full).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

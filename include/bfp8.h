@@ -532,7 +532,8 @@ bfp8_status bfp8_kv_cache_read(const bfp8_kv_cache* cache, const int64_t* slots,
  * A row that sees no token (q_len > kv_lens[b], an empty context) gets out = 0
  * and lse = -infinity.  Queries, keys and values that are not finite reach only
  * the rows that see them.  Softmax and sums are fp32; the products run on the
- * tensor cores from the exact bf16 queries and e4m3 codes, with the weights
+ * tensor cores from the e4m3 codes and the bf16 queries (elements smaller than
+ * 2^-17 of their row's largest may be lost), with the weights
  * rounded to fp16 (11 bits) for the second product.
  *   q, out   bf16 [total_q, num_heads, head_dim] with token and head strides
  *            in elements (element stride 1; 16-byte aligned pointers and
