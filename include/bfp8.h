@@ -463,7 +463,9 @@ bfp8_status bfp8_rmsnorm_quant(const void* x, int in_dtype, int64_t ld_x, const 
 
 /*
  * A paged cache of keys and values in e4m3, one fp32 scale per (token, kv
- * head): value = code * scale, scales not negative.  Token `o` of page `p`, kv head `h`:
+ * head): value = code * scale, scales not negative (the attention takes scales
+ * of values from 2^-95 to 2^126, and 0; those that bfp8_kv_cache_write makes
+ * of finite rows lie between 2^-43 and 2^120).  Token `o` of page `p`, kv head `h`:
  *   codes  k + p * stride_page + h * stride_head + o * stride_token, head_dim bytes
  *   scale  k_scale[p * scale_stride_page + h * scale_stride_head + o]
  * and the same offsets in v and v_scale.  A slot is p * page_size + o.
