@@ -37,6 +37,8 @@ EXPORTS = ("bfp8_group_quant", "bfp8_group_quant_ex", "bfp8_scale_ceil_ue8m0", "
            "bfp8_gemm_grouped_workspace_size", "bfp8_gemm_fused", "bfp8_gemm_fused_workspace_size",
            "bfp8_linear", "bfp8_linear_workspace_size", "bfp8_rmsnorm_quant", "bfp8_kv_cache_write",
            "bfp8_kv_cache_read", "bfp8_paged_attention", "bfp8_paged_attention_workspace_size",
+           "bfp8_shared_prefix_attention", "bfp8_shared_prefix_attention_workspace_size", "bfp8_kv_cache_weigh",
+           "bfp8_kv_cache_weigh_workspace_size", "bfp8_kv_cache_evict", "bfp8_kv_cache_evict_workspace_size",
            "bfp8_stream_capture_id")
 
 
@@ -81,10 +83,28 @@ class AttentionArgs(ctypes.Structure):
                 ("causal", ctypes.c_int), ("window", ctypes.c_int), ("reserved", ctypes.c_int)]
 
 
-# The two structures as packed bytes: half the host time of filling a ctypes Structure field by field.
+class PrefixArgs(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("max_pages", ctypes.c_int),
+                ("prefixes", ctypes.c_int), ("cu_q", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("max_q_len", ctypes.c_int), ("reserved", ctypes.c_int), ("max_len", ctypes.c_int64)]
+
+
+class EvictArgs(ctypes.Structure):
+    _fields_ = [("weights", ctypes.c_void_p), ("weights_stride_page", ctypes.c_int64),
+                ("weights_stride_head", ctypes.c_int64), ("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+                ("out_table", ctypes.c_void_p), ("ld_out", ctypes.c_int64), ("max_pages", ctypes.c_int),
+                ("max_out_pages", ctypes.c_int), ("kv_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p),
+                ("max_kv_len", ctypes.c_int64), ("budget", ctypes.c_int64), ("recent", ctypes.c_int64),
+                ("first", ctypes.c_int64), ("batch", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
+# The structures as packed bytes: half the host time of filling a ctypes Structure field by field.
 _pack_cache = struct.Struct("@PPPPqiiiiqqqqq")
 _pack_attention = struct.Struct("@PPPqiiqqqqPqiiqPPfiii")
+_pack_prefix = struct.Struct("@PqiiPPiiq")
+_pack_evict = struct.Struct("@PqqPqPqiiPPqqqqii")
 assert _pack_cache.size == ctypes.sizeof(KVCacheDesc) and _pack_attention.size == ctypes.sizeof(AttentionArgs)
+assert _pack_prefix.size == ctypes.sizeof(PrefixArgs) and _pack_evict.size == ctypes.sizeof(EvictArgs)
 
 _lock = threading.Lock()
 _lib = None
@@ -166,6 +186,18 @@ def lib():
             L.bfp8_paged_attention.argtypes = [P, P, P, sz, P]
             L.bfp8_paged_attention_workspace_size.restype = i32
             L.bfp8_paged_attention_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
+            L.bfp8_shared_prefix_attention.restype = i32
+            L.bfp8_shared_prefix_attention.argtypes = [P, P, P, P, sz, P]
+            L.bfp8_shared_prefix_attention_workspace_size.restype = i32
+            L.bfp8_shared_prefix_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32, i64, ctypes.POINTER(sz)]
+            L.bfp8_kv_cache_weigh.restype = i32
+            L.bfp8_kv_cache_weigh.argtypes = [P, P, P, i64, i64, i32, P, sz, P]
+            L.bfp8_kv_cache_weigh_workspace_size.restype = i32
+            L.bfp8_kv_cache_weigh_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
+            L.bfp8_kv_cache_evict.restype = i32
+            L.bfp8_kv_cache_evict.argtypes = [P, P, P, sz, P]
+            L.bfp8_kv_cache_evict_workspace_size.restype = i32
+            L.bfp8_kv_cache_evict_workspace_size.argtypes = [i32, i32, i64, i64, ctypes.POINTER(sz)]
             L.bfp8_stream_capture_id.restype = i32
             L.bfp8_stream_capture_id.argtypes = [P, ctypes.POINTER(ctypes.c_ulonglong)]
             _lib = L
@@ -764,6 +796,38 @@ def _attention_workspace(device, num_heads: int, num_kv_heads: int, head_dim: in
     return bfp8_paged_attention_workspace_size(num_heads, num_kv_heads, head_dim, max_q_len)
 
 
+def _check_query(q: torch.Tensor, cache: KVCache) -> None:
+    D = cache.k.shape[3]
+    if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
+        raise ValueError(f"q must be bfloat16 [total_q, heads, {D}] with unit inner stride")
+
+
+def _check_context(table: torch.Tensor, cu_q: torch.Tensor, lens: torch.Tensor, names=("block_table", "cu_q", "kv_lens")):
+    """Checks the tables and lengths of sequences (or prefixes); how many there are, the table's row stride and width."""
+    ts, tst = table.shape, table.stride()
+    if lens.dim() != 1 or cu_q.shape != (len(lens) + 1,) or not lens.is_contiguous() or not cu_q.is_contiguous():
+        raise ValueError(f"{names[2]} must be a contiguous [batch] tensor and {names[1]} a contiguous [batch + 1] one")
+    B = len(lens)
+    if len(ts) != 2 or ts[0] != B or (B > 0 and ts[1] > 1 and tst[1] != 1):
+        raise ValueError(f"{names[0]} must be [{B}, max_pages] with unit inner stride")
+    if table.dtype != torch.int32 or cu_q.dtype != torch.int32 or lens.dtype != torch.int32:
+        raise ValueError(f"{', '.join(names[:2])} and {names[2]} must be int32")
+    return B, tst[0] if B > 1 else ts[1], ts[1]
+
+
+def _workspace(need: int, dev, stream, sp: int) -> torch.Tensor:
+    """workspace_for without its lookups where the stream's buffer will do."""
+    ws = _ws_cache.get((dev.index, sp))
+    if ws is None or ws.numel() < need or _capture_id(stream, sp):
+        ws = workspace_for(need, dev, stream)
+    return ws
+
+
+def _axis(T: int, n: int, D: int, st) -> tuple[int, int]:
+    """Token and head strides; the stride of an axis of one means nothing: any will do."""
+    return D if T == 1 else st[0], D if n == 1 else st[1]
+
+
 def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
                          kv_lens: torch.Tensor, max_q_len: int, max_kv_len: int, scale: float | None = None,
                          causal: bool = True, window: int = 0, return_lse: bool = False,
@@ -773,19 +837,11 @@ def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
     (int32 [batch], the new ones included) on the pages block_table[b] (int32 [batch, max_pages]).  max_q_len and
     max_kv_len bound the lengths; scale defaults to head_dim ** -0.5.  Returns out (bf16, like q), or (out, lse)
     with lse fp32 [total_q, heads]."""
+    _check_query(q, cache)
     _, H, _, D = cache.k.shape
     qs, dev = q.shape, q.device
-    if len(qs) != 3 or qs[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
-        raise ValueError(f"q must be bfloat16 [total_q, heads, {D}] with unit inner stride")
     T, Hq, _ = qs
-    ts, tst = block_table.shape, block_table.stride()
-    if kv_lens.dim() != 1 or cu_q.shape != (len(kv_lens) + 1,) or not kv_lens.is_contiguous() or not cu_q.is_contiguous():
-        raise ValueError("kv_lens must be a contiguous [batch] tensor and cu_q a contiguous [batch + 1] one")
-    B = len(kv_lens)
-    if len(ts) != 2 or ts[0] != B or (B > 0 and ts[1] > 1 and tst[1] != 1):
-        raise ValueError(f"block_table must be [{B}, max_pages] with unit inner stride")
-    if block_table.dtype != torch.int32 or cu_q.dtype != torch.int32 or kv_lens.dtype != torch.int32:
-        raise ValueError("block_table, cu_q and kv_lens must be int32")
+    B, ld_table, width = _check_context(block_table, cu_q, kv_lens)
     if out is None:
         out = torch.empty(qs, dtype=torch.bfloat16, device=dev)
     elif out.shape != qs or out.dtype != torch.bfloat16 or out.stride(2) != 1:
@@ -794,23 +850,167 @@ def bfp8_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
     sp = _stream_of(stream)
     if workspace is None:
-        need = _attention_workspace(dev, Hq, H, D, min(max_q_len, _LONG_Q)) if T and B else 0
-        workspace = _ws_cache.get((dev.index, sp))
-        if workspace is None or workspace.numel() < need or _capture_id(stream, sp):
-            workspace = workspace_for(need, dev, stream)
-        ws_bytes = workspace.numel()
-    else:
-        ws_bytes = workspace.numel() * workspace.element_size()
-    (qt, qh, _), (ot, oh, _) = q.stride(), out.stride()
-    if T == 1:                                 # the stride of an axis of one means nothing: any will do
-        qt = ot = D
-    if Hq == 1:
-        qh = oh = D
+        workspace = _workspace(_attention_workspace(dev, Hq, H, D, min(max_q_len, _LONG_Q)) if T and B else 0, dev, stream, sp)
+    (qt, qh), (ot, oh) = _axis(T, Hq, D, q.stride()), _axis(T, Hq, D, out.stride())
     a = _pack_attention.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0, T, Hq, B, qt, qh,
-                      ot, oh, block_table.data_ptr(), tst[0] if B > 1 else ts[1], ts[1], max_q_len,
+                      ot, oh, block_table.data_ptr(), ld_table, width, max_q_len,
                       max_kv_len, cu_q.data_ptr(), kv_lens.data_ptr(), D ** -0.5 if scale is None else scale,
                       causal, window, 0)
-    _check((_lib or lib()).bfp8_paged_attention(a, cache._desc, workspace.data_ptr(), ws_bytes,
-                                                sp),
+    _check((_lib or lib()).bfp8_paged_attention(a, cache._desc, workspace.data_ptr(),
+                                                workspace.numel() * workspace.element_size(), sp),
            "bfp8_paged_attention")
     return (out, lse) if return_lse else out
+
+
+def bfp8_shared_prefix_attention_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int, max_prefix_q_len: int,
+                                                max_q_len: int, total_q: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().bfp8_shared_prefix_attention_workspace_size(num_heads, num_kv_heads, head_dim, max_prefix_q_len, max_q_len,
+                                                             total_q, ctypes.byref(n)),
+           "bfp8_shared_prefix_attention_workspace_size")
+    return int(n.value)
+
+
+# Of the scratch of both parts; what the rows take is added for each call.
+@functools.lru_cache(maxsize=None)
+def _shared_workspace(device, num_heads: int, num_kv_heads: int, head_dim: int, max_prefix_q_len: int, max_q_len: int) -> int:
+    return bfp8_shared_prefix_attention_workspace_size(num_heads, num_kv_heads, head_dim, max_prefix_q_len, max_q_len, 0)
+
+
+def bfp8_shared_prefix_attention(q: torch.Tensor, cache: KVCache, prefix_table: torch.Tensor, prefix_cu_q: torch.Tensor,
+                                 prefix_lens: torch.Tensor, max_prefix_q_len: int, max_prefix_len: int,
+                                 block_table: torch.Tensor, cu_q: torch.Tensor, kv_lens: torch.Tensor, max_q_len: int,
+                                 max_kv_len: int, scale: float | None = None, causal: bool = True,
+                                 return_lse: bool = False, out: torch.Tensor | None = None,
+                                 workspace: torch.Tensor | None = None, stream=None):
+    """bfp8_paged_attention for sequences that begin with the same text, whose tokens are read once for all of
+    them: prefix f's prefix_lens[f] tokens (int32 [prefixes]), on the pages prefix_table[f] (int32 [prefixes, max_pages]),
+    are seen by the rows prefix_cu_q[f] .. prefix_cu_q[f+1] of q (int32 [prefixes + 1]; max_prefix_q_len bounds how many
+    they are, max_prefix_len the lengths).  block_table, cu_q, kv_lens and their bounds are those of the sequences' own
+    tokens behind the prefix.  Returns out or (out, lse), of one softmax over both parts."""
+    _check_query(q, cache)
+    _, H, _, D = cache.k.shape
+    qs, dev = q.shape, q.device
+    T, Hq, _ = qs
+    B, ld_table, width = _check_context(block_table, cu_q, kv_lens)
+    F, ld_prefix, prefix_width = _check_context(prefix_table, prefix_cu_q, prefix_lens,
+                                                ("prefix_table", "prefix_cu_q", "prefix_lens"))
+    if out is None:
+        out = torch.empty(qs, dtype=torch.bfloat16, device=dev)
+    elif out.shape != qs or out.dtype != torch.bfloat16 or out.stride(2) != 1:
+        raise ValueError("out must be bfloat16, shaped like q, with unit inner stride")
+    _on(dev, cache.k, prefix_table, prefix_cu_q, prefix_lens, block_table, cu_q, kv_lens, out, workspace)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    sp = _stream_of(stream)
+    if workspace is None:
+        need = 0
+        if T and B:
+            mq = min(max_q_len, _LONG_Q)
+            need = _shared_workspace(dev, Hq, H, D, min(max_prefix_q_len, _LONG_Q) if F else mq, mq) + 4 * T * Hq * (D + 1)
+        workspace = _workspace(need, dev, stream, sp)
+    (qt, qh), (ot, oh) = _axis(T, Hq, D, q.stride()), _axis(T, Hq, D, out.stride())
+    a = _pack_attention.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0, T, Hq, B, qt, qh,
+                             ot, oh, block_table.data_ptr(), ld_table, width, max_q_len, max_kv_len, cu_q.data_ptr(),
+                             kv_lens.data_ptr(), D ** -0.5 if scale is None else scale, causal, 0, 0)
+    f = _pack_prefix.pack(prefix_table.data_ptr(), ld_prefix, prefix_width, F, prefix_cu_q.data_ptr(),
+                          prefix_lens.data_ptr(), max_prefix_q_len, 0, max_prefix_len)
+    _check((_lib or lib()).bfp8_shared_prefix_attention(a, f, cache._desc, workspace.data_ptr(),
+                                                        workspace.numel() * workspace.element_size(), sp),
+           "bfp8_shared_prefix_attention")
+    return (out, lse) if return_lse else out
+
+
+def _weight_strides(weights: torch.Tensor, cache: KVCache) -> tuple[int, int]:
+    """Page and head strides of the sums of a cache's tokens."""
+    P, H, page, _ = cache.k.shape
+    if weights.shape != (P, H, page) or weights.dtype != torch.float32 or weights.stride(2) != 1:
+        raise ValueError(f"weights must be float32 [{P}, {H}, {page}] with unit inner stride")
+    sp, sh, _ = weights.stride()
+    return sp if P > 1 else max(sp, H * page), sh if H > 1 else max(sh, page)
+
+
+def bfp8_kv_cache_weigh_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int, max_q_len: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().bfp8_kv_cache_weigh_workspace_size(num_heads, num_kv_heads, head_dim, max_q_len, ctypes.byref(n)),
+           "bfp8_kv_cache_weigh_workspace_size")
+    return int(n.value)
+
+
+@functools.lru_cache(maxsize=None)
+def _weigh_workspace(device, num_heads: int, num_kv_heads: int, head_dim: int, max_q_len: int) -> int:
+    return bfp8_kv_cache_weigh_workspace_size(num_heads, num_kv_heads, head_dim, max_q_len)
+
+
+def bfp8_kv_cache_weigh(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, weights: torch.Tensor,
+                        block_table: torch.Tensor, cu_q: torch.Tensor, kv_lens: torch.Tensor, max_q_len: int,
+                        max_kv_len: int, scale: float | None = None, causal: bool = True, window: int = 0,
+                        accumulate: bool = True, workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Adds to weights [pages, kv_heads, page_size] (fp32) the attention weight that each cached token receives from
+    the new tokens q, summed over them and over the query heads of a kv head.  lse [total_q, heads] (fp32) is what
+    bfp8_paged_attention or bfp8_shared_prefix_attention returned for the same q; the other arguments are as
+    there.  With accumulate the sums of the new tokens begin here (causal) and those of the earlier ones go on; without
+    it all sums of the context begin here."""
+    _check_query(q, cache)
+    _, H, _, D = cache.k.shape
+    T, Hq, _ = q.shape
+    dev = q.device
+    B, ld_table, width = _check_context(block_table, cu_q, kv_lens)
+    if lse.shape != (T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape ({T}, {Hq})")
+    wp, wh = _weight_strides(weights, cache)
+    _on(dev, lse, cache.k, weights, block_table, cu_q, kv_lens, workspace)
+    sp = _stream_of(stream)
+    if workspace is None:
+        workspace = _workspace(_weigh_workspace(dev, Hq, H, D, min(max_q_len, _LONG_Q)) if T and B else 0, dev, stream, sp)
+    qt, qh = _axis(T, Hq, D, q.stride())
+    a = _pack_attention.pack(q.data_ptr(), 0, lse.data_ptr(), T, Hq, B, qt, qh, 0, 0, block_table.data_ptr(), ld_table,
+                             width, max_q_len, max_kv_len, cu_q.data_ptr(), kv_lens.data_ptr(),
+                             D ** -0.5 if scale is None else scale, causal, window, 0)
+    _check((_lib or lib()).bfp8_kv_cache_weigh(a, cache._desc, weights.data_ptr(), wp, wh, int(accumulate),
+                                               workspace.data_ptr(), workspace.numel() * workspace.element_size(), sp),
+           "bfp8_kv_cache_weigh")
+
+
+def bfp8_kv_cache_evict_workspace_size(batch: int, num_kv_heads: int, max_kv_len: int, budget: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().bfp8_kv_cache_evict_workspace_size(batch, num_kv_heads, max_kv_len, budget, ctypes.byref(n)),
+           "bfp8_kv_cache_evict_workspace_size")
+    return int(n.value)
+
+
+def bfp8_kv_cache_evict(cache: KVCache, weights: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                        max_kv_len: int, budget: int, recent: int = 0, first: int = 0,
+                        out_table: torch.Tensor | None = None, new_lens: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Shortens sequences to budget tokens: every kv head keeps its first `first`, its last `recent` and of the others
+    the heaviest by weights [pages, kv_heads, page_size] (fp32, as bfp8_kv_cache_weigh sums them), in their order.
+    They move with codes, scales and weights to the pages out_table (int32 [batch, max_pages], none of them among
+    those of block_table; shorter sequences are copied whole), or, without one, to the first pages of block_table.
+    Returns the new lengths min(kv_lens, budget) (int32 [batch], into new_lens if given; not kv_lens itself)."""
+    _, H, page, _ = cache.k.shape
+    wp, wh = _weight_strides(weights, cache)
+    if kv_lens.dim() != 1 or kv_lens.dtype != torch.int32 or not kv_lens.is_contiguous():
+        raise ValueError("kv_lens must be a contiguous [batch] int32 tensor")
+    B, dev = len(kv_lens), kv_lens.device
+
+    def table(t, name):
+        if t.dim() != 2 or t.shape[0] != B or t.dtype != torch.int32 or (B > 0 and t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be int32 [{B}, max_pages] with unit inner stride")
+        return t.data_ptr(), t.stride(0) if B > 1 else t.shape[1], t.shape[1]
+
+    tp, ld, width = table(block_table, "block_table")
+    op, ld_out, out_width = (0, 0, 0) if out_table is None else table(out_table, "out_table")
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    elif new_lens.shape != (B,) or new_lens.dtype != torch.int32 or not new_lens.is_contiguous():
+        raise ValueError(f"new_lens must be a contiguous [{B}] int32 tensor")
+    _on(dev, cache.k, weights, block_table, out_table, new_lens, workspace)
+    sp = _stream_of(stream)
+    if workspace is None:
+        need = bfp8_kv_cache_evict_workspace_size(B, H, max_kv_len, budget) if B else 0
+        workspace = _workspace(need, dev, stream, sp)
+    a = _pack_evict.pack(weights.data_ptr(), wp, wh, tp, ld, op, ld_out, width, out_width, kv_lens.data_ptr(),
+                         new_lens.data_ptr(), max_kv_len, budget, recent, first, B, 0)
+    _check((_lib or lib()).bfp8_kv_cache_evict(a, cache._desc, workspace.data_ptr(),
+                                               workspace.numel() * workspace.element_size(), sp), "bfp8_kv_cache_evict")
+    return new_lens

@@ -25,15 +25,6 @@ bfp8_status bad(const char* fmt, V... v) {
 // cost the same from 33 rows to 128.
 constexpr int kFewRows = 32;
 
-bfp8_status check_heads(int heads, int kv_heads, int dim, int max_q) {
-  if (kv_heads < 1 || heads < kv_heads || heads > 65535 || heads % kv_heads != 0)
-    return bad("num_heads = %d is not a multiple of num_kv_heads = %d (at most 65535)", heads, kv_heads);
-  if (heads / kv_heads > 128) return bad("%d query heads a kv head (at most 128)", heads / kv_heads);
-  if (dim != 64 && dim != 128) return bad("head_dim = %d (expected 64 or 128)", dim);
-  if (max_q < 1 || max_q > (1 << 24)) return bad("max_q_len = %d (expected 1 .. 2^24)", max_q);
-  return BFP8_OK;
-}
-
 // Rows of a sequence up to which the kernel for few rows takes it, as a count
 // of eights: all sequences when even the longest is that short, else those of
 // a single token (a batch of chunks and decoding sequences).
@@ -55,7 +46,146 @@ size_t workspace_bytes_for(int group, int dim, int max_q, int sms) {
          (has_many(group, max_q) ? attn_tile_partial_bytes(dim, sms) : 0);
 }
 
+// The prefixes' part of every row, behind what either part's kernels take.
+size_t shared_scratch_bytes(int group, int dim, int max_prefix_q, int max_q, int sms) {
+  const size_t a = workspace_bytes_for(group, dim, max_prefix_q, sms), b = workspace_bytes_for(group, dim, max_q, sms);
+  return a > b ? a : b;
+}
+size_t shared_rows_bytes(int64_t total_q, int heads, int dim) {
+  return static_cast<size_t>(total_q) * heads * (dim + 1) * sizeof(float);
+}
+
+// Sequences (or prefixes), rows and context of a call, checked apart from the pointers.
+bfp8_status check_context(const char* what, int batch, int max_q, int max_pages, int64_t ld_table, int64_t max_kv, int page,
+                          bool empty) {
+  if (batch < 0 || batch > 65535) return bad("%s: %d (expected 0 .. 65535)", what, batch);
+  if (max_q < (empty ? 0 : 1) || max_q > (1 << 24)) return bad("%s: max_q_len = %d (expected 1 .. 2^24)", what, max_q);
+  if (max_pages < (empty ? 0 : 1) || ld_table < max_pages)
+    return bad("%s: max_pages = %d, ld_table = %lld", what, max_pages, (long long)ld_table);
+  if (max_kv < 0 || max_kv > (int64_t{1} << 30)) return bad("%s: bound of lengths = %lld (expected 0 .. 2^30)", what, (long long)max_kv);
+  if (max_kv > static_cast<int64_t>(max_pages) * page)
+    return bad("%s: bound of lengths = %lld exceeds max_pages * page_size", what, (long long)max_kv);
+  return BFP8_OK;
+}
+
+// The device, and a workspace of `need(sms)` bytes.
+template <typename Need>
+bfp8_status check_workspace(const void* workspace, size_t bytes, int* sms, int** err, Need need) {
+  const bfp8_status st = device_for_call(sms, err);
+  if (st != BFP8_OK) {
+    // a host without a device still learns of a missing workspace
+    if (!workspace || bytes < kCounterHeaderBytes || off_align(workspace, 256))
+      return set_last_errorf(BFP8_ERR_WORKSPACE, "workspace missing, too small or not 256-byte aligned");
+    return st;
+  }
+  const size_t n = need(*sms);
+  if (!workspace || bytes < n) return set_last_errorf(BFP8_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", bytes, n);
+  if (off_align(workspace, 256)) return set_last_errorf(BFP8_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  return BFP8_OK;
+}
+
+// Launches what one part takes: the kernel for many rows, that for few, or both.  after_tile: a tile kernel of
+// the prefixes' part is the launch before, and this part (kAttnOwn) needs it only where rows are joined.
+// *last_tile: the last launch is the tile kernel's.
+bfp8_status launch_part(AttnArgs a, AttnMode mode, int sms, void* workspace, bool after_tile, cudaStream_t cs,
+                        bool* last_tile) {
+  const int groups = few_groups(a.group, a.max_q);
+  a.few_rows = groups * 8;
+  const uint64_t dims[4] = {static_cast<uint64_t>(a.c.dim), static_cast<uint64_t>(a.c.page_size),
+                            static_cast<uint64_t>(a.c.heads), static_cast<uint64_t>(a.c.num_pages)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(a.c.st_tok), static_cast<uint64_t>(a.c.st_head),
+                               static_cast<uint64_t>(a.c.st_page)};
+  const uint32_t box[4] = {static_cast<uint32_t>(a.c.dim),
+                           static_cast<uint32_t>(a.c.page_size < 128 ? a.c.page_size : 128), 1u, 1u};
+  CUtensorMap mk, mv;
+  bfp8_status st;
+  if ((st = encode_bytes_tiled(&mk, a.c.k, 4, dims, strides, box, a.c.dim)) != BFP8_OK) return st;
+  if ((st = encode_bytes_tiled(&mv, a.c.v, 4, dims, strides, box, a.c.dim)) != BFP8_OK) return st;
+  int32_t* counters = static_cast<int32_t*>(workspace);
+  char* partials = static_cast<char*>(workspace) + kCounterHeaderBytes;
+  cudaError_t e = cudaSuccess;
+  // Can a sequence be short enough for the kernel for few rows?  Not if the others at their longest leave this
+  // one too many tokens (always so for a single chunk): then its launch is saved.
+  const bool many = has_many(a.group, a.max_q);
+  const bool few = a.group <= kFewRows &&
+                   (!many || a.total_q <= static_cast<int64_t>(a.batch - 1) * a.max_q + a.few_rows / a.group);
+  if (!few) a.few_rows = 0;
+  if (many)
+    e = launch_attn_tile(mk, mv, a, mode, sms, counters + sms,
+                         reinterpret_cast<float*>(partials + few_bytes(a.group, a.c.dim, a.max_q, sms)), cs);
+  if (e == cudaSuccess && few)
+    e = launch_attn_decode(mk, mv, a, mode, groups, sms, counters, reinterpret_cast<float*>(partials),
+                           many ? 1 : after_tile ? 2 : 0, cs);
+  if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
+  *last_tile = !few;
+  return BFP8_OK;
+}
+
 }  // namespace
+
+bfp8_status check_heads(int heads, int kv_heads, int dim, int max_q) {
+  if (kv_heads < 1 || heads < kv_heads || heads > 65535 || heads % kv_heads != 0)
+    return bad("num_heads = %d is not a multiple of num_kv_heads = %d (at most 65535)", heads, kv_heads);
+  if (heads / kv_heads > 128) return bad("%d query heads a kv head (at most 128)", heads / kv_heads);
+  if (dim != 64 && dim != 128) return bad("head_dim = %d (expected 64 or 128)", dim);
+  if (max_q < 1 || max_q > (1 << 24)) return bad("max_q_len = %d (expected 1 .. 2^24)", max_q);
+  return BFP8_OK;
+}
+
+bfp8_status check_attention(const bfp8_attention_args* p, AttnArgs* a, bool* empty, bool needs_out) {
+  if (!p) return bad("args is null");
+  // an empty call's bounds may be zero
+  *empty = p->batch == 0 || p->total_q == 0;
+  bfp8_status st = check_heads(p->num_heads, a->c.heads, a->c.dim, *empty && p->max_q_len == 0 ? 1 : p->max_q_len);
+  if (st != BFP8_OK) return st;
+  if (p->batch < 0 || p->batch > 65535 || p->total_q < 0 || p->total_q >= (int64_t{1} << 31))
+    return bad("batch = %d, total_q = %lld", p->batch, (long long)p->total_q);
+  if (p->max_pages < (*empty ? 0 : 1) || p->ld_table < p->max_pages)
+    return bad("max_pages = %d, ld_table = %lld", p->max_pages, (long long)p->ld_table);
+  if (p->max_kv_len < 0 || p->max_kv_len > (int64_t{1} << 30))
+    return bad("max_kv_len = %lld (expected 0 .. 2^30)", (long long)p->max_kv_len);
+  if (p->max_kv_len > static_cast<int64_t>(p->max_pages) * a->c.page_size)
+    return bad("max_kv_len = %lld exceeds max_pages * page_size", (long long)p->max_kv_len);
+  if (!std::isfinite(p->softmax_scale)) return bad("softmax_scale is not finite");
+  if (p->causal != 0 && p->causal != 1) return bad("causal = %d (expected 0 or 1)", p->causal);
+  if (p->window < 0) return bad("window = %d (expected >= 0)", p->window);
+  if (*empty) return BFP8_OK;
+  if (!p->q || (needs_out && !p->out) || !p->block_table || !p->cu_q || !p->kv_lens)
+    return bad("null pointer (q=%p out=%p block_table=%p cu_q=%p kv_lens=%p)", p->q, p->out,
+               (const void*)p->block_table, (const void*)p->cu_q, (const void*)p->kv_lens);
+  const int64_t o_st = needs_out ? p->out_stride_token : a->c.dim, o_sh = needs_out ? p->out_stride_head : a->c.dim;
+  for (int64_t s : {p->q_stride_token, p->q_stride_head, o_st, o_sh})
+    if (s < 0) return bad("negative stride %lld", (long long)s);
+  if (o_sh < a->c.dim || o_st < a->c.dim) return bad("out strides must be >= head_dim");
+  for (int64_t s : {p->q_stride_token, p->q_stride_head, o_st, o_sh})
+    if (s % 8) return set_last_errorf(BFP8_ERR_ALIGNMENT, "q and out strides must be multiples of 8 elements");
+  if (off_align(p->q, 16) || (needs_out && off_align(p->out, 16)) || off_align(p->lse, 4) || off_align(p->block_table, 4) ||
+      off_align(p->cu_q, 4) || off_align(p->kv_lens, 4))
+    return set_last_errorf(BFP8_ERR_ALIGNMENT, "q and out must be 16-byte aligned, the rest 4-byte");
+  a->group = p->num_heads / a->c.heads;
+  a->q = static_cast<const __nv_bfloat16*>(p->q);
+  a->out = needs_out ? static_cast<__nv_bfloat16*>(p->out) : nullptr;
+  a->lse = p->lse;
+  a->q_st = p->q_stride_token;
+  a->q_sh = p->q_stride_head;
+  a->o_st = o_st;
+  a->o_sh = o_sh;
+  a->table = p->block_table;
+  a->ld_table = p->ld_table;
+  a->cu_q = p->cu_q;
+  a->kv_lens = p->kv_lens;
+  a->total_q = p->total_q;
+  a->max_kv = p->max_kv_len;
+  a->heads = p->num_heads;
+  a->batch = p->batch;
+  a->max_q = p->max_q_len;
+  a->causal = p->causal;
+  // A window past every distance hides nothing.  Positions begin at -max_q_len (more new tokens than context), so
+  // without this p - window + 1 would leave 32 bits for the widest windows.
+  a->window = p->window > p->max_kv_len + p->max_q_len ? 0 : p->window;
+  a->scale = p->softmax_scale;
+  return BFP8_OK;
+}
 
 }  // namespace bfp8
 
@@ -79,94 +209,82 @@ extern "C" bfp8_status bfp8_paged_attention(const bfp8_attention_args* p, const 
   AttnArgs a{};
   bfp8_status st = check_cache(cache, &a.c);
   if (st != BFP8_OK) return st;
-  if (!p) return bad("args is null");
-  // an empty call's bounds may be zero
-  const bool empty = p->batch == 0 || p->total_q == 0;
-  if ((st = check_heads(p->num_heads, a.c.heads, a.c.dim, empty && p->max_q_len == 0 ? 1 : p->max_q_len)) != BFP8_OK)
-    return st;
-  if (p->batch < 0 || p->batch > 65535 || p->total_q < 0 || p->total_q >= (int64_t{1} << 31))
-    return bad("batch = %d, total_q = %lld", p->batch, (long long)p->total_q);
-  if (p->max_pages < (empty ? 0 : 1) || p->ld_table < p->max_pages)
-    return bad("max_pages = %d, ld_table = %lld", p->max_pages, (long long)p->ld_table);
-  if (p->max_kv_len < 0 || p->max_kv_len > (int64_t{1} << 30))
-    return bad("max_kv_len = %lld (expected 0 .. 2^30)", (long long)p->max_kv_len);
-  if (p->max_kv_len > static_cast<int64_t>(p->max_pages) * a.c.page_size)
-    return bad("max_kv_len = %lld exceeds max_pages * page_size", (long long)p->max_kv_len);
-  if (!std::isfinite(p->softmax_scale)) return bad("softmax_scale is not finite");
-  if (p->causal != 0 && p->causal != 1) return bad("causal = %d (expected 0 or 1)", p->causal);
-  if (p->window < 0) return bad("window = %d (expected >= 0)", p->window);
+  bool empty = false;
+  if ((st = check_attention(p, &a, &empty, true)) != BFP8_OK) return st;
   if (empty) return set_last_error(BFP8_OK, "");
-  if (!p->q || !p->out || !p->block_table || !p->cu_q || !p->kv_lens)
-    return bad("null pointer (q=%p out=%p block_table=%p cu_q=%p kv_lens=%p)", p->q, p->out,
-               (const void*)p->block_table, (const void*)p->cu_q, (const void*)p->kv_lens);
-  for (int64_t s : {p->q_stride_token, p->q_stride_head, p->out_stride_token, p->out_stride_head})
-    if (s < 0) return bad("negative stride %lld", (long long)s);
-  if (p->out_stride_head < a.c.dim || p->out_stride_token < a.c.dim)
-    return bad("out strides must be >= head_dim");
-  for (int64_t s : {p->q_stride_token, p->q_stride_head, p->out_stride_token, p->out_stride_head})
-    if (s % 8) return set_last_errorf(BFP8_ERR_ALIGNMENT, "q and out strides must be multiples of 8 elements");
-  if (off_align(p->q, 16) || off_align(p->out, 16) || off_align(p->lse, 4) || off_align(p->block_table, 4) ||
-      off_align(p->cu_q, 4) || off_align(p->kv_lens, 4))
-    return set_last_errorf(BFP8_ERR_ALIGNMENT, "q and out must be 16-byte aligned, the rest 4-byte");
   int sms = 0;
-  if ((st = device_for_call(&sms, &a.err)) != BFP8_OK) {
-    // a host without a device still learns of a missing workspace
-    if (!workspace || workspace_bytes < kCounterHeaderBytes || off_align(workspace, 256))
-      return set_last_errorf(BFP8_ERR_WORKSPACE, "workspace missing, too small or not 256-byte aligned");
+  st = check_workspace(workspace, workspace_bytes, &sms, &a.err,
+                       [&](int n) { return workspace_bytes_for(a.group, a.c.dim, a.max_q, n); });
+  if (st != BFP8_OK) return st;
+  bool tile = false;
+  if ((st = launch_part(a, kAttnWhole, sms, workspace, false, static_cast<cudaStream_t>(stream), &tile)) != BFP8_OK) return st;
+  return set_last_error(BFP8_OK, "");
+}
+
+extern "C" bfp8_status bfp8_shared_prefix_attention_workspace_size(int num_heads, int num_kv_heads, int head_dim,
+                                                                   int max_prefix_q_len, int max_q_len, int64_t total_q,
+                                                                   size_t* bytes) {
+  bfp8_status st = check_heads(num_heads, num_kv_heads, head_dim, max_q_len);
+  if (st == BFP8_OK) st = check_heads(num_heads, num_kv_heads, head_dim, max_prefix_q_len);
+  if (st != BFP8_OK) return st;
+  if (total_q < 0 || total_q >= (int64_t{1} << 31)) return bad("total_q = %lld", (long long)total_q);
+  if (!bytes) return bad("bytes is null");
+  int sms = 0;
+  int* err = nullptr;
+  if ((st = device_for_call(&sms, &err)) != BFP8_OK) return st;
+  *bytes = shared_scratch_bytes(num_heads / num_kv_heads, head_dim, max_prefix_q_len, max_q_len, sms) +
+           shared_rows_bytes(total_q, num_heads, head_dim);
+  return set_last_error(BFP8_OK, "");
+}
+
+extern "C" bfp8_status bfp8_shared_prefix_attention(const bfp8_attention_args* p, const bfp8_prefix_args* f,
+                                                    const bfp8_kv_cache* cache, void* workspace, size_t workspace_bytes,
+                                                    void* stream) {
+  AttnArgs a{};
+  bfp8_status st = check_cache(cache, &a.c);
+  if (st != BFP8_OK) return st;
+  bool empty = false;
+  if ((st = check_attention(p, &a, &empty, true)) != BFP8_OK) return st;
+  if (p->window != 0) return bad("window = %d: a window over a shared prefix is not supported", p->window);
+  if (!f) return bad("prefix is null");
+  const bool none = empty || f->prefixes == 0;
+  if ((st = check_context("prefix", f->prefixes, f->max_q_len, f->max_pages, f->ld_table, f->max_len, a.c.page_size, none)) != BFP8_OK)
     return st;
+  if (empty) return set_last_error(BFP8_OK, "");
+  if (!none) {
+    if (!f->block_table || !f->cu_q || !f->lens)
+      return bad("prefix: null pointer (block_table=%p cu_q=%p lens=%p)", (const void*)f->block_table, (const void*)f->cu_q,
+                 (const void*)f->lens);
+    if (off_align(f->block_table, 4) || off_align(f->cu_q, 4) || off_align(f->lens, 4))
+      return set_last_errorf(BFP8_ERR_ALIGNMENT, "prefix: pointers must be 4-byte aligned");
   }
-  a.group = p->num_heads / a.c.heads;
-  const size_t need = workspace_bytes_for(a.group, a.c.dim, p->max_q_len, sms);
-  if (!workspace || workspace_bytes < need)
-    return set_last_errorf(BFP8_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-  if (off_align(workspace, 256)) return set_last_errorf(BFP8_ERR_WORKSPACE, "workspace is not 256-byte aligned");
-  a.q = static_cast<const __nv_bfloat16*>(p->q);
-  a.out = static_cast<__nv_bfloat16*>(p->out);
-  a.lse = p->lse;
-  a.q_st = p->q_stride_token;
-  a.q_sh = p->q_stride_head;
-  a.o_st = p->out_stride_token;
-  a.o_sh = p->out_stride_head;
-  a.table = p->block_table;
-  a.ld_table = p->ld_table;
-  a.cu_q = p->cu_q;
-  a.kv_lens = p->kv_lens;
-  a.total_q = p->total_q;
-  a.max_kv = p->max_kv_len;
-  a.heads = p->num_heads;
-  a.batch = p->batch;
-  a.max_q = p->max_q_len;
-  a.causal = p->causal;
-  // A window past every distance hides nothing.  Positions begin at -max_q_len (more new tokens than context), so
-  // without this p - window + 1 would leave 32 bits for the widest windows.
-  a.window = p->window > p->max_kv_len + p->max_q_len ? 0 : p->window;
-  a.scale = p->softmax_scale;
-  const int groups = few_groups(a.group, p->max_q_len);
-  a.few_rows = groups * 8;
-  const uint64_t dims[4] = {static_cast<uint64_t>(a.c.dim), static_cast<uint64_t>(a.c.page_size),
-                            static_cast<uint64_t>(a.c.heads), static_cast<uint64_t>(a.c.num_pages)};
-  const uint64_t strides[3] = {static_cast<uint64_t>(a.c.st_tok), static_cast<uint64_t>(a.c.st_head),
-                               static_cast<uint64_t>(a.c.st_page)};
-  const uint32_t box[4] = {static_cast<uint32_t>(a.c.dim),
-                           static_cast<uint32_t>(a.c.page_size < 128 ? a.c.page_size : 128), 1u, 1u};
-  CUtensorMap mk, mv;
-  if ((st = encode_bytes_tiled(&mk, a.c.k, 4, dims, strides, box, a.c.dim)) != BFP8_OK) return st;
-  if ((st = encode_bytes_tiled(&mv, a.c.v, 4, dims, strides, box, a.c.dim)) != BFP8_OK) return st;
+  int sms = 0;
+  const size_t rows = none ? 0 : shared_rows_bytes(a.total_q, a.heads, a.c.dim);
+  const int pq = none ? a.max_q : f->max_q_len;
+  st = check_workspace(workspace, workspace_bytes, &sms, &a.err,
+                       [&](int n) { return shared_scratch_bytes(a.group, a.c.dim, pq, a.max_q, n) + rows; });
+  if (st != BFP8_OK) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  int32_t* counters = static_cast<int32_t*>(workspace);
-  char* partials = static_cast<char*>(workspace) + kCounterHeaderBytes;
-  cudaError_t e = cudaSuccess;
-  // Can a sequence be short enough for the kernel for few rows?  Not if the others at their longest leave this
-  // one too many tokens (always so for a single chunk): then its launch is saved.
-  const bool many = has_many(a.group, p->max_q_len);
-  const bool few = a.group <= kFewRows &&
-                   (!many || p->total_q <= static_cast<int64_t>(p->batch - 1) * p->max_q_len + a.few_rows / a.group);
-  if (!few) a.few_rows = 0;
-  if (many)
-    e = launch_attn_tile(mk, mv, a, sms, counters + sms,
-                         reinterpret_cast<float*>(partials + few_bytes(a.group, a.c.dim, p->max_q_len, sms)), cs);
-  if (e == cudaSuccess && few)
-    e = launch_attn_decode(mk, mv, a, groups, sms, counters, reinterpret_cast<float*>(partials), many, cs);
-  if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
+  bool tile = false;
+  if (!none) {
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + shared_scratch_bytes(a.group, a.c.dim, pq, a.max_q, sms));
+    a.part_lse2 = a.part_o + a.total_q * a.heads * a.c.dim;
+    a.part_cu = f->cu_q;
+    a.prefixes = f->prefixes;
+    AttnArgs b = a;
+    b.out = nullptr;
+    b.lse = nullptr;
+    b.table = f->block_table;
+    b.ld_table = f->ld_table;
+    b.cu_q = f->cu_q;
+    b.kv_lens = f->lens;
+    b.max_kv = f->max_len;
+    b.batch = f->prefixes;
+    b.max_q = f->max_q_len;
+    b.causal = 0;
+    b.window = 0;
+    if ((st = launch_part(b, kAttnPrefix, sms, workspace, false, cs, &tile)) != BFP8_OK) return st;
+  }
+  if ((st = launch_part(a, none ? kAttnWhole : kAttnOwn, sms, workspace, tile, cs, &tile)) != BFP8_OK) return st;
   return set_last_error(BFP8_OK, "");
 }

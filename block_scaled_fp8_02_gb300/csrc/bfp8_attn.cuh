@@ -32,7 +32,42 @@ struct AttnArgs {
   float scale;
   CacheView c;
   int* err;
+  // One of two parts of the rows' contexts (AttnMode): fp32 rows [total_q, heads, dim] over the shared prefixes, their log2
+  // sums [total_q, heads], and the prefixes' bounds [prefixes + 1] among the rows.
+  float* part_o;
+  float* part_lse2;
+  const int32_t* part_cu;
+  int32_t prefixes;
 };
+
+// What a launch computes: attention as it stands; the part over shared prefixes, which goes to part_o and part_lse2; or
+// the part over the sequences' own tokens, joined with that one.
+enum AttnMode : int { kAttnWhole = 0, kAttnPrefix = 1, kAttnOwn = 2 };
+
+// Where the prefix's part of a row stands.
+__device__ __forceinline__ int64_t part_row(const AttnArgs& a, int64_t token, int head) { return token * a.heads + head; }
+
+// A row's own part has the log2 sum lse2; how it and the prefix's part are weighted: with ref the larger log2 sum,
+// w = 2^(lse2 - ref), out = (w1 o1 + w2 o2) / (w1 + w2).  Rows outside every prefix, and parts that see nothing, weigh
+// nothing; a NaN stays one.  Both parts come in fp32, so that the output is rounded once.
+struct Joined {
+  float own, prefix, lse2;
+  bool covered;                 // some prefix's row
+};
+__device__ __forceinline__ Joined join_prefix(const AttnArgs& a, int64_t token, int head, float lse2) {
+  const bool covered = token >= a.part_cu[0] && token < a.part_cu[a.prefixes];
+  const float other = covered ? __ldcg(a.part_lse2 + part_row(a, token, head)) : -INFINITY;
+  float ref = fmaxf(lse2, other);
+  if (ref == -INFINITY) ref = 0.f;
+  const float w1 = exp2f(lse2 - ref), w2 = exp2f(other - ref), sum = w1 + w2;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  Joined j;
+  j.covered = covered;
+  j.own = w1 * inv;
+  j.prefix = w2 * inv;
+  j.lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
+  return j;
+}
 
 // Sequence b: its rows of q and its context, clamped to the bounds, so that no
 // length can lead out of a buffer.
@@ -76,18 +111,24 @@ __device__ __forceinline__ int share_of(int64_t u, int64_t total, int64_t ctas) 
   return static_cast<int>(((u + 1) * ctas - 1) / total);
 }
 
+// Host checks (bfp8_attn.cu) of heads, and of an attention call's arguments, which fill `a` but for its device's part
+// (a->c is filled); needs_out false: out is neither looked at nor taken over.
+bfp8_status check_heads(int heads, int kv_heads, int dim, int max_q);
+bfp8_status check_attention(const bfp8_attention_args* p, AttnArgs* a, bool* empty, bool needs_out);
+
 // The kernel for few rows a sequence (bfp8_attn_decode.cu): `groups` (1 to 4)
 // eights of rows, `ctas` persistent CTAs, counters[ctas] zero.
 // k, v: tensor maps [dim, token, head, page] of bytes, boxes of min(page_size, 128) tokens.
-// behind: the launch before it in the stream is launch_attn_tile's of the same call; the two run beside each other.
+// behind 1: the launch before it in the stream is launch_attn_tile's of the same part; the two run beside each other.
+// behind 2 (kAttnOwn): it is launch_attn_tile's of the prefixes' part, needed only once rows are joined.
 int attn_decode_groups(int64_t rows);
 size_t attn_decode_partial_bytes(int groups, int dim, int ctas);
-cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int groups, int ctas,
-                               int32_t* counters, float* partials, bool behind, cudaStream_t stream);
+cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, AttnMode mode, int groups, int ctas,
+                               int32_t* counters, float* partials, int behind, cudaStream_t stream);
 
 // The kernel for more rows (bfp8_attn_tile.cu); counters[2 * ctas] zero.
 size_t attn_tile_partial_bytes(int dim, int ctas);
-cudaError_t launch_attn_tile(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int ctas, int32_t* counters,
-                             float* partials, cudaStream_t stream);
+cudaError_t launch_attn_tile(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, AttnMode mode, int ctas,
+                             int32_t* counters, float* partials, cudaStream_t stream);
 
 }  // namespace bfp8

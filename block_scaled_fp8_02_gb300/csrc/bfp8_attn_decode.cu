@@ -179,10 +179,10 @@ struct DecodeArgs {
   int32_t* counters;          // one a CTA, zero between calls
   float* partials;            // two slots a CTA: NG * 8 rows of D floats, then their log2 sums
   unsigned long long wait_limit;
-  int32_t behind;             // launched right behind the other kernel, for the same call
+  int32_t behind;             // launched right behind the other kernel: 1 of the same part, 2 of the prefixes'
 };
 
-template <int D, int NG, int RT>
+template <int D, int NG, int RT, int MODE>
 __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ DecodeArgs p) {
@@ -692,6 +692,35 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
     more = next(nx);
     if (more) fetch(nx);
 
+    // rows are joined from here on
+    if constexpr (MODE == kAttnOwn)
+      if (p.behind == 2) griddep_wait();
+    // row r of the item as lane's elements of it, and its log2 sum
+    auto finish = [&](int r, float (&o)[D / 32], float lse2) {
+      const int i = r / a.group, head = c.h * a.group + r - i * a.group;
+      const int64_t token = w.row0 + i;
+      using Vec = typename std::conditional<D == 128, float4, float2>::type;
+      if constexpr (MODE == kAttnPrefix) {
+        Vec x;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) reinterpret_cast<float*>(&x)[e] = o[e];
+        *(reinterpret_cast<Vec*>(a.part_o + part_row(a, token, head) * D) + lane) = x;
+        if (lane == 0) a.part_lse2[part_row(a, token, head)] = lse2;
+      } else {
+        if constexpr (MODE == kAttnOwn) {
+          const Joined j = join_prefix(a, token, head, lse2);
+          Vec x{};
+          if (j.covered) x = __ldcg(reinterpret_cast<const Vec*>(a.part_o + part_row(a, token, head) * D) + lane);
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) o[e] = fmaf(reinterpret_cast<const float*>(&x)[e], j.prefix, o[e] * j.own);
+          lse2 = j.lse2;
+        }
+        __nv_bfloat16* dst = a.out + token * a.o_st + head * a.o_sh + lane * (D / 32);
+        if constexpr (D == 128) st_global_v2(dst, pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+        else *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0], o[1]);
+        if (a.lse != nullptr && lane == 0) a.lse[token * a.heads + head] = lse2 * 0.6931471805599453f;
+      }
+    };
     // ---- the warps' parts of the item, added in warp order, four rows at a time
     const bool whole = c.k0 == 0 && c.k1 == w.units;
     const int slot_id = 2 * blockIdx.x + (c.item0 + c.k0 == u0 ? 0 : 1);
@@ -753,14 +782,7 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
           for (int e = 0; e < D / 32; ++e) o[e] = fmaf(src[e], ci, o[e]);
         }
         if (whole) {
-          const int i = r / a.group, head = c.h * a.group + r - i * a.group;
-          __nv_bfloat16* dst = a.out + (w.row0 + i) * a.o_st + head * a.o_sh + lane * (D / 32);
-          if (ok) {
-            if constexpr (D == 128) st_global_v2(dst, pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-            else *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0], o[1]);
-            if (a.lse != nullptr && lane == 0)
-              a.lse[(w.row0 + i) * a.heads + head] = lse2 * 0.6931471805599453f;
-          }
+          if (ok) finish(r, o, lse2);
         } else {
           if constexpr (D == 128)
             *reinterpret_cast<float4*>(part_o + r * D + lane * 4) = make_float4(o[0], o[1], o[2], o[3]);
@@ -820,16 +842,9 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
             }
           }
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          const int i = r / a.group, head = c.h * a.group + r - i * a.group;
-          __nv_bfloat16* dst = a.out + (w.row0 + i) * a.o_st + head * a.o_sh + lane * (D / 32);
-          if (ok) {
-            if constexpr (D == 128)
-              st_global_v2(dst, pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-            else *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
-            if (a.lse != nullptr && lane == 0)
-              a.lse[(w.row0 + i) * a.heads + head] =
-                  sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
-          }
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) o[e] *= inv;
+          if (ok) finish(r, o, sum == 0.f ? -INFINITY : ref + log2f(sum));
         }
       }
     }
@@ -839,11 +854,11 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
   if (p.behind) griddep_wait();
 }
 
-template <int D, int NG, int RT>
+template <int D, int NG, int RT, int MODE>
 cudaError_t launch_decode_ng(const CUtensorMap& k, const CUtensorMap& v, const DecodeArgs& p, int ctas,
                              cudaStream_t stream) {
   using C = DecCfg<D, NG, RT>;
-  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NG, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NG, RT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -856,7 +871,26 @@ cudaError_t launch_decode_ng(const CUtensorMap& k, const CUtensorMap& v, const D
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, NG, RT>, k, v, p);
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, NG, RT, MODE>, k, v, p);
+}
+
+template <int MODE>
+cudaError_t launch_decode_mode(const CUtensorMap& k, const CUtensorMap& v, const DecodeArgs& p, int groups, int ctas,
+                               cudaStream_t stream) {
+  if (p.a.c.dim == 128) {
+    switch (groups) {
+      case 1: return launch_decode_ng<128, 1, 1, MODE>(k, v, p, ctas, stream);
+      case 2: return launch_decode_ng<128, 2, 1, MODE>(k, v, p, ctas, stream);
+      case 3: return launch_decode_ng<128, 1, 3, MODE>(k, v, p, ctas, stream);
+      default: return launch_decode_ng<128, 2, 2, MODE>(k, v, p, ctas, stream);
+    }
+  }
+  switch (groups) {
+    case 1: return launch_decode_ng<64, 1, 1, MODE>(k, v, p, ctas, stream);
+    case 2: return launch_decode_ng<64, 2, 1, MODE>(k, v, p, ctas, stream);
+    case 3: return launch_decode_ng<64, 1, 3, MODE>(k, v, p, ctas, stream);
+    default: return launch_decode_ng<64, 2, 2, MODE>(k, v, p, ctas, stream);
+  }
 }
 
 }  // namespace
@@ -867,27 +901,18 @@ size_t attn_decode_partial_bytes(int groups, int dim, int ctas) {
   return static_cast<size_t>(2) * ctas * groups * 8 * (dim + 1) * sizeof(float);
 }
 
-cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int groups, int ctas,
-                               int32_t* counters, float* partials, bool behind, cudaStream_t stream) {
+cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, AttnMode mode, int groups, int ctas,
+                               int32_t* counters, float* partials, int behind, cudaStream_t stream) {
   DecodeArgs p;
   p.a = a;
   p.counters = counters;
   p.partials = partials;
   p.wait_limit = 1ull << 31;
   p.behind = behind;
-  if (a.c.dim == 128) {
-    switch (groups) {
-      case 1: return launch_decode_ng<128, 1, 1>(k, v, p, ctas, stream);
-      case 2: return launch_decode_ng<128, 2, 1>(k, v, p, ctas, stream);
-      case 3: return launch_decode_ng<128, 1, 3>(k, v, p, ctas, stream);
-      default: return launch_decode_ng<128, 2, 2>(k, v, p, ctas, stream);
-    }
-  }
-  switch (groups) {
-    case 1: return launch_decode_ng<64, 1, 1>(k, v, p, ctas, stream);
-    case 2: return launch_decode_ng<64, 2, 1>(k, v, p, ctas, stream);
-    case 3: return launch_decode_ng<64, 1, 3>(k, v, p, ctas, stream);
-    default: return launch_decode_ng<64, 2, 2>(k, v, p, ctas, stream);
+  switch (mode) {
+    case kAttnPrefix: return launch_decode_mode<kAttnPrefix>(k, v, p, groups, ctas, stream);
+    case kAttnOwn: return launch_decode_mode<kAttnOwn>(k, v, p, groups, ctas, stream);
+    default: return launch_decode_mode<kAttnWhole>(k, v, p, groups, ctas, stream);
   }
 }
 

@@ -45,6 +45,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "bfp8_attn.cuh"
 #include "bfp8_attn_math.cuh"
@@ -313,7 +314,7 @@ __device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i])::"memory");
 }
 
-template <int D>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ TileArgs p) {
@@ -1135,6 +1136,46 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       float* part = p.partials + slot_id * slot_floats<D>();
       float* part_lse = part + kBlockRows * D;
       __nv_bfloat16* dst = a.out + (c.w.row0 + (live ? i : 0)) * a.o_st + head * a.o_sh;
+      const int64_t prow = MODE == kAttnWhole ? 0 : part_row(a, c.w.row0 + (live ? i : 0), head);
+      float* const part_dst = MODE == kAttnWhole ? nullptr : a.part_o + prow * D;
+      Joined jn{1.f, 0.f, lse2, false};
+      if constexpr (MODE == kAttnOwn)
+        if (whole && live) {
+          jn = join_prefix(a, c.w.row0 + i, head, lse2);
+          inv *= jn.own;
+        }
+      // columns 32 g .. of the row, from its fp32 ones
+      auto store32 = [&](int g, const float* x) {
+        if constexpr (MODE == kAttnPrefix) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part_dst + 32 * g + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        } else {
+          float y[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = x[e];
+          if constexpr (MODE == kAttnOwn) {
+            if (jn.covered) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(part_dst + 32 * g + e));
+                y[e] = fmaf(v.x, jn.prefix, y[e]);
+                y[e + 1] = fmaf(v.y, jn.prefix, y[e + 1]);
+                y[e + 2] = fmaf(v.z, jn.prefix, y[e + 2]);
+                y[e + 3] = fmaf(v.w, jn.prefix, y[e + 3]);
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            st_global_v4(dst + 32 * g + e, pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
+                         pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
+        }
+      };
+      auto store_lse = [&](float v) {
+        if constexpr (MODE == kAttnPrefix) a.part_lse2[prow] = v;
+        else if (a.lse != nullptr) a.lse[(c.w.row0 + i) * a.heads + head] = v * 0.6931471805599453f;
+      };
 #pragma unroll 1
       for (int g = 0; g < D / 32; ++g) {
         uint32_t o[32];
@@ -1143,13 +1184,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         reg_fence32(o);
         if (whole) {
           if (live && ok) {
+            float x[32];
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              st_global_v4(dst + 32 * g + e,
-                           pack_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv),
-                           pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv),
-                           pack_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv),
-                           pack_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv));
+            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(o[e]) * inv;
+            store32(g, x);
           }
         } else {
 #pragma unroll
@@ -1160,7 +1198,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if (whole) {
-        if (live && ok && a.lse != nullptr) a.lse[(c.w.row0 + i) * a.heads + head] = lse2 * 0.6931471805599453f;
+        if (live && ok) store_lse(jn.lse2);
       } else {
         part_lse[t * kTile + r] = lse2;
         const int64_t i0 = c.item0, i1 = c.item0 + c.n, total = s_total, ctas = s_ctas;
@@ -1186,6 +1224,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             best = fmaxf(best, __ldcg(slot_of(cta) + kBlockRows * D + t * kTile + r));
           const float ref = best == -INFINITY ? 0.f : best;
           float sum = 0.f;
+          float joined2 = 0.f;
 #pragma unroll 1
           for (int g = 0; g < D / 64; ++g) {         // 64 columns' loads in flight
             float o[64];
@@ -1209,17 +1248,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 o[4 * e + 3] = fmaf(v[e].w, w, o[4 * e + 3]);
               }
             }
-            const float is = sum == 0.f ? 0.f : 1.f / sum;
+            float is = sum == 0.f ? 0.f : 1.f / sum;
+            joined2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
             if (live && ok) {
+              if constexpr (MODE == kAttnOwn) {
+                jn = join_prefix(a, c.w.row0 + i, head, joined2);
+                joined2 = jn.lse2;
+                is *= jn.own;
+              }
 #pragma unroll
-              for (int e = 0; e < 64; e += 8)
-                st_global_v4(dst + 64 * g + e, pack_bf16x2(o[e] * is, o[e + 1] * is),
-                             pack_bf16x2(o[e + 2] * is, o[e + 3] * is), pack_bf16x2(o[e + 4] * is, o[e + 5] * is),
-                             pack_bf16x2(o[e + 6] * is, o[e + 7] * is));
+              for (int e = 0; e < 64; ++e) o[e] *= is;
+              store32(2 * g, o);
+              store32(2 * g + 1, o + 32);
             }
           }
-          if (live && ok && a.lse != nullptr)
-            a.lse[(c.w.row0 + i) * a.heads + head] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+          if (live && ok) store_lse(joined2);
         }
       }
       tc_fence_before();                       // O and S are read: the next block may overwrite them
@@ -1234,10 +1277,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
 }
 
-template <int D>
+template <int D, int MODE>
 cudaError_t launch_tile(const CUtensorMap& k, const CUtensorMap& v, const TileArgs& p, int ctas, cudaStream_t stream) {
   using C = TileCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
@@ -1249,7 +1292,7 @@ cudaError_t launch_tile(const CUtensorMap& k, const CUtensorMap& v, const TileAr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_tile_kernel<D>, k, v, p);
+  return cudaLaunchKernelEx(&cfg, attn_tile_kernel<D, MODE>, k, v, p);
 }
 
 }  // namespace
@@ -1258,15 +1301,23 @@ size_t attn_tile_partial_bytes(int dim, int ctas) {
   return static_cast<size_t>(2) * ctas * (dim == 128 ? slot_floats<128>() : slot_floats<64>()) * sizeof(float);
 }
 
-cudaError_t launch_attn_tile(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int ctas, int32_t* counters,
-                             float* partials, cudaStream_t stream) {
+cudaError_t launch_attn_tile(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, AttnMode mode, int ctas,
+                             int32_t* counters, float* partials, cudaStream_t stream) {
   TileArgs p;
   p.a = a;
   p.counters = counters;
   p.partials = partials;
   p.wait_limit = 1ull << 31;
   p.min_tiles = 4;
-  return a.c.dim == 128 ? launch_tile<128>(k, v, p, ctas, stream) : launch_tile<64>(k, v, p, ctas, stream);
+  auto go = [&](auto m) {
+    return a.c.dim == 128 ? launch_tile<128, decltype(m)::value>(k, v, p, ctas, stream)
+                          : launch_tile<64, decltype(m)::value>(k, v, p, ctas, stream);
+  };
+  switch (mode) {
+    case kAttnPrefix: return go(std::integral_constant<int, kAttnPrefix>{});
+    case kAttnOwn: return go(std::integral_constant<int, kAttnOwn>{});
+    default: return go(std::integral_constant<int, kAttnWhole>{});
+  }
 }
 
 }  // namespace bfp8

@@ -586,6 +586,132 @@ bfp8_status bfp8_paged_attention(const bfp8_attention_args* args, const bfp8_kv_
 bfp8_status bfp8_paged_attention_workspace_size(int num_heads, int num_kv_heads, int head_dim,
                                                 int max_q_len, size_t* bytes);
 
+/*
+ * bfp8_shared_prefix_attention -- bfp8_paged_attention for a batch whose
+ * sequences begin with the same text: the tokens of a shared prefix are read
+ * once for all rows that see them, where a block table with the same pages in
+ * many rows would have them read once a sequence.  Prefix f has lens[f] tokens
+ * on the pages block_table[f * ld_table ..] and is seen whole by the rows
+ * cu_q[f] .. cu_q[f+1] of q (usually those of neighbouring sequences); a row
+ * outside cu_q[0] .. cu_q[prefixes] sees no prefix.  The sequences' own tokens (args) are
+ * what comes behind the prefix: kv_lens and block_table count and hold them alone,
+ * and a row sees them as in bfp8_paged_attention, so that it stands at
+ * position lens[f] + kv_lens[b] - q_len + i of the whole.  Out and lse are those of
+ * one softmax over all tokens that a row sees; a row that sees none of
+ * either part gets 0 and -infinity.
+ *   args     as for bfp8_paged_attention, with window = 0 (BFP8_ERR_INVALID_ARG else).
+ *   prefix   block_table, cu_q [prefixes + 1] (non-decreasing, from 0 to total_q at most) and
+ *            lens [prefixes] are device int32; max_q_len bounds the rows of one
+ *            prefix (cu_q[f+1] - cu_q[f]), max_len the lens.  prefixes == 0: bfp8_paged_attention.
+ *   workspace  as for bfp8_paged_attention, bfp8_shared_prefix_attention_workspace_size
+ *            bytes: its part over the prefix is held there in fp32 for every row.
+ * The output is rounded once.  Page numbers and lengths as for bfp8_paged_attention; rows of
+ * a prefix past its bound max_q_len have unspecified outputs.  Results are deterministic.
+ */
+typedef struct {
+  const int32_t* block_table;
+  int64_t ld_table;
+  int max_pages;
+  int prefixes;
+  const int32_t* cu_q;
+  const int32_t* lens;
+  int max_q_len;
+  int reserved;
+  int64_t max_len;
+} bfp8_prefix_args;
+
+bfp8_status bfp8_shared_prefix_attention(const bfp8_attention_args* args, const bfp8_prefix_args* prefix,
+                                         const bfp8_kv_cache* cache, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* Workspace bytes bfp8_shared_prefix_attention needs on the current device for up
+ * to max_prefix_q_len rows a prefix, max_q_len new tokens a sequence and total_q rows. */
+bfp8_status bfp8_shared_prefix_attention_workspace_size(int num_heads, int num_kv_heads, int head_dim,
+                                                        int max_prefix_q_len, int max_q_len,
+                                                        int64_t total_q, size_t* bytes);
+
+/*
+ * bfp8_kv_cache_weigh -- how much attention every cached token received: to the
+ * sum of token j and kv head h is added
+ *   sum over the query heads of h, over the new tokens i that see j, of exp(softmax_scale * q_i . k_j - lse_i)
+ * where lse is what an attention call returned for these rows (of
+ * bfp8_shared_prefix_attention too, whose softmax runs over the prefix as well: then the
+ * sequences' own tokens are weighed with the arguments of that call, the prefix's with
+ * its table, its cu_q and lens, and causal = 0).  All in fp32, from
+ * the bf16 queries and the codes.
+ *   args     as for bfp8_paged_attention; out and its strides are not used,
+ *            lse [total_q, num_heads] is an input, q strides are at least head_dim.
+ *   weights  fp32 sums, one for every token of the cache's pages and kv head: token o of
+ *            page p at weights[p * weights_stride_page + h * weights_stride_head + o];
+ *            strides in floats, at least page_size.  4-byte aligned.
+ *   accumulate  1: the sums of the tokens that were cached before are added to, those of
+ *            the new tokens (causal = 1: the last q_len of the context) begin here,
+ *            whatever their places held; 0: the sums of the whole context begin here
+ *            (0 where no row sees a token).
+ * A sequence without new tokens keeps its sums.  Rows with a query, a key or an lse that is not a
+ * number make the sums of the tokens that they see NaN, and of no others.
+ *   workspace  as for bfp8_paged_attention, bfp8_kv_cache_weigh_workspace_size bytes.
+ * Sequences of one call have no page in common (the sums of a page in two tables would be those of
+ * either).  Page numbers and lengths as for bfp8_paged_attention; the sums of a token on a
+ * page outside the cache go nowhere.  Results are deterministic.
+ */
+bfp8_status bfp8_kv_cache_weigh(const bfp8_attention_args* args, const bfp8_kv_cache* cache,
+                                float* weights, int64_t weights_stride_page,
+                                int64_t weights_stride_head, int accumulate, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+bfp8_status bfp8_kv_cache_weigh_workspace_size(int num_heads, int num_kv_heads, int head_dim,
+                                               int max_q_len, size_t* bytes);
+
+/*
+ * bfp8_kv_cache_evict -- shortens sequences to `budget` tokens.  A sequence of
+ * n = kv_lens[b] > budget tokens keeps, for each kv head by itself, its first
+ * `first` and its last `recent` tokens and of the others the budget - first -
+ * recent with the largest weights (as bfp8_kv_cache_weigh sums them; of equal
+ * ones, those of lower position; a NaN counts as larger than any number).  They
+ * keep their order: the i-th of them becomes token i of the shortened sequence,
+ * with its codes, scales and weight.  What it saw of positions (a rotary
+ * encoding) was applied before it was cached and stays as it was.
+ * new_lens[b] = min(n, budget).
+ *   block_table  device int32 [batch, max_pages], row stride ld_table.
+ *   out_table    device int32 [batch, max_out_pages], row stride ld_out: the pages that the
+ *            tokens move to, max_out_pages * page_size >= min(budget, max_kv_len).  None of them is among the
+ *            pages that block_table holds for the call's sequences.  A sequence of at
+ *            most budget tokens is copied whole.  The pages that it came from are left as they were.
+ *            NULL: in place, to the first pages of block_table (a sequence of at most
+ *            budget tokens stays as it is); places behind the budget are left as they were.
+ *   weights  as for bfp8_kv_cache_weigh.
+ *   kv_lens, new_lens   device int32 [batch], not overlapping.
+ *   max_kv_len   host upper bound of the lengths.
+ *   budget >= 1, first >= 0, recent >= 0, first + recent <= budget.
+ *   workspace  as for bfp8_paged_attention, bfp8_kv_cache_evict_workspace_size bytes.
+ * batch * num_kv_heads is at most 65535.  Sequences of one call have no page in common.
+ * A page number outside the cache is recorded as BFP8_DEV_BAD_CACHE_INDEX and its tokens
+ * are not moved; lengths outside the bounds are taken at the bounds.
+ * batch == 0 launches nothing.
+ */
+typedef struct {
+  float* weights;
+  int64_t weights_stride_page, weights_stride_head;
+  const int32_t* block_table;
+  int64_t ld_table;
+  const int32_t* out_table;
+  int64_t ld_out;
+  int max_pages, max_out_pages;
+  const int32_t* kv_lens;
+  int32_t* new_lens;
+  int64_t max_kv_len;
+  int64_t budget, recent, first;
+  int batch;
+  int reserved;
+} bfp8_evict_args;
+
+bfp8_status bfp8_kv_cache_evict(const bfp8_evict_args* args, const bfp8_kv_cache* cache, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+bfp8_status bfp8_kv_cache_evict_workspace_size(int batch, int num_kv_heads, int64_t max_kv_len,
+                                               int64_t budget, size_t* bytes);
+
 /* ------------------------------------------------------------------------ */
 /* Status and diagnostics                                                    */
 /* ------------------------------------------------------------------------ */
