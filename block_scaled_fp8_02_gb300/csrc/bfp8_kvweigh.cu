@@ -5,15 +5,17 @@
 //   a[h, j] = sum over query heads of kv head h, over new tokens i that see j, of exp(scale q_i . k_j - lse_i)
 //
 // With at most 16 rows (new tokens x heads of a kv head) it is bound by reading
-// the keys once.  The units (32 tokens of a sequence and kv head) of all
+// the keys once.  The units (16 tokens of a sequence and kv head) of all
 // sequences form one line; CTAs take equal shares of it and their warps turns in
 // it, each by itself: a token's sum is one warp's, so that nothing is joined.
 // The tokens are the 16-row operand of mma.sync.m16n8k16 (f16, fp32 sums), the
-// query rows its 8 columns.  A lane reads 16 codes of a token at a time straight
-// from the cache and makes f16 of them (exact); the contraction's slots hold a
-// permutation of it that makes these reads whole.  Queries are scaled by a power of two
-// a row (exact in f16 to 2^-37 of its largest).  The next unit's
-// keys and the page numbers of the one behind it are on their way meanwhile.
+// query rows its 8 columns.  A lane reads 16 codes of a token at a time and makes
+// f16 of them (exact); the contraction's slots hold a permutation of it that makes these
+// reads whole.  Queries are scaled by a power of two a row (exact in f16 to 2^-37
+// of its largest).  Units come by asynchronous copies, each lane into places that
+// it alone reads, so that a warp has several on their way, waits for nobody else and
+// holds none in registers (a unit on its way in registers: 127 us for 64 sequences of up
+// to 8000 tokens, 64 / 8 heads of 128).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -29,10 +31,9 @@ namespace bfp8 {
 
 namespace {
 
-constexpr int kUnit = 32;                  // tokens of a unit
+constexpr int kUnit = 16;                  // tokens of a unit: never more than a page
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kItemCost = 4;               // places of a (sequence, head) in the line besides its units
-constexpr int kSeqCache = 32;              // sequences whose lengths a CTA keeps in shared memory
+constexpr int kItemCost = 8;               // places of a (sequence, head) in the line besides its units
 constexpr int kCtasPerSm = 2;
 
 // A sequence as the scheduler sees it: tokens [t0, t1) have sums to be written.
@@ -85,27 +86,49 @@ __device__ __forceinline__ void mma_f16_16x8x16(float (&d)[4], uint32_t a0, uint
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+template <int D>
+struct FewCfg {
+  static constexpr int kKeys = kUnit * D;
+  static constexpr int kStages = D == 128 ? 5 : 8;                 // units of a warp on their way
+  static constexpr int kOffKs = kKeys;                             // scales of tokens g and g + 8 of each lane
+  static constexpr int kOffOld = kOffKs + 2 * 32 * 4;              // the sum so far of the token that the lane writes
+  static constexpr int kStage = kOffOld + 32 * 4;
+  static constexpr int kSmem = kWarps * kStages * kStage;
+  static_assert(kCtasPerSm * (kSmem + 4096) <= 227 * 1024, "shared memory of the CTAs of a SM");
+};
+
+// 16 or 4 bytes into shared memory, zeros in place of a source that is not there.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Where a warp is in the line.
 struct Cursor {
   int b, h;
   int64_t item0;          // line position of the item's first unit
-  SeqWork w;
+  int32_t units, t0, kv_len, pos0;
 };
-// A unit on its way: its first token, and its pages (of each half; one page where a page holds both).
+// A unit: its first token and its page; b < 0: none.
 struct Unit {
   int b, h;
-  int32_t tok;
-  int32_t page[2];
-  bool live;
+  int32_t tok, page;
 };
 
 template <int D, int NG>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const __grid_constant__ WeighArgs p) {
+  using C = FewCfg<D>;
   constexpr int kRows = NG * 8;
   constexpr int KC = D / 64;               // 16-byte key chunks a lane reads of a token
   const AttnArgs& a = p.a;
+  extern __shared__ __align__(16) uint8_t few_smem[];
   __shared__ int64_t part[kWarps];
-  __shared__ SeqWork seqs[kSeqCache];
+  __shared__ Unit units[kWarps][C::kStages];
   __shared__ int64_t s_before;
   __shared__ int s_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -114,11 +137,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
   griddep_wait();
 
   // ---- this CTA's share [u0, u1) of the line of units, and where it starts
-  int64_t run = 0;
+  int64_t run = 0, incl0 = 0;
+  int32_t n0 = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     const int b = b0 + tid;
-    const int64_t incl = block_scan(b < a.batch ? line_cost(seq_work(p, b, kRows).units) : 0, part);
-    if (tid == kThreads - 1) part[0] = incl;
+    n0 = b < a.batch ? line_cost(seq_work(p, b, kRows).units) : 0;
+    incl0 = block_scan(n0, part);
+    if (tid == kThreads - 1) part[0] = incl0;
     __syncthreads();
     run += part[0];
     __syncthreads();
@@ -127,95 +152,105 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
   const int64_t want = (total + kWarps - 1) / kWarps, ctas = want < gridDim.x ? want : gridDim.x;
   if (blockIdx.x >= ctas) return;
   const int64_t u0 = share_begin(blockIdx.x, total, ctas), u1 = share_begin(blockIdx.x + 1, total, ctas);
-  run = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-    const int b = b0 + tid;
-    const int32_t n = b < a.batch ? line_cost(seq_work(p, b, kRows).units) : 0;
-    const int64_t incl = run + block_scan(n, part);
+  auto find = [&](int b, int64_t incl, int32_t n) {
     if (n > 0 && (incl - n) * H <= u0 && u0 < incl * H) {
       s_b = b;
       s_before = (incl - n) * H;
     }
-    if (tid == kThreads - 1) part[0] = incl;
-    __syncthreads();
-    run = part[0];
-    __syncthreads();
+  };
+  if (a.batch <= kThreads) {
+    find(tid, incl0, n0);
+  } else {
+    run = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+      const int b = b0 + tid;
+      const int32_t n = b < a.batch ? line_cost(seq_work(p, b, kRows).units) : 0;
+      const int64_t incl = run + block_scan(n, part);
+      find(b, incl, n);
+      if (tid == kThreads - 1) part[0] = incl;
+      __syncthreads();
+      run = part[0];
+      __syncthreads();
+    }
   }
-  const int b_first = s_b;
-  if (tid < kSeqCache && b_first + tid < a.batch) seqs[tid] = seq_work(p, b_first + tid, kRows);
   __syncthreads();
-  auto get_seq = [&](int b) -> SeqWork { return b - b_first < kSeqCache ? seqs[b - b_first] : seq_work(p, b, kRows); };
 
   Cursor c;
-  c.b = b_first;
-  c.w = get_seq(c.b);
-  c.h = static_cast<int>((u0 - s_before) / line_cost(c.w.units));
-  c.item0 = s_before + static_cast<int64_t>(c.h) * line_cost(c.w.units);
+  auto enter = [&](int b) {
+    const SeqWork w = seq_work(p, b, kRows);
+    c.b = b;
+    c.units = w.units;
+    c.t0 = w.t0;
+    c.kv_len = w.kv_len;
+    c.pos0 = w.pos0;
+  };
+  enter(s_b);
+  c.h = static_cast<int>((u0 - s_before) / line_cost(c.units));
+  c.item0 = s_before + static_cast<int64_t>(c.h) * line_cost(c.units);
   int64_t u = u0 + warp;
-  // the warp's next unit, its page numbers asked for
+  // the warp's next unit, its page's number asked for; bounds: of its tokens
+  int32_t t0 = 0, kv_len = 0, pos0 = 0;
   auto locate = [&]() {
-    Unit n{};
+    Unit n;
+    n.b = -1;
+    n.h = n.tok = n.page = 0;
     while (u < u1) {
-      const int32_t cost = line_cost(c.w.units);
+      const int32_t cost = line_cost(c.units);
       if (u >= c.item0 + cost) {
         c.item0 += cost;
         if (++c.h == H) {
           c.h = 0;
           do {
-            c.w = get_seq(++c.b);
-          } while (c.w.units == 0);
+            enter(c.b + 1);
+          } while (c.units == 0);
         }
         continue;
       }
       const int32_t k = static_cast<int32_t>(u - c.item0);
       u += kWarps;
-      if (k >= c.w.units) continue;                                  // the places behind an item
+      if (k >= c.units) continue;                                    // the places behind an item
       n.b = c.b;
       n.h = c.h;
-      n.tok = (c.w.t0 / kUnit + k) * kUnit;
-      n.live = true;
-      const int32_t* row = a.table + c.b * a.ld_table;
-      n.page[0] = __ldg(row + (n.tok >> a.c.page_shift));
-      n.page[1] = n.tok + 16 < c.w.kv_len ? __ldg(row + ((n.tok + 16) >> a.c.page_shift)) : n.page[0];
+      n.tok = (c.t0 / kUnit + k) * kUnit;
+      n.page = __ldg(a.table + c.b * a.ld_table + (n.tok >> a.c.page_shift));
+      t0 = c.t0;
+      kv_len = c.kv_len;
+      pos0 = c.pos0;
       break;
     }
     return n;
   };
-  // its keys, their scales, and the sum that this lane will write (token 16 (t / 2) + 8 (t % 2) + g)
-  struct Data {
-    uint4 k[2][2][KC];
-    float ks[2][2];
-    float old;
-  };
-  auto sum_at = [&](const Unit& n) -> float* {
-    const int32_t j = n.tok + 16 * (t >> 1) + 8 * (t & 1) + g;
-    return p.w + n.page[t >> 1] * p.ws_page + n.h * p.ws_head + (j & (a.c.page_size - 1));
-  };
-  auto fetch = [&](Unit& n, Data& d) {
-    if (!n.live) return;
-    const SeqWork& w = get_seq(n.b);
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (n.page[e] < 0 || n.page[e] >= a.c.num_pages) {
-        report_failure(a.err, kDevBadCacheIndex);
-        n.page[e] = -1;
+  uint8_t* const ring = few_smem + warp * (C::kStages * C::kStage);
+  const uint32_t ring_at = smem_addr(ring);
+  // the token whose sum this lane writes: g, or g + 8 (lanes t = 0 and 1)
+  const int out = g + 8 * t;
+  // starts the copies of a unit located last: keys, their scales, the sum to be added to
+  auto fetch = [&](Unit& n, int slot) {
+    if (n.b >= 0) {
+      if (n.page < 0 || n.page >= a.c.num_pages) {
+        if (lane == 0) report_failure(a.err, kDevBadCacheIndex);
+        n.page = -1;
       }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
+      const bool there = n.page >= 0;
+      const int64_t page = there ? n.page : 0;
+      const int off = n.tok & (a.c.page_size - 1);
+      const uint8_t* keys = a.c.k + page * a.c.st_page + n.h * a.c.st_head + (off + g) * a.c.st_tok + 16 * t;
+      const float* scales = a.c.ks + page * a.c.ss_page + n.h * a.c.ss_head + off + g;
+      const uint32_t at = ring_at + slot * C::kStage;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int32_t j = n.tok + 16 * e + 8 * r + g;
-        const bool ok = n.page[e] >= 0 && j < w.kv_len;
-        const int off = j & (a.c.page_size - 1);
-        const uint8_t* src = a.c.k + (ok ? n.page[e] : 0) * a.c.st_page + n.h * a.c.st_head + off * a.c.st_tok + 16 * t;
+        const bool live = there && n.tok + 8 * r + g < kv_len;
 #pragma unroll
-        for (int h = 0; h < KC; ++h)
-          d.k[e][r][h] = ok ? __ldg(reinterpret_cast<const uint4*>(src + 64 * h)) : make_uint4(0u, 0u, 0u, 0u);
-        d.ks[e][r] = ok ? __ldg(a.c.ks + n.page[e] * a.c.ss_page + n.h * a.c.ss_head + off) : 0.f;
+        for (int h = 0; h < KC; ++h) copy16(at + ((r * KC + h) * 32 + lane) * 16, keys + 8 * r * a.c.st_tok + 64 * h, live);
+        copy4(at + C::kOffKs + (r * 32 + lane) * 4, scales + 8 * r, live);
       }
+      const int32_t j = n.tok + out;
+      if (t < 2)
+        copy4(at + C::kOffOld + lane * 4, p.w + page * p.ws_page + n.h * p.ws_head + off + out,
+              there && j < kv_len && !begins_here(p, j, pos0));
     }
-    const int32_t j = n.tok + 16 * (t >> 1) + 8 * (t & 1) + g;
-    d.old = n.page[t >> 1] >= 0 && j >= w.t0 && j < w.kv_len && !begins_here(p, j, w.pos0) ? *sum_at(n) : 0.f;
+    if (lane == 0) units[warp][slot] = n;
+    copies_end();
   };
 
   // ---- the queries at hand: rows grp * 8 + g, f16 after scaling by a power of two
@@ -223,9 +258,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
   float cq[NG][2], bias[NG][2];            // of the rows 8 grp + 2 t, + 1: factor of the score, -lse in powers of two
   int32_t lo[NG][2], hi[NG][2];            // tokens that they see
   int q_b = -1, q_h = -1;
-  auto queries = [&](const Unit& n, const SeqWork& w) {
+  int32_t q_t0 = 0, q_end = 0;             // the tokens of the sequence whose sums are written
+  auto queries = [&](const Unit& n) {
     q_b = n.b;
     q_h = n.h;
+    const SeqWork w = seq_work(p, n.b, kRows);
+    q_t0 = w.t0;
+    q_end = w.kv_len;
     const int rows = w.q_len * a.group;
 #pragma unroll
     for (int grp = 0; grp < NG; ++grp) {
@@ -281,70 +320,74 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
     }
   };
 
-  auto compute = [&](const Unit& n, const Data& d) {
-    const SeqWork& w = get_seq(n.b);
-    if (n.b != q_b || n.h != q_h) queries(n, w);
-    float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-    float s[2][NG][KC][4];
+  auto compute = [&](const Unit& n, int slot) {
+    if (n.b != q_b || n.h != q_h) queries(n);
+    const uint8_t* at = ring + slot * C::kStage;
+    const float* sc = reinterpret_cast<const float*>(at + C::kOffKs) + lane;
+    const float ks[2] = {sc[0], sc[32]};
+    float s[NG][KC][4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
-      for (int grp = 0; grp < NG; ++grp)
+      for (int h = 0; h < KC; ++h) s[grp][h][0] = s[grp][h][1] = s[grp][h][2] = s[grp][h][3] = 0.f;
 #pragma unroll
-        for (int h = 0; h < KC; ++h) s[e][grp][h][0] = s[e][grp][h][1] = s[e][grp][h][2] = s[e][grp][h][3] = 0.f;
+    for (int h = 0; h < KC; ++h) {
+      const uint4 ka = *reinterpret_cast<const uint4*>(at + (h * 32 + lane) * 16),
+                  kb = *reinterpret_cast<const uint4*>(at + ((KC + h) * 32 + lane) * 16);
 #pragma unroll
-    for (int h = 0; h < KC; ++h)
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t wa = x == 0 ? ka.x : x == 1 ? ka.y : x == 2 ? ka.z : ka.w;
+        const uint32_t wb = x == 0 ? kb.x : x == 1 ? kb.y : x == 2 ? kb.z : kb.w;
+        uint32_t a0, a1, a2, a3;
+        e4m3x4_to_f16(wa, a0, a2);
+        e4m3x4_to_f16(wb, a1, a3);
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint4 &ka = d.k[e][0][h], &kb = d.k[e][1][h];
-          const uint32_t wa = x == 0 ? ka.x : x == 1 ? ka.y : x == 2 ? ka.z : ka.w;
-          const uint32_t wb = x == 0 ? kb.x : x == 1 ? kb.y : x == 2 ? kb.z : kb.w;
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16(wa, a0, a2);
-          e4m3x4_to_f16(wb, a1, a3);
-#pragma unroll
-          for (int grp = 0; grp < NG; ++grp)
-            mma_f16_16x8x16(s[e][grp][h], a0, a1, a2, a3, qf[grp][h * 4 + x][0], qf[grp][h * 4 + x][1]);
-        }
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int grp = 0; grp < NG; ++grp)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = i >> 1, x = i & 1;
-          float v = s[e][grp][0][i];
-          if constexpr (KC == 2) v += s[e][grp][1][i];
-          const int32_t j = n.tok + 16 * e + 8 * r + g;
-          v = ex2(fmaf(v, d.ks[e][r] * cq[grp][x], bias[grp][x]));
-          if (j >= lo[grp][x] && j < hi[grp][x]) sum[e][r] += v;
-        }
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        sum[e][r] += __shfl_xor_sync(0xffffffffu, sum[e][r], 1);
-        sum[e][r] += __shfl_xor_sync(0xffffffffu, sum[e][r], 2);
+        for (int grp = 0; grp < NG; ++grp)
+          mma_f16_16x8x16(s[grp][h], a0, a1, a2, a3, qf[grp][h * 4 + x][0], qf[grp][h * 4 + x][1]);
       }
-    const float mine = (t >> 1) == 0 ? ((t & 1) == 0 ? sum[0][0] : sum[0][1]) : ((t & 1) == 0 ? sum[1][0] : sum[1][1]);
-    const int32_t j = n.tok + 16 * (t >> 1) + 8 * (t & 1) + g;
-    if (n.page[t >> 1] >= 0 && j >= w.t0 && j < w.kv_len) *sum_at(n) = d.old + mine;
+    }
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i >> 1, x = i & 1;
+        float v = s[grp][0][i];
+        if constexpr (KC == 2) v += s[grp][1][i];
+        const int32_t j = n.tok + 8 * r + g;
+        v = ex2(fmaf(v, ks[r] * cq[grp][x], bias[grp][x]));
+        if (j >= lo[grp][x] && j < hi[grp][x]) sum[r] += v;
+      }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+    }
+    const int32_t j = n.tok + out;
+    if (t < 2 && n.page >= 0 && j >= q_t0 && j < q_end)
+      p.w[n.page * p.ws_page + n.h * p.ws_head + (j & (a.c.page_size - 1))] =
+          reinterpret_cast<const float*>(at + C::kOffOld)[lane] + (t == 0 ? sum[0] : sum[1]);
   };
 
-  Unit cur = locate();
-  Data dc, dn;
-  fetch(cur, dc);
-  Unit nxt = locate();
-  while (cur.live) {
-    fetch(nxt, dn);
-    const Unit after = locate();
-    compute(cur, dc);
-    cur = nxt;
-    dc = dn;
-    nxt = after;
+  // a unit's page number is asked for a turn before its copies start
+  Unit next = locate();
+  int slot = 0;
+  for (int i = 0; i < C::kStages - 1; ++i) {
+    fetch(next, i);
+    next = locate();
   }
+  while (true) {
+    copies_wait<C::kStages - 2>();
+    __syncwarp();                                                    // lane 0's note of the unit, and the slot read last
+    const Unit n = units[warp][slot];
+    if (n.b < 0) break;
+    const int free = slot == 0 ? C::kStages - 1 : slot - 1;
+    fetch(next, free);
+    next = locate();
+    compute(n, slot);
+    slot = slot + 1 == C::kStages ? 0 : slot + 1;
+  }
+  copies_wait<0>();
 }
 
 inline bool off_align(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
@@ -369,18 +412,31 @@ size_t workspace_bytes_for(int group, int max_q, int sms) {
 
 }  // namespace
 
-cudaError_t launch_weigh_few(const WeighArgs& p, int groups, int ctas, cudaStream_t stream) {
+namespace {
+
+template <int D, int NG>
+cudaError_t launch_few(const WeighArgs& p, int ctas, cudaStream_t stream) {
+  using C = FewCfg<D>;
+  cudaError_t e = cudaFuncSetAttribute(weigh_few_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas * kCtasPerSm));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.a.c.dim == 128) return cudaLaunchKernelEx(&cfg, groups == 1 ? weigh_few_kernel<128, 1> : weigh_few_kernel<128, 2>, p);
-  return cudaLaunchKernelEx(&cfg, groups == 1 ? weigh_few_kernel<64, 1> : weigh_few_kernel<64, 2>, p);
+  return cudaLaunchKernelEx(&cfg, weigh_few_kernel<D, NG>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_weigh_few(const WeighArgs& p, int groups, int ctas, cudaStream_t stream) {
+  if (p.a.c.dim == 128) return groups == 1 ? launch_few<128, 1>(p, ctas, stream) : launch_few<128, 2>(p, ctas, stream);
+  return groups == 1 ? launch_few<64, 1>(p, ctas, stream) : launch_few<64, 2>(p, ctas, stream);
 }
 
 }  // namespace bfp8
