@@ -978,6 +978,12 @@ def bfp8_kv_cache_evict_workspace_size(batch: int, num_kv_heads: int, max_kv_len
     return int(n.value)
 
 
+# It goes by the budget alone where anything can be evicted, and is the same for all lengths where nothing can.
+@functools.lru_cache(maxsize=256)
+def _evict_workspace(batch: int, num_kv_heads: int, budget: int) -> int:
+    return bfp8_kv_cache_evict_workspace_size(batch, num_kv_heads, budget + 1 if budget else 0, budget or 1)
+
+
 def bfp8_kv_cache_evict(cache: KVCache, weights: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
                         max_kv_len: int, budget: int, recent: int = 0, first: int = 0,
                         out_table: torch.Tensor | None = None, new_lens: torch.Tensor | None = None,
@@ -1007,8 +1013,7 @@ def bfp8_kv_cache_evict(cache: KVCache, weights: torch.Tensor, block_table: torc
     _on(dev, cache.k, weights, block_table, out_table, new_lens, workspace)
     sp = _stream_of(stream)
     if workspace is None:
-        need = bfp8_kv_cache_evict_workspace_size(B, H, max_kv_len, budget) if B else 0
-        workspace = _workspace(need, dev, stream, sp)
+        workspace = _workspace(_evict_workspace(B, H, budget if max_kv_len > budget else 0) if B else 0, dev, stream, sp)
     a = _pack_evict.pack(weights.data_ptr(), wp, wh, tp, ld, op, ld_out, width, out_width, kv_lens.data_ptr(),
                          new_lens.data_ptr(), max_kv_len, budget, recent, first, B, 0)
     _check((_lib or lib()).bfp8_kv_cache_evict(a, cache._desc, workspace.data_ptr(),

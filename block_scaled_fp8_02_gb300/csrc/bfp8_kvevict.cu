@@ -6,14 +6,13 @@
 //   kept = {j < first} + {j >= n - recent} + the (budget - first - recent) largest
 //          of the rest, of equal ones those of lower position       (n > budget)
 //
-// Two kernels.  The first finds each (sequence, head)'s kept positions: a cluster
-// of CTAs holds the sums as ordered 32-bit keys in shared memory and finds the
-// key of rank `budget` by its 11, 11 and 10 bits, from histograms that the cluster's
-// CTAs read from each other; then every warp writes the positions of its stretch
-// behind those of the stretches before it.  The second moves the rows, 64 ranks a
-// CTA at a time; in place, where a rank's source may be another rank's destination
-// (never a lower one's: rank <= position), a cluster takes 512 ranks at once and
-// loads them all before it stores one.
+// A cluster of CTAs (or one) a (sequence, head).  Its threads hold the sums as ordered
+// 32-bit keys and find the key of rank `budget` by its 11, 11 and 10 bits, from
+// histograms that are added up in the cluster's first CTA; the positions kept are written
+// in order, by counts of them before each 32, and the warps move the
+// rows, each 16 or 32 ranks at a time.  In place a rank's source may be
+// another's destination (never a lower one's: rank <= position), so there the
+// cluster loads all ranks of a round before it stores one.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -27,13 +26,19 @@ namespace bfp8 {
 
 namespace {
 
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kSelKeys = 40960;                    // keys of a CTA that its shared memory holds; the rest is read again
-constexpr int kSelMaxCluster = 8;
-constexpr int kSelSmem = 2 * kBins * 4 + kSelKeys * 4;
+// Threads of a CTA that looks for the kept positions, and keys that each holds (a longer stretch is read anew each time).
+// Many (sequence, head)s: small CTAs, four a SM (64 x 8 heads of 8000 tokens 28 us, 41 with clusters of two).  Few long ones: large
+// ones, in clusters (the measured cost of a cluster's barriers is about a microsecond each, so no more CTAs than the
+// keys need).
+template <int T>
+struct Find {
+  static constexpr int kWarps = T / 32, kHold = T == 256 ? 32 : 16, kChunk = kHold * T, kCtasPerSm = T == 256 ? 4 : 1;
+};
+constexpr int kMaxCluster = 4;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveTokens = 64;                    // ranks of a CTA's step
+constexpr int kMoveTokens = 64;                    // ranks of a CTA's step (a warp moving 16 by itself, their pages asked for
+                                                   // ahead: 92 us against 80 for 64 sequences' 2048 tokens, 8 heads of 128)
 constexpr int kMoveCluster = 8;
 
 struct EvictArgs {
@@ -64,106 +69,128 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return (u >> 31) != 0u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
-  extern __shared__ __align__(16) uint32_t sel_smem[];
-  uint32_t* const hist0 = sel_smem;                         // two, by turns: another CTA may still read the last
-  uint32_t* const keys = sel_smem + 2 * kBins;
-  __shared__ uint32_t s_scan[kSelWarps];
-  __shared__ uint32_t s_pick[2];                            // bin, ranks above it
-  __shared__ uint32_t s_cnt[2];                             // this CTA's keys above the border, and at it
-  __shared__ uint32_t s_warp[2][kSelWarps];
-  const int C = static_cast<int>(gridDim.x);                // one cluster a (sequence, head)
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int item = static_cast<int>(blockIdx.y), b = item / a.c.heads, h = item - b * a.c.heads;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  griddep_launch_dependents();
-  griddep_wait();
-  const int32_t n = length_of(a, b);
-  if (rank == 0 && h == 0 && tid == 0) a.new_lens[b] = n < a.budget ? n : a.budget;
-  if (n <= a.budget) return;                                // the whole cluster
-  // this CTA's stretch, a whole number of warps' rows a warp
-  const int32_t per_warp = (n + C * kSelThreads - 1) / (C * kSelThreads) * 32;
-  const int32_t seg = per_warp * kSelWarps;
-  const int32_t j0 = rank * seg < n ? rank * seg : n, j1 = j0 + seg < n ? j0 + seg : n;
-  const int32_t* row = a.table + b * a.ld_table;
-  auto page_ok = [&](int32_t page) {
-    if (page >= 0 && page < a.c.num_pages) return true;
-    report_failure(a.err, kDevBadCacheIndex);
-    return false;
-  };
-  auto forced = [&](int32_t j) { return j < a.first || j >= n - a.recent; };
-  auto load_key = [&](int32_t j) -> uint32_t {
-    if (forced(j)) return 0xFFFFFFFFu;
-    const int32_t page = __ldg(row + (j >> a.c.page_shift));
-    return page_ok(page) ? key_of(a.w[page * a.ws_page + h * a.ws_head + (j & (a.c.page_size - 1))]) : 0u;
-  };
-  auto key_at = [&](int32_t j) { return j - j0 < kSelKeys ? keys[j - j0] : load_key(j); };
-  for (int i = tid; i < 2 * kBins; i += kSelThreads) hist0[i] = 0u;
-  // (eight at a time: the pages' numbers, then the sums; one by one their latencies add up: 8 CTAs for each of 8 heads'
-  // 60000 tokens took 26 us with what follows)
-  const int32_t held = j1 - j0 < kSelKeys ? j1 - j0 : kSelKeys;
-  for (int32_t i0 = tid; i0 < held; i0 += 8 * kSelThreads) {
-    int32_t page[8];
-    float w[8];
+// Sum over the block's threads before this one (all call it); s_scan: a place a warp.
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* s_scan) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t incl = v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int32_t j = j0 + i0 + e * kSelThreads;
-      page[e] = i0 + e * kSelThreads < held && !forced(j) ? __ldg(row + (j >> a.c.page_shift)) : 0;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int32_t j = j0 + i0 + e * kSelThreads;
-      const bool there = i0 + e * kSelThreads < held && !forced(j) && page[e] >= 0 && page[e] < a.c.num_pages;
-      w[e] = there ? __ldcg(a.w + page[e] * a.ws_page + h * a.ws_head + (j & (a.c.page_size - 1))) : 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int32_t i = i0 + e * kSelThreads;
-      if (i < held) keys[i] = forced(j0 + i) ? 0xFFFFFFFFu : page_ok(page[e]) ? key_of(w[e]) : 0u;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
   }
+  if (lane == 31) s_scan[warp] = incl;
   __syncthreads();
+  const uint32_t other = lane < warp ? s_scan[lane] : 0u;
+  const uint32_t before = __reduce_add_sync(0xffffffffu, other) + incl - v;
+  __syncthreads();
+  return before;
+}
+
+__device__ __forceinline__ void add_shared_cluster(uint32_t at, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void ld_shared_cluster_u2(uint32_t at, uint32_t& x, uint32_t& y) {
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(at) : "memory");
+}
+
+// Writes the positions that (sequence, head h) keeps of its n > budget tokens, in order, to `kept`.  All threads of the
+// cluster's C CTAs call it.
+template <int kThreads>
+__device__ __forceinline__ void find_kept(const EvictArgs& a, int C, int rank, int h, int32_t n, const int32_t* row, int32_t* kept) {
+  constexpr int kWarps = Find<kThreads>::kWarps, kHold = Find<kThreads>::kHold, kChunk = Find<kThreads>::kChunk;
+  constexpr int kOwn = kBins / kThreads;                    // bins that a thread adds up
+  constexpr int kAllBins = 2 * kBins + kBins / 2;           // of the three passes
+  __shared__ __align__(16) uint32_t s_own[kAllBins], s_all[kAllBins];     // of this CTA's keys; of the cluster's (the first CTA's)
+  __shared__ uint32_t s_scan[kWarps];
+  __shared__ uint32_t s_pick[2];                            // bin, ranks above it
+  __shared__ uint32_t s_before[2];                          // keys above the border, and at it, of the CTAs before this one
+  __shared__ uint32_t s_above[kHold * kWarps], s_at[kHold * kWarps];      // ... of each 32 positions
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kCounts = kHold * kWarps;
+  static_assert(kCounts <= kThreads, "a thread a count");
+  // this CTA's stretch
+  const int32_t seg = (n + C * 32 - 1) / (C * 32) * 32;
+  const int32_t j0 = rank * seg < n ? rank * seg : n, j1 = j0 + seg < n ? j0 + seg : n;
+  const uint32_t choice = static_cast<uint32_t>(n - a.recent - a.first);  // positions that are not kept in any case, from `first` on
+  const float* sums = a.w + h * a.ws_head;
+  uint32_t key[kHold];                                      // of positions at + e * kThreads + tid
+  // (eight at a time: the pages' numbers, then the sums; one by one their latencies add up)
+  auto load = [&](int32_t at) {
+#pragma unroll
+    for (int e0 = 0; e0 < kHold; e0 += 8) {
+      if (at + e0 * kThreads >= j1) break;
+      int32_t page[8];
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int32_t j = at + (e0 + e) * kThreads + tid;
+        page[e] = j < j1 && static_cast<uint32_t>(j - a.first) < choice ? __ldg(row + (j >> a.c.page_shift)) : -1;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int32_t j = at + (e0 + e) * kThreads + tid;
+        w[e] = 0.f;
+        if (static_cast<uint32_t>(page[e]) < static_cast<uint32_t>(a.c.num_pages))
+          w[e] = __ldcg(sums + page[e] * a.ws_page + (j & (a.c.page_size - 1)));
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int32_t j = at + (e0 + e) * kThreads + tid;
+        key[e0 + e] = key_of(w[e]);
+        if (static_cast<uint32_t>(page[e]) >= static_cast<uint32_t>(a.c.num_pages)) {
+          const bool chosen = static_cast<uint32_t>(j - a.first) < choice;       // else kept in any case
+          if (chosen && j < j1) report_failure(a.err, kDevBadCacheIndex);
+          key[e0 + e] = chosen ? 0u : 0xFFFFFFFFu;
+        }
+      }
+    }
+  };
+  const bool once = j1 - j0 <= kChunk;
+  for (int i = tid; i < kAllBins; i += kThreads) s_own[i] = s_all[i] = 0u;
+  if (tid < 2) s_before[tid] = 0u;
+  if (once) load(j0);
+  if (C > 1) cluster_sync();
+  else __syncthreads();
   // ---- the key of rank `budget`, from its top bits down
   uint32_t border = 0u, need = static_cast<uint32_t>(a.budget);     // ranks still to be found at or below `border`'s bits
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? kBins / 2 : kBins;
     const uint32_t above = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
-    uint32_t* hist = hist0 + (pass & 1) * kBins;
-    for (int32_t j = j0 + tid; j < j1; j += kSelThreads) {
-      const uint32_t k = key_at(j);
-      if ((k & above) == border) atomicAdd(hist + ((k >> shift) & (bins - 1)), 1u);
-    }
-    if (C > 1) cluster_sync();
-    else __syncthreads();
-    // four bins a thread, the largest first, over the whole cluster
-    const int top = bins - 4 - 4 * tid;
-    uint32_t cnt[4] = {0u, 0u, 0u, 0u};
-    if (top >= 0) {
-      for (int r = 0; r < C; ++r) {
-        uint32_t v[4];
-        const uint32_t at = mapa_shared(smem_addr(hist + top), static_cast<uint32_t>(r));
-        asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+    uint32_t *own = s_own + pass * kBins, *all = s_all + pass * kBins;
+#pragma unroll 1
+    for (int32_t at = j0; at < j1; at += kChunk) {
+      if (!once) load(at);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) cnt[e] += v[e];
+      for (int e = 0; e < kHold; ++e) {
+        if (at + e * kThreads >= j1) break;
+        if (at + e * kThreads + tid < j1 && (key[e] & above) == border) atomicAdd(own + ((key[e] >> shift) & (bins - 1)), 1u);
       }
     }
-    const uint32_t mine = cnt[0] + cnt[1] + cnt[2] + cnt[3];
-    uint32_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
-    uint32_t before = incl - mine;
-    for (int w = 0; w < warp; ++w) before += s_scan[w];
+    // a thread's bins, the largest first; a cluster's are added up in its first CTA, where most are empty
+    const int top = bins - kOwn - kOwn * tid;
+    uint32_t cnt[kOwn] = {};
+    if (C > 1) {
+      const uint32_t sum = mapa_shared(smem_addr(all), 0u);
+      for (int i = tid; i < bins; i += kThreads)
+        if (own[i] != 0u) add_shared_cluster(sum + 4 * i, own[i]);
+      cluster_sync();
+      if (top >= 0)
+#pragma unroll
+        for (int e = 0; e < kOwn; e += 2) ld_shared_cluster_u2(sum + 4 * (top + e), cnt[e], cnt[e + 1]);
+    } else if (top >= 0) {
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e) cnt[e] = own[top + e];
+    }
+    uint32_t mine = 0u;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) mine += cnt[e];
+    const uint32_t before = sum_before(mine, s_scan);
     if (before < need && need <= before + mine) {
       uint32_t at = before;
 #pragma unroll
-      for (int e = 3; e >= 0; --e) {
+      for (int e = kOwn - 1; e >= 0; --e) {
         if (at < need && need <= at + cnt[e]) {
           s_pick[0] = static_cast<uint32_t>(top + e);
           s_pick[1] = at;
@@ -171,69 +198,87 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         at += cnt[e];
       }
     }
-    // the third pass counts where the first did: all have passed the second's barrier, nobody reads that any more
-    if (pass == 1)
-      for (int i = tid; i < kBins; i += kSelThreads) hist0[i] = 0u;
     __syncthreads();
     border |= s_pick[0] << shift;
     need -= s_pick[1];
     __syncthreads();
   }
   // ---- positions kept: every key above the border, and the first `need` at it
-  const int32_t w0 = j0 + warp * per_warp < j1 ? j0 + warp * per_warp : j1, w1 = w0 + per_warp < j1 ? w0 + per_warp : j1;
-  uint32_t gt = 0u, eq = 0u;
-  for (int32_t j = w0 + lane; j < w1; j += 32) {
-    const uint32_t k = key_at(j);
-    gt += k > border;
-    eq += k == border;
-  }
+  uint32_t g0 = 0u, e0 = 0u;                                // above and at the border, before this CTA's stretch
+  if (C > 1) {
+    uint32_t gt = 0u, eq = 0u;
+#pragma unroll 1
+    for (int32_t at = j0; at < j1; at += kChunk) {
+      if (!once) load(at);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    gt += __shfl_xor_sync(0xffffffffu, gt, o);
-    eq += __shfl_xor_sync(0xffffffffu, eq, o);
-  }
-  if (lane == 0) {
-    s_warp[0][warp] = gt;
-    s_warp[1][warp] = eq;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    uint32_t g = 0u, e = 0u;
-    for (int w = 0; w < kSelWarps; ++w) {
-      g += s_warp[0][w];
-      e += s_warp[1][w];
+      for (int e = 0; e < kHold; ++e) {
+        if (at + e * kThreads >= j1) break;
+        const bool live = at + e * kThreads + tid < j1;
+        gt += live && key[e] > border;
+        eq += live && key[e] == border;
+      }
     }
-    s_cnt[0] = g;
-    s_cnt[1] = e;
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    // to the CTAs behind this one
+    if (lane < 2)
+      for (int r = rank + 1; r < C; ++r) add_shared_cluster(mapa_shared(smem_addr(s_before + lane), static_cast<uint32_t>(r)), lane == 0 ? gt : eq);
+    cluster_sync();
+    g0 = s_before[0];
+    e0 = s_before[1];
   }
-  if (C > 1) cluster_sync();
-  else __syncthreads();
-  uint32_t g0 = 0u, e0 = 0u;                                // above and at the border, before this warp's stretch
-  for (int r = 0; r < rank; ++r) {
-    uint32_t g, e;
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(g), "=r"(e)
-                 : "r"(mapa_shared(smem_addr(s_cnt), static_cast<uint32_t>(r))) : "memory");
-    g0 += g;
-    e0 += e;
-  }
-  for (int w = 0; w < warp; ++w) {
-    g0 += s_warp[0][w];
-    e0 += s_warp[1][w];
-  }
-  int32_t* out = a.kept + item * a.cap;
   const uint32_t below = (1u << lane) - 1u;
-  for (int32_t base = w0; base < w1; base += 32) {
-    const int32_t j = base + lane;
-    const uint32_t k = j < w1 ? key_at(j) : 0u;
-    const uint32_t mg = __ballot_sync(0xffffffffu, j < w1 && k > border);
-    const uint32_t me = __ballot_sync(0xffffffffu, j < w1 && k == border);
-    const uint32_t eb = e0 + __popc(me & below), taken = eb < need ? eb : need;
-    const bool keep = j < w1 && (k > border || (k == border && eb < need));
-    if (keep) out[g0 + __popc(mg & below) + taken] = j;
-    g0 += __popc(mg);
-    e0 += __popc(me);
+#pragma unroll 1
+  for (int32_t at = j0; at < j1; at += kChunk) {
+    if (!once) load(at);
+    if (tid < kCounts) s_above[tid] = s_at[tid] = 0u;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kHold; ++e) {
+      if (at + e * kThreads >= j1) break;
+      const bool live = at + e * kThreads + tid < j1;
+      const uint32_t mg = __ballot_sync(0xffffffffu, live && key[e] > border), me = __ballot_sync(0xffffffffu, live && key[e] == border);
+      if (lane == 0) {
+        s_above[e * kWarps + warp] = __popc(mg);
+        s_at[e * kWarps + warp] = __popc(me);
+      }
+    }
+    __syncthreads();
+    const uint32_t ng = tid < kCounts ? s_above[tid] : 0u, ne = tid < kCounts ? s_at[tid] : 0u;
+    const uint32_t bg = sum_before(ng, s_scan), be = sum_before(ne, s_scan);
+    if (tid < kCounts) {
+      s_above[tid] = g0 + bg;
+      s_at[tid] = e0 + be;
+    }
+    if (tid == kThreads - 1) {                              // for the next chunk
+      s_pick[0] = g0 + bg + ng;
+      s_pick[1] = e0 + be + ne;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kHold; ++e) {
+      if (at + e * kThreads >= j1) break;
+      const int32_t j = at + e * kThreads + tid;
+      const bool more = j < j1 && key[e] > border, same = j < j1 && key[e] == border;
+      const uint32_t mg = __ballot_sync(0xffffffffu, more), me = __ballot_sync(0xffffffffu, same);
+      const uint32_t ge = s_above[e * kWarps + warp] + __popc(mg & below), ee = s_at[e * kWarps + warp] + __popc(me & below);
+      if (more || (same && ee < need)) kept[ge + (ee < need ? ee : need)] = j;
+    }
+    g0 = s_pick[0];
+    e0 = s_pick[1];
+    __syncthreads();
   }
-  if (C > 1) cluster_sync();                                // the others may still read this CTA's counts
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, Find<kThreads>::kCtasPerSm) evict_select_kernel(const __grid_constant__ EvictArgs a) {
+  const int C = static_cast<int>(gridDim.x), rank = static_cast<int>(cluster_ctarank());      // a cluster a (sequence, head)
+  const int item = static_cast<int>(blockIdx.y), b = item / a.c.heads, h = item - b * a.c.heads;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int32_t n = length_of(a, b);
+  if (rank == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = n < a.budget ? n : a.budget;
+  if (n > a.budget) find_kept<kThreads>(a, C, rank, h, n, a.table + b * a.ld_table, a.kept + item * a.cap);
 }
 
 template <int D, bool kInPlace>
@@ -308,20 +353,20 @@ bfp8_status bad(const char* fmt, V... v) {
   return set_last_errorf(BFP8_ERR_INVALID_ARG, fmt, v...);
 }
 
+// x blocks for each (sequence, head), as a cluster or not.
 template <typename F>
-cudaError_t launch(F* f, dim3 grid, int threads, int smem, int cluster, const EvictArgs& a, cudaStream_t stream) {
+cudaError_t launch(F* f, int x, int items, bool cluster, int threads, const EvictArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
+  cfg.gridDim = dim3(x, items);
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  attr[1].val.clusterDim = {static_cast<unsigned>(x), 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = cluster && x > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, f, a);
 }
 
@@ -400,27 +445,20 @@ extern "C" bfp8_status bfp8_kv_cache_evict(const bfp8_evict_args* p, const bfp8_
   a.first = static_cast<int32_t>(p->first < a.budget ? p->first : a.budget);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int items = p->batch * a.c.heads;
-  // CTAs of a (sequence, head): as many as leave each SM one and each thread a few keys
-  int cluster = 1;
-  while (cluster < kSelMaxCluster && items * cluster < sms && p->max_kv_len > static_cast<int64_t>(cluster) * 4 * kSelThreads) cluster *= 2;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem);
-  if (e == cudaSuccess) {
-    // the keys of a stretch at its longest
-    const int64_t stretch = (p->max_kv_len + cluster * kSelThreads - 1) / (cluster * kSelThreads) * kSelThreads;
-    const int smem = 2 * kBins * 4 + 4 * static_cast<int>(stretch < kSelKeys ? stretch : kSelKeys);
-    e = launch(evict_select_kernel, dim3(cluster, items), kSelThreads, smem, cluster, a, cs);
+  // (8 heads of a sequence of 60000 tokens: see Find)
+  cudaError_t e;
+  if (items * 4 > sms || p->max_kv_len <= 4 * Find<256>::kChunk / 8) {
+    e = launch(evict_select_kernel<256>, 1, items, false, 256, a, cs);
+  } else {
+    int cluster = 1;
+    while (cluster < kMaxCluster && p->max_kv_len > static_cast<int64_t>(cluster) * Find<1024>::kChunk) cluster *= 2;
+    e = launch(evict_select_kernel<1024>, cluster, items, true, 1024, a, cs);
   }
-  if (e == cudaSuccess && most > 0) {
-    if (in_place) {
-      if (a.cap > 0) {
-        auto f = a.c.dim == 128 ? evict_move_kernel<128, true> : evict_move_kernel<64, true>;
-        e = launch(f, dim3(kMoveCluster, items), kMoveThreads, 0, kMoveCluster, a, cs);
-      }
-    } else {
-      auto f = a.c.dim == 128 ? evict_move_kernel<128, false> : evict_move_kernel<64, false>;
-      const int64_t blocks = (most + kMoveTokens - 1) / kMoveTokens;
-      e = launch(f, dim3(static_cast<unsigned>(blocks), items), kMoveThreads, 0, 1, a, cs);
-    }
+  if (e == cudaSuccess && most > 0 && (!in_place || a.cap > 0)) {
+    auto f = a.c.dim == 128 ? (in_place ? evict_move_kernel<128, true> : evict_move_kernel<128, false>)
+                            : (in_place ? evict_move_kernel<64, true> : evict_move_kernel<64, false>);
+    const int64_t blocks = (most + kMoveTokens - 1) / kMoveTokens;
+    e = launch(f, in_place ? kMoveCluster : static_cast<int>(blocks), items, in_place, kMoveThreads, a, cs);
   }
   if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "cache evict launch: %s", cudaGetErrorString(e));
   return set_last_error(BFP8_OK, "");
