@@ -26,7 +26,7 @@ __device__ __forceinline__ bool begins_here(const WeighArgs& p, int32_t j, int32
 // Sequences of at most 8 * groups (1 or 2) rows, `ctas` SMs (bfp8_kvweigh.cu).
 cudaError_t launch_weigh_few(const WeighArgs& p, int groups, int ctas, cudaStream_t stream);
 
-// The others (bfp8_kvweigh_tile.cu); counters[ctas] zero.  q: tensor map of the queries as bytes [dim, head, token],
+// The others (bfp8_kvweigh_tile.cu); counters[2 * ctas] zero.  q: tensor map of the queries as bytes [dim, head, token],
 // 128-byte swizzle, boxes of 128 bytes x group x weigh_tile_tokens(group, max_q).
 int weigh_tile_tokens(int group, int max_q);
 size_t weigh_tile_partial_bytes(int ctas);

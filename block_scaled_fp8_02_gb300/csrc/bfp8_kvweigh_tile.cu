@@ -1,18 +1,20 @@
 // bfp8_kvweigh_tile.cu -- the attention weight that cached tokens receive from
 // many new tokens, on the 5th-generation tensor cores.
 //
-// A tile of 128 tokens of a sequence and kv head stays while the query rows that
-// see it (new tokens x the group's heads, heads innermost) pass by, up to 256 at a time:
+// A tile of 256 tokens of a sequence and kv head, in two halves, stays while the query rows
+// that see it (new tokens x the group's heads, heads innermost) pass by, up to 128 at a time:
 //   S^T = K Q^T    tcgen05.mma kind::f16 on bf16: K's codes converted once a tile (exact), Q as it is, by TMA
 //   a += exp2(S^T ks scale log2 e - lse log2 e)
 // so that a thread holds a token, its sum stays in a register, and the rows' log
 // sums are the same for all threads (read from shared memory, four at a time).
-// Roles: eight warps of exponentials (two warpgroups, 128 rows each), four that
+// (Tiles of 128 tokens and units of 256 rows asked the L2 cache for twice the
+// queries: a chunk of 4096 tokens at a context of 16384, 64 / 8 heads of 128, took 893 us.)
+// Roles: a warpgroup of exponentials for each half, four warps that
 // convert keys (the next tile's beside this one's rows), one for the MMAs,
 // one for the queries' TMA and one for the rows' log sums.
 //
 // The row tiles of all token tiles form one line that the persistent CTAs
-// share equally; a token tile cut by a border leaves 128 partial sums in the
+// share equally; a token tile cut by a border leaves 256 partial sums in the
 // workspace and the last CTA to arrive adds them in CTA order.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -30,8 +32,8 @@ namespace bfp8 {
 
 namespace {
 
-constexpr int kTile = 128;                 // tokens of a tile
-constexpr int kRowsMax = 256;              // query rows of a unit
+constexpr int kHalf = 128, kTile = 2 * kHalf;  // tokens of a half, and of a tile
+constexpr int kRowsMax = 128;              // query rows of a unit
 constexpr int kWarpMma = 8, kWarpQuery = 9, kWarpBias = 10, kWarpConv = 12, kConvWarps = 4;
 constexpr int kThreads = (kWarpConv + kConvWarps) * 32;
 constexpr int kItemCost = 1;               // places of a token tile in the line besides its units
@@ -40,18 +42,17 @@ constexpr int kBiasSlots = 4;
 
 template <int D>
 struct Cfg {
-  static constexpr int kHalves = D / 64;
-  static constexpr int kA = kTile * D * 2;                // keys of a tile, bf16
+  static constexpr int kParts = D / 64;                   // of a row, 128 bytes each
+  static constexpr int kA = kHalf * D * 2;                // keys of a half, bf16
   static constexpr int kQ = kRowsMax * D * 2;             // queries of a unit
-  static constexpr int kQStages = D == 128 ? 2 : 4;
+  static constexpr int kASlots = D == 128 ? 3 : 4, kQStages = D == 128 ? 3 : 4;
   static constexpr int kOffA = 0;
-  static constexpr int kOffQ = 2 * kA;
+  static constexpr int kOffQ = kASlots * kA;
   static constexpr int kOffBias = kOffQ + kQStages * kQ;
   static constexpr int kOffKs = kOffBias + kBiasSlots * kRowsMax * 4;   // key scale, as the exponent takes it
-  static constexpr int kOffAt = kOffKs + 2 * kTile * 4;                 // where the token's sum is; -1: nowhere
-  static constexpr int kOffSum = kOffAt + 2 * kTile * 8;                // the second warpgroup's sums
-  static constexpr int kOffBar = kOffSum + 2 * kTile * 4;
-  static constexpr int kBars = 2 * kQStages + 2 * kBiasSlots + 8;
+  static constexpr int kOffAt = kOffKs + kASlots * kHalf * 4;           // where the token's sum is; -1: nowhere
+  static constexpr int kOffBar = kOffAt + kASlots * kHalf * 8;
+  static constexpr int kBars = 2 * kQStages + 2 * kBiasSlots + 2 * kASlots + 8;
   static constexpr int kSmem = kOffBar + kBars * 8 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kSeqChunk * 8 <= kOffBias, "sequences' places fit the operands' space");
@@ -59,8 +60,8 @@ struct Cfg {
 
 struct TileArgs {
   WeighArgs w;
-  int32_t* counters;          // one a CTA, zero between calls
-  float* partials;            // two slots a CTA of 128 sums
+  int32_t* counters;          // two a CTA, zero between calls
+  float* partials;            // two slots a CTA of 256 sums
   unsigned long long wait_limit;
   int32_t step;               // new tokens of a unit
 };
@@ -156,12 +157,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.c.heads;
   auto bar = [&](int i) { return sbase + static_cast<uint32_t>(C::kOffBar + 8 * i); };
+  // full and empty: queries, log sums, keys of a half, scores of a half (buffer * 2 + half)
   constexpr int bQf = 0, bQe = bQf + C::kQStages, bBf = bQe + C::kQStages, bBe = bBf + kBiasSlots, bAf = bBe + kBiasSlots,
-                bAe = bAf + 2, bTf = bAe + 2, bTe = bTf + 2;
+                bAe = bAf + C::kASlots, bTf = bAe + C::kASlots, bTe = bTf + 4;
   __shared__ uint32_t s_tmem;
   __shared__ int64_t s_total;
   __shared__ Cursor s_first;
-  __shared__ int s_last;
+  __shared__ int s_last[2];
 
   if (tid == 0) {
     for (int i = 0; i < C::kQStages; ++i) {
@@ -172,11 +174,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(bBf + i), 1);
       mbar_init(bar(bBe + i), 8);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kASlots; ++i) {
       mbar_init(bar(bAf + i), kConvWarps);
-      mbar_init(bar(bAe + i), 1 + 8);
+      mbar_init(bar(bAe + i), 1 + 4);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(bar(bTf + i), 1);
-      mbar_init(bar(bTe + i), 8);
+      mbar_init(bar(bTe + i), 4);
     }
     fence_barrier_init();
   }
@@ -324,21 +328,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 8) {
     // ------------------------------------------------------------ exponentials
-    const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int half = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float* s_ks = reinterpret_cast<const float*>(smem + C::kOffKs);
     const int64_t* s_at = reinterpret_cast<const int64_t*>(smem + C::kOffAt);
-    float* s_sum = reinterpret_cast<float*>(smem + C::kOffSum);
     for (; more; more = next(), ++item) {
-      const int slot = static_cast<int>(item & 1);
-      wait_all(bAf + slot, ph(item, 2), kDevTimeoutEpilogue);
-      const float ks = s_ks[slot * kTile + r];
-      const int64_t at = s_at[slot * kTile + r];
+      const uint32_t hq = 2 * item + half;
+      const int slot = static_cast<int>(hq % C::kASlots);
+      wait_all(bAf + slot, ph(hq, C::kASlots), kDevTimeoutEpilogue);
+      const float ks = s_ks[slot * kHalf + r];
+      const int64_t at = s_at[slot * kHalf + r];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bAe + slot));
-      const int32_t j = c.kt * kTile + r;
+      const int32_t j = c.kt * kTile + half * kHalf + r;
       const bool whole = c.k0 == 0 && c.k1 == c.n;
-      const bool writes = wg == 0 && at >= 0 && ok;
+      const bool writes = at >= 0 && ok;
       float old = 0.f;
       if (writes && whole && !begins_here(p.w, j, c.w.pos0)) old = p.w.w[at];
       int32_t lo, hi;
@@ -348,42 +352,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
         const int bs = static_cast<int>(q % kBiasSlots), ts = static_cast<int>(q & 1);
         const int64_t first = static_cast<int64_t>(c.r0 + k) * p.step;         // new token of the unit's first row
-        // this thread's rows among the 128 columns of its warpgroup
+        // this thread's rows among the unit's columns
         auto column = [&](int32_t i) {
-          int64_t n = i - first;
-          n = n < 0 ? 0 : n > p.step ? p.step : n;
-          const int32_t col = static_cast<int32_t>(n) * a.group - wg * 128;
-          return col < 0 ? 0 : col > 128 ? 128 : col;
+          const int64_t n = i - first;
+          return static_cast<int32_t>(n < 0 ? 0 : n > p.step ? p.step : n) * a.group;
         };
         const int32_t from = column(lo), to = column(hi);
         wait_all(bBf + bs, ph(q, kBiasSlots), kDevTimeoutEpilogue);
-        wait_all(bTf + ts, ph(q, 2), kDevTimeoutEpilogue);
+        wait_all(bTf + 2 * ts + half, ph(q, 2), kDevTimeoutEpilogue);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t tS = tmem + lanes + ts * kRowsMax + wg * 128;
-        const float* bias = reinterpret_cast<const float*>(smem + C::kOffBias) + bs * kRowsMax + wg * 128;
-        if (__all_sync(0xffffffffu, from == 0 && to == 128)) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 64) {
-            uint32_t o[2][32];
-            tmem_ld32(tS + c0, o[0]);
-            tmem_ld32(tS + c0 + 32, o[1]);
-            tmem_wait_ld();
-            reg_fence32(o[0]);
-            reg_fence32(o[1]);
+        const uint32_t tS = tmem + lanes + ts * 2 * kRowsMax + half * kRowsMax;
+        const float* bias = reinterpret_cast<const float*>(smem + C::kOffBias) + bs * kRowsMax;
+        if (__all_sync(0xffffffffu, from == 0 && to == kRowsMax)) {
+          // 32 columns at a time, the next ones on their way from tensor memory meanwhile
+          uint32_t o[2][32];
+          tmem_ld32(tS, o[0]);
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-              const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(bias + c0 + e);
-              float x[4];
-              unpack_f32x2(fma_f32x2(pack_u32x2(o[e / 32][e % 32], o[e / 32][e % 32 + 1]), ks2, b2.x), x[0], x[1]);
-              unpack_f32x2(fma_f32x2(pack_u32x2(o[e / 32][e % 32 + 2], o[e / 32][e % 32 + 3]), ks2, b2.y), x[2], x[3]);
-              sum2[0] = add_f32x2(sum2[0], pack_u32x2(__float_as_uint(ex2(x[0])), __float_as_uint(ex2(x[1]))));
-              sum2[1] = add_f32x2(sum2[1], pack_u32x2(__float_as_uint(ex2(x[2])), __float_as_uint(ex2(x[3]))));
+          for (int x = 0; x < kRowsMax / 32; ++x) {
+            uint32_t(&now)[32] = o[x & 1];
+            tmem_wait_ld();
+            reg_fence32(now);
+            if (x + 1 < kRowsMax / 32) tmem_ld32(tS + 32 * (x + 1), o[(x + 1) & 1]);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(bias + 32 * x + e);
+              float y[4];
+              unpack_f32x2(fma_f32x2(pack_u32x2(now[e], now[e + 1]), ks2, b2.x), y[0], y[1]);
+              unpack_f32x2(fma_f32x2(pack_u32x2(now[e + 2], now[e + 3]), ks2, b2.y), y[2], y[3]);
+              sum2[0] = add_f32x2(sum2[0], pack_u32x2(__float_as_uint(ex2(y[0])), __float_as_uint(ex2(y[1]))));
+              sum2[1] = add_f32x2(sum2[1], pack_u32x2(__float_as_uint(ex2(y[2])), __float_as_uint(ex2(y[3]))));
             }
           }
         } else {
 #pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 32) {
+          for (int c0 = 0; c0 < kRowsMax; c0 += 32) {
             if (!__any_sync(0xffffffffu, from < c0 + 32 && to > c0 && from < to)) continue;
             uint32_t o[32];
             tmem_ld32(tS + c0, o);
@@ -402,41 +405,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar(bTe + ts));
+          mbar_arrive(bar(bTe + 2 * ts + half));
           mbar_arrive(bar(bBe + bs));
         }
       }
       float s0, s1;
       unpack_f32x2(add_f32x2(sum2[0], sum2[1]), s0, s1);
-      float sum = s0 + s1;
-      if (wg == 1) s_sum[slot * kTile + r] = sum;
-      named_bar_sync(1, 256);
-      if (wg == 0) {
-        sum += s_sum[slot * kTile + r];
-        if (whole) {
-          if (writes) p.w.w[at] = old + sum;
-        } else {
-          // ---- the last CTA of the item to arrive adds the parts in CTA order
-          const int c_first = share_of(c.item0, total, ctas), c_last = share_of(c.item0 + c.n - 1, total, ctas);
-          const int slot_id = 2 * blockIdx.x + (c.item0 + c.k0 == u0 ? 0 : 1);
-          p.partials[static_cast<int64_t>(slot_id) * kTile + r] = sum;
+      const float sum = s0 + s1;
+      if (whole) {
+        if (writes && ok) p.w.w[at] = old + sum;
+      } else {
+        // ---- the last CTA of the item to arrive adds the parts in CTA order
+        const int c_first = share_of(c.item0, total, ctas), c_last = share_of(c.item0 + c.n - 1, total, ctas);
+        const int slot_id = 2 * blockIdx.x + (c.item0 + c.k0 == u0 ? 0 : 1);
+        p.partials[static_cast<int64_t>(slot_id) * kTile + half * kHalf + r] = sum;
+        __threadfence();
+        named_bar_sync(1 + half, kHalf);
+        if (r == 0) {
+          const int n = atomicAdd(p.counters + 2 * c_first + half, 1);
+          s_last[half] = n == c_last - c_first;
+          if (s_last[half]) p.counters[2 * c_first + half] = 0;
+        }
+        named_bar_sync(1 + half, kHalf);
+        if (s_last[half] && writes && ok) {
           __threadfence();
-          named_bar_sync(2, kTile);
-          if (r == 0) {
-            const int n = atomicAdd(p.counters + c_first, 1);
-            s_last = n == c_last - c_first;
-            if (s_last) p.counters[c_first] = 0;
-          }
-          named_bar_sync(2, kTile);
-          if (s_last && writes) {
-            __threadfence();
-            // the first CTA's part is its last segment, unless the item begins with its share
-            const int first_slot = 2 * c_first + (share_begin(c_first, total, ctas) < c.item0 ? 1 : 0);
-            float v = 0.f;
-            for (int cc = c_first; cc <= c_last; ++cc)
-              v += __ldcg(p.partials + static_cast<int64_t>(cc == c_first ? first_slot : 2 * cc) * kTile + r);
-            p.w.w[at] = begins_here(p.w, j, c.w.pos0) ? v : p.w.w[at] + v;
-          }
+          // the first CTA's part is its last segment, unless the item begins with its share
+          const int first_slot = 2 * c_first + (share_begin(c_first, total, ctas) < c.item0 ? 1 : 0);
+          float v = 0.f;
+          for (int cc = c_first; cc <= c_last; ++cc)
+            v += __ldcg(p.partials + static_cast<int64_t>(cc == c_first ? first_slot : 2 * cc) * kTile + half * kHalf + r);
+          p.w.w[at] = begins_here(p.w, j, c.w.pos0) ? v : p.w.w[at] + v;
         }
       }
     }
@@ -452,50 +450,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     for (; more; more = next(), ++item) {
-      const int slot = static_cast<int>(item & 1);
+      const uint32_t hq = 2 * item;
+      const int slot[2] = {static_cast<int>(hq % C::kASlots), static_cast<int>((hq + 1) % C::kASlots)};
       if (elect_one()) {
-        wait1(bAf + slot, ph(item, 2));
+        wait1(bAf + slot[0], ph(hq, C::kASlots));
+        wait1(bAf + slot[1], ph(hq + 1, C::kASlots));
         for (int32_t k = c.k0; k < c.k1; ++k, ++q) {
           const int qs = static_cast<int>(q % C::kQStages), ts = static_cast<int>(q & 1);
           wait1(bQf + qs, ph(q, C::kQStages));
-          wait1(bTe + ts, ph(q, 2) ^ 1u);
-          if (!ok) break;
-          tc_fence_after();
           const int64_t left = c.w.q_len - static_cast<int64_t>(c.r0 + k) * p.step;
           const int rows = static_cast<int>(left < p.step ? left : p.step) * a.group;
-          const uint32_t id = idesc_bf16(kTile, (rows + 15) / 16 * 16);
-          const uint32_t ad = lo + ((C::kOffA + slot * C::kA) >> 4), qd = lo + ((C::kOffQ + qs * C::kQ) >> 4);
+          const uint32_t id = idesc_bf16(kHalf, (rows + 15) / 16 * 16);
+          const uint32_t qd = lo + ((C::kOffQ + qs * C::kQ) >> 4);
 #pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
+          for (int half = 0; half < 2; ++half) {
+            wait1(bTe + 2 * ts + half, ph(q, 2) ^ 1u);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t ad = lo + ((C::kOffA + slot[half] * C::kA) >> 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_bf16_ss(tmem + ts * kRowsMax, ad + h * (kTile * 128 >> 4) + 2 * i, qd + h * (kRowsMax * 128 >> 4) + 2 * i, hi, id,
-                          (h | i) != 0);
+            for (int h = 0; h < C::kParts; ++h)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_bf16_ss(tmem + ts * 2 * kRowsMax + half * kRowsMax, ad + h * (kHalf * 128 >> 4) + 2 * i,
+                            qd + h * (kRowsMax * 128 >> 4) + 2 * i, hi, id, (h | i) != 0);
+            mma_commit(bar(bTf + 2 * ts + half));
+          }
+          if (!ok) break;
           mma_commit(bar(bQe + qs));
-          mma_commit(bar(bTf + ts));
           done = q + 1;
         }
         if (ok) {
-          mma_commit(bar(bAe + slot));
+          mma_commit(bar(bAe + slot[0]));
+          mma_commit(bar(bAe + slot[1]));
           items_done = item + 1;
         }
       }
       __syncwarp();
     }
-    // every commit has arrived before the CTA exits
+    // every commit has arrived before the CTA exits (the last one comes after all others)
     if (elect_one()) {
       for (uint32_t i = done > C::kQStages ? done - C::kQStages : 0; i < done; ++i)
         mbar_wait_bounded(bar(bQe + static_cast<int>(i % C::kQStages)), ph(i, C::kQStages), p.wait_limit);
-      for (uint32_t i = done > 2 ? done - 2 : 0; i < done; ++i)
-        mbar_wait_bounded(bar(bTf + static_cast<int>(i & 1)), ph(i, 2), p.wait_limit);
       if (ok)
-        for (uint32_t i = items_done > 2 ? items_done - 2 : 0; i < items_done; ++i)
-          mbar_wait_bounded(bar(bAe + static_cast<int>(i & 1)), ph(i, 2), p.wait_limit);
+        for (uint32_t i = items_done > 0 ? 2 * items_done - 2 : 0; i < 2 * items_done; ++i)
+          mbar_wait_bounded(bar(bAe + static_cast<int>(i % C::kASlots)), ph(i, C::kASlots), p.wait_limit);
     }
     __syncwarp();
   } else if (warp == kWarpQuery) {
     // ---------------------------------------------------------------- queries
-    const uint32_t bytes = static_cast<uint32_t>(C::kHalves * 128 * p.step * a.group);
+    const uint32_t bytes = static_cast<uint32_t>(C::kParts * 128 * p.step * a.group);
     for (; more && ok; more = next()) {
       for (int32_t k = c.k0; k < c.k1; ++k) {
         const int qs = static_cast<int>(q % C::kQStages);
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t dst = sbase + static_cast<uint32_t>(C::kOffQ + qs * C::kQ);
           const int32_t row = static_cast<int32_t>(c.w.row0 + static_cast<int64_t>(c.r0 + k) * p.step);
 #pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
+          for (int h = 0; h < C::kParts; ++h)
             tma_load_3d(dst + h * kRowsMax * 128, &tmQ, bar(bQf + qs), 128 * h, c.h * a.group, row);
         }
         __syncwarp();
@@ -555,14 +559,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cw = warp - kWarpConv, ch = lane % CH, sub = lane / CH;
     float* s_ks = reinterpret_cast<float*>(smem + C::kOffKs);
     int64_t* s_at = reinterpret_cast<int64_t*>(smem + C::kOffAt);
-    // this warp's 32 tokens: a lane looks up its token's page, then eight (or four) lanes read a token
+    // this warp's 32 tokens of a half: a lane looks up its token's page, then eight (or four) lanes read a token
     struct Data {
       uint4 k[IT];
       float ks;
       int64_t at;
     };
-    auto fetch = [&](Data& d) {
-      const int32_t j = c.kt * kTile + cw * 32 + lane;
+    auto fetch = [&](Data& d, int half) {
+      const int32_t j = c.kt * kTile + half * kHalf + cw * 32 + lane;
       int64_t code = -1;
       d.at = -1;
       d.ks = 0.f;
@@ -584,14 +588,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     Data cur, nxt;
-    if (more) fetch(cur);
+    uint32_t hq = 0;                                              // halves begun
+    if (more) fetch(cur, 0);
     while (more && ok) {
-      const int slot = static_cast<int>(item & 1);
-      more = next();
-      if (more) fetch(nxt);
-      wait_warp(bAe + slot, ph(item, 2) ^ 1u, kDevTimeoutProducer);
+      const int slot = static_cast<int>(hq % C::kASlots);
+      if (hq & 1) more = next();
+      if (more) fetch(nxt, (hq & 1) ^ 1);
+      wait_warp(bAe + slot, ph(hq, C::kASlots) ^ 1u, kDevTimeoutProducer);
       if (!ok) break;
-      uint8_t* dst = smem + C::kOffA + slot * C::kA + (ch / 4) * (kTile * 128);
+      uint8_t* dst = smem + C::kOffA + slot * C::kA + (ch / 4) * (kHalf * 128);
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
         const int row = cw * 32 + i * RPI + sub;
@@ -603,13 +608,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4*>(dst + row * 128 + ((c0 ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(dst + row * 128 + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      s_ks[slot * kTile + cw * 32 + lane] = cur.ks;
-      s_at[slot * kTile + cw * 32 + lane] = cur.at;
+      s_ks[slot * kHalf + cw * 32 + lane] = cur.ks;
+      s_at[slot * kHalf + cw * 32 + lane] = cur.at;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bAf + slot));
       cur = nxt;
-      ++item;
+      ++hq;
     }
   }
   __syncthreads();
