@@ -626,8 +626,9 @@ def _stream_of(stream) -> int:
 
 def _on(dev: torch.device, *tensors) -> None:
     """All on one device: an address of another one (a length left on the host, say) would fault in the kernel."""
+    index = dev.index                          # (a comparison of numbers: half the time of one of devices)
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index and t.device != dev:
             raise ValueError(f"a tensor is on {t.device}, the others on {dev}")
 
 
@@ -798,16 +799,17 @@ def _attention_workspace(device, num_heads: int, num_kv_heads: int, head_dim: in
 
 def _check_query(q: torch.Tensor, cache: KVCache) -> None:
     D = cache.k.shape[3]
-    if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
+    qs = q.shape
+    if len(qs) != 3 or qs[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
         raise ValueError(f"q must be bfloat16 [total_q, heads, {D}] with unit inner stride")
 
 
 def _check_context(table: torch.Tensor, cu_q: torch.Tensor, lens: torch.Tensor, names=("block_table", "cu_q", "kv_lens")):
     """Checks the tables and lengths of sequences (or prefixes); how many there are, the table's row stride and width."""
-    ts, tst = table.shape, table.stride()
-    if lens.dim() != 1 or cu_q.shape != (len(lens) + 1,) or not lens.is_contiguous() or not cu_q.is_contiguous():
+    ts, tst, ls = table.shape, table.stride(), lens.shape
+    B = ls[0] if len(ls) == 1 else -1
+    if B < 0 or cu_q.shape != (B + 1,) or not lens.is_contiguous() or not cu_q.is_contiguous():
         raise ValueError(f"{names[2]} must be a contiguous [batch] tensor and {names[1]} a contiguous [batch + 1] one")
-    B = len(lens)
     if len(ts) != 2 or ts[0] != B or (B > 0 and ts[1] > 1 and tst[1] != 1):
         raise ValueError(f"{names[0]} must be [{B}, max_pages] with unit inner stride")
     if table.dtype != torch.int32 or cu_q.dtype != torch.int32 or lens.dtype != torch.int32:
@@ -887,7 +889,8 @@ def bfp8_shared_prefix_attention(q: torch.Tensor, cache: KVCache, prefix_table: 
     them: prefix f's prefix_lens[f] tokens (int32 [prefixes]), on the pages prefix_table[f] (int32 [prefixes, max_pages]),
     are seen by the rows prefix_cu_q[f] .. prefix_cu_q[f+1] of q (int32 [prefixes + 1]; max_prefix_q_len bounds how many
     they are, max_prefix_len the lengths).  block_table, cu_q, kv_lens and their bounds are those of the sequences' own
-    tokens behind the prefix.  Returns out or (out, lse), of one softmax over both parts."""
+    tokens behind the prefix.  Returns out or (out, lse), of one softmax over both parts.  (The workspace holds the
+    prefixes' part in fp32: 4 (head_dim + 1) bytes a row and head.)"""
     _check_query(q, cache)
     _, H, _, D = cache.k.shape
     qs, dev = q.shape, q.device
@@ -906,7 +909,7 @@ def bfp8_shared_prefix_attention(q: torch.Tensor, cache: KVCache, prefix_table: 
         need = 0
         if T and B:
             mq = min(max_q_len, _LONG_Q)
-            need = _shared_workspace(dev, Hq, H, D, min(max_prefix_q_len, _LONG_Q) if F else mq, mq) + 4 * T * Hq * (D + 1)
+            need = _shared_workspace(dev, Hq, H, D, min(max_prefix_q_len, _LONG_Q) if F else mq, mq) + (4 * T * Hq * (D + 1) if F else 0)
         workspace = _workspace(need, dev, stream, sp)
     (qt, qh), (ot, oh) = _axis(T, Hq, D, q.stride()), _axis(T, Hq, D, out.stride())
     a = _pack_attention.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0, T, Hq, B, qt, qh,
@@ -991,18 +994,21 @@ def bfp8_kv_cache_evict(cache: KVCache, weights: torch.Tensor, block_table: torc
     """Shortens sequences to budget tokens: every kv head keeps its first `first`, its last `recent` and of the others
     the heaviest by weights [pages, kv_heads, page_size] (fp32, as bfp8_kv_cache_weigh sums them), in their order.
     They move with codes, scales and weights to the pages out_table (int32 [batch, max_pages], none of them among
-    those of block_table; shorter sequences are copied whole), or, without one, to the first pages of block_table.
+    those of block_table; shorter sequences are copied whole), or, without one, to the first pages of block_table
+    (so too where out_table is block_table, or its first columns).
     Returns the new lengths min(kv_lens, budget) (int32 [batch], into new_lens if given; not kv_lens itself)."""
     _, H, page, _ = cache.k.shape
     wp, wh = _weight_strides(weights, cache)
-    if kv_lens.dim() != 1 or kv_lens.dtype != torch.int32 or not kv_lens.is_contiguous():
+    ls = kv_lens.shape
+    if len(ls) != 1 or kv_lens.dtype != torch.int32 or not kv_lens.is_contiguous():
         raise ValueError("kv_lens must be a contiguous [batch] int32 tensor")
-    B, dev = len(kv_lens), kv_lens.device
+    B, dev = ls[0], kv_lens.device
 
     def table(t, name):
-        if t.dim() != 2 or t.shape[0] != B or t.dtype != torch.int32 or (B > 0 and t.shape[1] > 1 and t.stride(1) != 1):
+        ts, st = t.shape, t.stride()
+        if len(ts) != 2 or ts[0] != B or t.dtype != torch.int32 or (B > 0 and ts[1] > 1 and st[1] != 1):
             raise ValueError(f"{name} must be int32 [{B}, max_pages] with unit inner stride")
-        return t.data_ptr(), t.stride(0) if B > 1 else t.shape[1], t.shape[1]
+        return t.data_ptr(), st[0] if B > 1 else ts[1], ts[1]
 
     tp, ld, width = table(block_table, "block_table")
     op, ld_out, out_width = (0, 0, 0) if out_table is None else table(out_table, "out_table")

@@ -84,23 +84,28 @@ bfp8_status check_workspace(const void* workspace, size_t bytes, int* sms, int**
   return BFP8_OK;
 }
 
+// Tensor maps of the keys' and values' codes.
+struct CacheMaps {
+  CUtensorMap k, v;
+};
+bfp8_status encode_maps(const CacheView& c, CacheMaps* m) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(c.dim), static_cast<uint64_t>(c.page_size),
+                            static_cast<uint64_t>(c.heads), static_cast<uint64_t>(c.num_pages)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(c.st_tok), static_cast<uint64_t>(c.st_head),
+                               static_cast<uint64_t>(c.st_page)};
+  const uint32_t box[4] = {static_cast<uint32_t>(c.dim),
+                           static_cast<uint32_t>(c.page_size < 128 ? c.page_size : 128), 1u, 1u};
+  const bfp8_status st = encode_bytes_tiled(&m->k, c.k, 4, dims, strides, box, c.dim);
+  return st != BFP8_OK ? st : encode_bytes_tiled(&m->v, c.v, 4, dims, strides, box, c.dim);
+}
+
 // Launches what one part takes: the kernel for many rows, that for few, or both.  after_tile: a tile kernel of
 // the prefixes' part is the launch before, and this part (kAttnOwn) needs it only where rows are joined.
 // *last_tile: the last launch is the tile kernel's.
-bfp8_status launch_part(AttnArgs a, AttnMode mode, int sms, void* workspace, bool after_tile, cudaStream_t cs,
+bfp8_status launch_part(const CacheMaps& m, AttnArgs a, AttnMode mode, int sms, void* workspace, bool after_tile, cudaStream_t cs,
                         bool* last_tile) {
   const int groups = few_groups(a.group, a.max_q);
   a.few_rows = groups * 8;
-  const uint64_t dims[4] = {static_cast<uint64_t>(a.c.dim), static_cast<uint64_t>(a.c.page_size),
-                            static_cast<uint64_t>(a.c.heads), static_cast<uint64_t>(a.c.num_pages)};
-  const uint64_t strides[3] = {static_cast<uint64_t>(a.c.st_tok), static_cast<uint64_t>(a.c.st_head),
-                               static_cast<uint64_t>(a.c.st_page)};
-  const uint32_t box[4] = {static_cast<uint32_t>(a.c.dim),
-                           static_cast<uint32_t>(a.c.page_size < 128 ? a.c.page_size : 128), 1u, 1u};
-  CUtensorMap mk, mv;
-  bfp8_status st;
-  if ((st = encode_bytes_tiled(&mk, a.c.k, 4, dims, strides, box, a.c.dim)) != BFP8_OK) return st;
-  if ((st = encode_bytes_tiled(&mv, a.c.v, 4, dims, strides, box, a.c.dim)) != BFP8_OK) return st;
   int32_t* counters = static_cast<int32_t*>(workspace);
   char* partials = static_cast<char*>(workspace) + kCounterHeaderBytes;
   cudaError_t e = cudaSuccess;
@@ -111,10 +116,10 @@ bfp8_status launch_part(AttnArgs a, AttnMode mode, int sms, void* workspace, boo
                    (!many || a.total_q <= static_cast<int64_t>(a.batch - 1) * a.max_q + a.few_rows / a.group);
   if (!few) a.few_rows = 0;
   if (many)
-    e = launch_attn_tile(mk, mv, a, mode, sms, counters + sms,
+    e = launch_attn_tile(m.k, m.v, a, mode, sms, counters + sms,
                          reinterpret_cast<float*>(partials + few_bytes(a.group, a.c.dim, a.max_q, sms)), cs);
   if (e == cudaSuccess && few)
-    e = launch_attn_decode(mk, mv, a, mode, groups, sms, counters, reinterpret_cast<float*>(partials),
+    e = launch_attn_decode(m.k, m.v, a, mode, groups, sms, counters, reinterpret_cast<float*>(partials),
                            many ? 1 : after_tile ? 2 : 0, cs);
   if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
   *last_tile = !few;
@@ -217,7 +222,9 @@ extern "C" bfp8_status bfp8_paged_attention(const bfp8_attention_args* p, const 
                        [&](int n) { return workspace_bytes_for(a.group, a.c.dim, a.max_q, n); });
   if (st != BFP8_OK) return st;
   bool tile = false;
-  if ((st = launch_part(a, kAttnWhole, sms, workspace, false, static_cast<cudaStream_t>(stream), &tile)) != BFP8_OK) return st;
+  CacheMaps m;
+  if ((st = encode_maps(a.c, &m)) != BFP8_OK) return st;
+  if ((st = launch_part(m, a, kAttnWhole, sms, workspace, false, static_cast<cudaStream_t>(stream), &tile)) != BFP8_OK) return st;
   return set_last_error(BFP8_OK, "");
 }
 
@@ -266,6 +273,8 @@ extern "C" bfp8_status bfp8_shared_prefix_attention(const bfp8_attention_args* p
   if (st != BFP8_OK) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   bool tile = false;
+  CacheMaps m;
+  if ((st = encode_maps(a.c, &m)) != BFP8_OK) return st;
   if (!none) {
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + shared_scratch_bytes(a.group, a.c.dim, pq, a.max_q, sms));
     a.part_lse2 = a.part_o + a.total_q * a.heads * a.c.dim;
@@ -283,8 +292,8 @@ extern "C" bfp8_status bfp8_shared_prefix_attention(const bfp8_attention_args* p
     b.max_q = f->max_q_len;
     b.causal = 0;
     b.window = 0;
-    if ((st = launch_part(b, kAttnPrefix, sms, workspace, false, cs, &tile)) != BFP8_OK) return st;
+    if ((st = launch_part(m, b, kAttnPrefix, sms, workspace, false, cs, &tile)) != BFP8_OK) return st;
   }
-  if ((st = launch_part(a, none ? kAttnWhole : kAttnOwn, sms, workspace, tile, cs, &tile)) != BFP8_OK) return st;
+  if ((st = launch_part(m, a, none ? kAttnWhole : kAttnOwn, sms, workspace, tile, cs, &tile)) != BFP8_OK) return st;
   return set_last_error(BFP8_OK, "");
 }

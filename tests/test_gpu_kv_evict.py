@@ -157,6 +157,19 @@ def test_bounds_above_the_lengths(dev):
     check(dev, c, max_kv=40000, in_place=True)
 
 
+def test_block_table_as_its_own_destination(dev):
+    """The same as none: in place."""
+    c = make([1300, 80], 600, H=1)
+    want, lens = evict_ref([c["k"].view(torch.uint8), c["w"]], c["w"], c["table"], c["kv"], 600, 7, 0)
+    for columns in (c["table"].shape[1], 10):
+        d = {n: c[n].to(dev) for n in ("k", "v", "ks", "vs", "w")}
+        table = c["table"].to(dev)
+        got = bf.bfp8_kv_cache_evict(bf.KVCache(d["k"], d["v"], d["ks"], d["vs"]), d["w"], table, ints(c["kv"], dev), 1300, 600, recent=7,
+                                     out_table=table[:, :columns])
+        assert got.tolist() == lens
+        assert torch.equal(d["k"].view(torch.uint8).cpu(), want[0]) and torch.equal(d["w"].cpu(), want[1])
+
+
 def test_lengths_for_the_caller(dev):
     c = make([300, 80], 64)
     lens = torch.empty(2, dtype=torch.int32, device=dev)
