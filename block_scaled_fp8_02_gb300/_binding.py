@@ -873,10 +873,12 @@ def bfp8_shared_prefix_attention_workspace_size(num_heads: int, num_kv_heads: in
     return int(n.value)
 
 
-# Of the scratch of both parts; what the rows take is added for each call.
 @functools.lru_cache(maxsize=None)
-def _shared_workspace(device, num_heads: int, num_kv_heads: int, head_dim: int, max_prefix_q_len: int, max_q_len: int) -> int:
-    return bfp8_shared_prefix_attention_workspace_size(num_heads, num_kv_heads, head_dim, max_prefix_q_len, max_q_len, 0)
+def _shared_workspace(device, num_heads: int, num_kv_heads: int, head_dim: int, max_prefix_q_len: int, max_q_len: int) -> tuple[int, int]:
+    """The bytes of a call without rows, and those that each row of q adds."""
+    none, one = (bfp8_shared_prefix_attention_workspace_size(num_heads, num_kv_heads, head_dim, max_prefix_q_len, max_q_len, n)
+                 for n in (0, 1))
+    return none, one - none
 
 
 def bfp8_shared_prefix_attention(q: torch.Tensor, cache: KVCache, prefix_table: torch.Tensor, prefix_cu_q: torch.Tensor,
@@ -890,7 +892,7 @@ def bfp8_shared_prefix_attention(q: torch.Tensor, cache: KVCache, prefix_table: 
     are seen by the rows prefix_cu_q[f] .. prefix_cu_q[f+1] of q (int32 [prefixes + 1]; max_prefix_q_len bounds how many
     they are, max_prefix_len the lengths).  block_table, cu_q, kv_lens and their bounds are those of the sequences' own
     tokens behind the prefix.  Returns out or (out, lse), of one softmax over both parts.  (The workspace holds the
-    prefixes' part in fp32: 4 (head_dim + 1) bytes a row and head.)"""
+    prefixes' part in fp32, and in some calls the own one: up to 8 (head_dim + 1) bytes a row and head.)"""
     _check_query(q, cache)
     _, H, _, D = cache.k.shape
     qs, dev = q.shape, q.device
@@ -909,7 +911,8 @@ def bfp8_shared_prefix_attention(q: torch.Tensor, cache: KVCache, prefix_table: 
         need = 0
         if T and B:
             mq = min(max_q_len, _LONG_Q)
-            need = _shared_workspace(dev, Hq, H, D, min(max_prefix_q_len, _LONG_Q) if F else mq, mq) + (4 * T * Hq * (D + 1) if F else 0)
+            need, per_row = _shared_workspace(dev, Hq, H, D, min(max_prefix_q_len, _LONG_Q) if F else mq, mq)
+            need += per_row * T if F else 0
         workspace = _workspace(need, dev, stream, sp)
     (qt, qh), (ot, oh) = _axis(T, Hq, D, q.stride()), _axis(T, Hq, D, out.stride())
     a = _pack_attention.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0, T, Hq, B, qt, qh,

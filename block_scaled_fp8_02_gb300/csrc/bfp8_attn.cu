@@ -5,9 +5,11 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "bfp8_attn.cuh"
 #include "bfp8_internal.h"
+#include "bfp8_ptx.cuh"
 
 namespace bfp8 {
 
@@ -46,13 +48,24 @@ size_t workspace_bytes_for(int group, int dim, int max_q, int sms) {
          (has_many(group, max_q) ? attn_tile_partial_bytes(dim, sms) : 0);
 }
 
-// The prefixes' part of every row, behind what either part's kernels take.
-size_t shared_scratch_bytes(int group, int dim, int max_prefix_q, int max_q, int sms) {
-  const size_t a = workspace_bytes_for(group, dim, max_prefix_q, sms), b = workspace_bytes_for(group, dim, max_q, sms);
+// A call over shared prefixes: its parts may run beside each other, so the partial rows of the kernel for few rows (of either)
+// and those of the other have places of their own.
+size_t shared_few_bytes(int group, int dim, int max_prefix_q, int max_q, int sms) {
+  const size_t a = few_bytes(group, dim, max_prefix_q, sms), b = few_bytes(group, dim, max_q, sms);
   return a > b ? a : b;
 }
-size_t shared_rows_bytes(int64_t total_q, int heads, int dim) {
-  return static_cast<size_t>(total_q) * heads * (dim + 1) * sizeof(float);
+size_t shared_scratch_bytes(int group, int dim, int max_prefix_q, int max_q, int sms) {
+  const bool tile = has_many(group, max_prefix_q) || has_many(group, max_q);
+  return kCounterHeaderBytes + shared_few_bytes(group, dim, max_prefix_q, max_q, sms) + (tile ? attn_tile_partial_bytes(dim, sms) : 0);
+}
+// Are both parts computed apart, beside each other, and joined in a launch of their own?  Where the prefixes' takes the tile kernel and
+// the own one the kernel for few rows: many sequences' single tokens.  64 of them, own contexts up to 1000 behind a prefix of
+// 8192, 64 / 8 heads of 128: 98 us with the own part's rows waiting for the prefix's.  (With more new tokens the parts' fp32 rows
+// would take longer to write and read than the wait.)
+bool parts_apart(int group, int max_prefix_q, int max_q) { return has_many(group, max_prefix_q) && !has_many(group, max_q); }
+// Behind all that: a part's rows in fp32 and their log2 sums, for each part that is not joined at once.
+size_t shared_rows_bytes(int64_t total_q, int heads, int dim, bool apart) {
+  return static_cast<size_t>(total_q) * heads * (dim + 1) * sizeof(float) * (apart ? 2 : 1);
 }
 
 // Sequences (or prefixes), rows and context of a call, checked apart from the pointers.
@@ -99,30 +112,89 @@ bfp8_status encode_maps(const CacheView& c, CacheMaps* m) {
   return st != BFP8_OK ? st : encode_bytes_tiled(&m->v, c.v, 4, dims, strides, box, c.dim);
 }
 
-// Launches what one part takes: the kernel for many rows, that for few, or both.  after_tile: a tile kernel of
-// the prefixes' part is the launch before, and this part (kAttnOwn) needs it only where rows are joined.
-// *last_tile: the last launch is the tile kernel's.
-bfp8_status launch_part(const CacheMaps& m, AttnArgs a, AttnMode mode, int sms, void* workspace, bool after_tile, cudaStream_t cs,
-                        bool* last_tile) {
+// Can a sequence be short enough for the kernel for few rows?  Not if the others at their longest leave this
+// one too many tokens (always so for a single chunk): then its launch is saved.
+bool few_launched(const AttnArgs& a) {
+  return a.group <= kFewRows && (!has_many(a.group, a.max_q) ||
+                                 a.total_q <= static_cast<int64_t>(a.batch - 1) * a.max_q + 8 * few_groups(a.group, a.max_q) / a.group);
+}
+
+// SMs that the tile kernel gets for the prefixes' part `b` where the kernel for few rows takes the own part `a` beside it: by the
+// cycles that each needs at its bounds (own contexts at three quarters of theirs), a block's and an item's own among them.  64 sequences,
+// own contexts up to 1000 behind 8192 tokens, 64 / 8 heads of 128, by the tile kernel's SMs: 48 81 us, 64 69, 80 71, 96 78, 112 104; 79
+// with the kernel for few rows behind the other, on the SMs that it leaves.
+int tile_sms(const AttnArgs& a, const AttnArgs& b, int sms) {
+  const double blocks = static_cast<double>(b.batch) * b.c.heads * ((static_cast<int64_t>(b.max_q) * b.group + 255) / 256);
+  const double tile = blocks * (static_cast<double>(b.max_kv) / 128 + 8) * 4500;
+  const double few = static_cast<double>(a.batch) * a.c.heads * (0.75 * static_cast<double>(a.max_kv) / 128 + 4) * 1340;
+  const int n = static_cast<int>(sms * (tile / (tile + few)));
+  return n < sms / 4 ? sms / 4 : n > sms * 3 / 4 ? sms * 3 / 4 : n;
+}
+
+// Joins both parts of the rows of all sequences: a warp a (row, head).
+struct JoinArgs {
+  AttnArgs a;                         // the prefixes' part
+  const float* own_o;                 // the own part's
+  const float* own_lse2;
+};
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_parts_kernel(const __grid_constant__ JoinArgs p) {
+  const AttnArgs& a = p.a;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);      // token * heads + head
+  const int lane = threadIdx.x & 31;
+  const int64_t token = row / a.heads;
+  const int head = static_cast<int>(row - token * a.heads);
+  if (token >= a.total_q || token < a.cu_q[0] || token >= a.cu_q[a.batch]) return;
+  using Vec = typename std::conditional<D == 128, float4, float2>::type;
+  const Joined j = join_prefix(a, token, head, __ldcg(p.own_lse2 + row));
+  const Vec y = __ldcg(reinterpret_cast<const Vec*>(p.own_o + row * D) + lane);
+  Vec x{};
+  if (j.covered) x = __ldcg(reinterpret_cast<const Vec*>(a.part_o + row * D) + lane);
+  float o[D / 32];
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e)
+    o[e] = fmaf(reinterpret_cast<const float*>(&x)[e], j.prefix, reinterpret_cast<const float*>(&y)[e] * j.own);
+  __nv_bfloat16* dst = a.out + token * a.o_st + head * a.o_sh + lane * (D / 32);
+  if constexpr (D == 128) st_global_v2(dst, pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+  else *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0], o[1]);
+  if (a.lse != nullptr && lane == 0) a.lse[row] = j.lse2 * 0.6931471805599453f;
+}
+
+cudaError_t launch_join(const JoinArgs& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.a.total_q * p.a.heads + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, p.a.c.dim == 128 ? join_parts_kernel<128> : join_parts_kernel<64>, p);
+}
+
+// Launches what one part (or all) takes: the kernel for many rows, that for few, or both.  few_space: bytes of the partial rows
+// of the kernel for few rows, before the other's; ctas: SMs that it takes.  beside: the launch before is the tile kernel's, of
+// another part, and this one takes the kernel for few rows alone, which needs nothing of it.
+bfp8_status launch_part(const CacheMaps& m, AttnArgs a, AttnMode mode, int sms, int ctas, void* workspace, size_t few_space,
+                        bool beside, cudaStream_t cs) {
   const int groups = few_groups(a.group, a.max_q);
   a.few_rows = groups * 8;
   int32_t* counters = static_cast<int32_t*>(workspace);
   char* partials = static_cast<char*>(workspace) + kCounterHeaderBytes;
   cudaError_t e = cudaSuccess;
-  // Can a sequence be short enough for the kernel for few rows?  Not if the others at their longest leave this
-  // one too many tokens (always so for a single chunk): then its launch is saved.
-  const bool many = has_many(a.group, a.max_q);
-  const bool few = a.group <= kFewRows &&
-                   (!many || a.total_q <= static_cast<int64_t>(a.batch - 1) * a.max_q + a.few_rows / a.group);
+  const bool many = has_many(a.group, a.max_q), few = few_launched(a);
   if (!few) a.few_rows = 0;
   if (many)
-    e = launch_attn_tile(m.k, m.v, a, mode, sms, counters + sms,
-                         reinterpret_cast<float*>(partials + few_bytes(a.group, a.c.dim, a.max_q, sms)), cs);
+    e = launch_attn_tile(m.k, m.v, a, mode, ctas, counters + sms,
+                         reinterpret_cast<float*>(partials + few_space), cs);
   if (e == cudaSuccess && few)
-    e = launch_attn_decode(m.k, m.v, a, mode, groups, sms, counters, reinterpret_cast<float*>(partials),
-                           many ? 1 : after_tile ? 2 : 0, cs);
+    e = launch_attn_decode(m.k, m.v, a, mode, groups, ctas, counters, reinterpret_cast<float*>(partials),
+                           many || beside, cs);
   if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
-  *last_tile = !few;
   return BFP8_OK;
 }
 
@@ -221,10 +293,11 @@ extern "C" bfp8_status bfp8_paged_attention(const bfp8_attention_args* p, const 
   st = check_workspace(workspace, workspace_bytes, &sms, &a.err,
                        [&](int n) { return workspace_bytes_for(a.group, a.c.dim, a.max_q, n); });
   if (st != BFP8_OK) return st;
-  bool tile = false;
   CacheMaps m;
   if ((st = encode_maps(a.c, &m)) != BFP8_OK) return st;
-  if ((st = launch_part(m, a, kAttnWhole, sms, workspace, false, static_cast<cudaStream_t>(stream), &tile)) != BFP8_OK) return st;
+  if ((st = launch_part(m, a, kAttnWhole, sms, sms, workspace, few_bytes(a.group, a.c.dim, a.max_q, sms), false,
+                        static_cast<cudaStream_t>(stream))) != BFP8_OK)
+    return st;
   return set_last_error(BFP8_OK, "");
 }
 
@@ -240,7 +313,7 @@ extern "C" bfp8_status bfp8_shared_prefix_attention_workspace_size(int num_heads
   int* err = nullptr;
   if ((st = device_for_call(&sms, &err)) != BFP8_OK) return st;
   *bytes = shared_scratch_bytes(num_heads / num_kv_heads, head_dim, max_prefix_q_len, max_q_len, sms) +
-           shared_rows_bytes(total_q, num_heads, head_dim);
+           shared_rows_bytes(total_q, num_heads, head_dim, parts_apart(num_heads / num_kv_heads, max_prefix_q_len, max_q_len));
   return set_last_error(BFP8_OK, "");
 }
 
@@ -266,34 +339,49 @@ extern "C" bfp8_status bfp8_shared_prefix_attention(const bfp8_attention_args* p
       return set_last_errorf(BFP8_ERR_ALIGNMENT, "prefix: pointers must be 4-byte aligned");
   }
   int sms = 0;
-  const size_t rows = none ? 0 : shared_rows_bytes(a.total_q, a.heads, a.c.dim);
   const int pq = none ? a.max_q : f->max_q_len;
+  const bool apart = !none && parts_apart(a.group, pq, a.max_q);
+  const size_t rows = none ? 0 : shared_rows_bytes(a.total_q, a.heads, a.c.dim, apart);
   st = check_workspace(workspace, workspace_bytes, &sms, &a.err,
                        [&](int n) { return shared_scratch_bytes(a.group, a.c.dim, pq, a.max_q, n) + rows; });
   if (st != BFP8_OK) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  bool tile = false;
+  const size_t few_space = shared_few_bytes(a.group, a.c.dim, pq, a.max_q, sms);
   CacheMaps m;
   if ((st = encode_maps(a.c, &m)) != BFP8_OK) return st;
-  if (!none) {
-    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + shared_scratch_bytes(a.group, a.c.dim, pq, a.max_q, sms));
-    a.part_lse2 = a.part_o + a.total_q * a.heads * a.c.dim;
-    a.part_cu = f->cu_q;
-    a.prefixes = f->prefixes;
-    AttnArgs b = a;
-    b.out = nullptr;
-    b.lse = nullptr;
-    b.table = f->block_table;
-    b.ld_table = f->ld_table;
-    b.cu_q = f->cu_q;
-    b.kv_lens = f->lens;
-    b.max_kv = f->max_len;
-    b.batch = f->prefixes;
-    b.max_q = f->max_q_len;
-    b.causal = 0;
-    b.window = 0;
-    if ((st = launch_part(m, b, kAttnPrefix, sms, workspace, false, cs, &tile)) != BFP8_OK) return st;
+  if (none) {
+    if ((st = launch_part(m, a, kAttnWhole, sms, sms, workspace, few_space, false, cs)) != BFP8_OK) return st;
+    return set_last_error(BFP8_OK, "");
   }
-  if ((st = launch_part(m, a, none ? kAttnWhole : kAttnOwn, sms, workspace, tile, cs, &tile)) != BFP8_OK) return st;
+  // rows of one part or both (whole rows: read and written in vectors), then their sums
+  const int64_t row_floats = a.total_q * a.heads * a.c.dim;
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + shared_scratch_bytes(a.group, a.c.dim, pq, a.max_q, sms));
+  a.part_lse2 = a.part_o + (apart ? 2 : 1) * row_floats;
+  a.part_cu = f->cu_q;
+  a.prefixes = f->prefixes;
+  AttnArgs b = a;
+  b.table = f->block_table;
+  b.ld_table = f->ld_table;
+  b.cu_q = f->cu_q;
+  b.kv_lens = f->lens;
+  b.max_kv = f->max_len;
+  b.batch = f->prefixes;
+  b.max_q = f->max_q_len;
+  b.causal = 0;
+  b.window = 0;
+  // (beside only the tile kernel: one for few rows before it has the same partial rows and counters)
+  const bool beside = apart && !few_launched(b);
+  const int ctas = beside ? tile_sms(a, b, sms) : sms;
+  if ((st = launch_part(m, b, kAttnPart, sms, ctas, workspace, few_space, false, cs)) != BFP8_OK) return st;
+  if (!apart) {
+    if ((st = launch_part(m, a, kAttnOwn, sms, sms, workspace, few_space, false, cs)) != BFP8_OK) return st;
+    return set_last_error(BFP8_OK, "");
+  }
+  AttnArgs own = a;
+  own.part_o = a.part_o + row_floats;
+  own.part_lse2 = a.part_lse2 + a.total_q * a.heads;
+  if ((st = launch_part(m, own, kAttnPart, sms, beside ? sms - ctas : sms, workspace, few_space, beside, cs)) != BFP8_OK) return st;
+  const cudaError_t e = launch_join(JoinArgs{a, own.part_o, own.part_lse2}, cs);
+  if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
   return set_last_error(BFP8_OK, "");
 }

@@ -40,9 +40,9 @@ struct AttnArgs {
   int32_t prefixes;
 };
 
-// What a launch computes: attention as it stands; the part over shared prefixes, which goes to part_o and part_lse2; or
-// the part over the sequences' own tokens, joined with that one.
-enum AttnMode : int { kAttnWhole = 0, kAttnPrefix = 1, kAttnOwn = 2 };
+// What a launch computes: attention as it stands; one part, which goes to part_o and part_lse2; or the part over the
+// sequences' own tokens, joined with the prefixes' that stands there.
+enum AttnMode : int { kAttnWhole = 0, kAttnPart = 1, kAttnOwn = 2 };
 
 // Where the prefix's part of a row stands.
 __device__ __forceinline__ int64_t part_row(const AttnArgs& a, int64_t token, int head) { return token * a.heads + head; }
@@ -119,12 +119,11 @@ bfp8_status check_attention(const bfp8_attention_args* p, AttnArgs* a, bool* emp
 // The kernel for few rows a sequence (bfp8_attn_decode.cu): `groups` (1 to 4)
 // eights of rows, `ctas` persistent CTAs, counters[ctas] zero.
 // k, v: tensor maps [dim, token, head, page] of bytes, boxes of min(page_size, 128) tokens.
-// behind 1: the launch before it in the stream is launch_attn_tile's of the same part; the two run beside each other.
-// behind 2 (kAttnOwn): it is launch_attn_tile's of the prefixes' part, needed only once rows are joined.
+// behind: the launch before it in the stream is launch_attn_tile's of the same call; the two run beside each other.
 int attn_decode_groups(int64_t rows);
 size_t attn_decode_partial_bytes(int groups, int dim, int ctas);
 cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, AttnMode mode, int groups, int ctas,
-                               int32_t* counters, float* partials, int behind, cudaStream_t stream);
+                               int32_t* counters, float* partials, bool behind, cudaStream_t stream);
 
 // The kernel for more rows (bfp8_attn_tile.cu); counters[2 * ctas] zero.
 size_t attn_tile_partial_bytes(int dim, int ctas);

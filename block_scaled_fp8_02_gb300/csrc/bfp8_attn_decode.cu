@@ -179,7 +179,7 @@ struct DecodeArgs {
   int32_t* counters;          // one a CTA, zero between calls
   float* partials;            // two slots a CTA: NG * 8 rows of D floats, then their log2 sums
   unsigned long long wait_limit;
-  int32_t behind;             // launched right behind the other kernel: 1 of the same part, 2 of the prefixes'
+  int32_t behind;             // launched right behind the other kernel, for the same call
 };
 
 template <int D, int NG, int RT, int MODE>
@@ -692,15 +692,12 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
     more = next(nx);
     if (more) fetch(nx);
 
-    // rows are joined from here on
-    if constexpr (MODE == kAttnOwn)
-      if (p.behind == 2) griddep_wait();
     // row r of the item as lane's elements of it, and its log2 sum
     auto finish = [&](int r, float (&o)[D / 32], float lse2) {
       const int i = r / a.group, head = c.h * a.group + r - i * a.group;
       const int64_t token = w.row0 + i;
       using Vec = typename std::conditional<D == 128, float4, float2>::type;
-      if constexpr (MODE == kAttnPrefix) {
+      if constexpr (MODE == kAttnPart) {
         Vec x;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) reinterpret_cast<float*>(&x)[e] = o[e];
@@ -902,7 +899,7 @@ size_t attn_decode_partial_bytes(int groups, int dim, int ctas) {
 }
 
 cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, AttnMode mode, int groups, int ctas,
-                               int32_t* counters, float* partials, int behind, cudaStream_t stream) {
+                               int32_t* counters, float* partials, bool behind, cudaStream_t stream) {
   DecodeArgs p;
   p.a = a;
   p.counters = counters;
@@ -910,7 +907,7 @@ cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const
   p.wait_limit = 1ull << 31;
   p.behind = behind;
   switch (mode) {
-    case kAttnPrefix: return launch_decode_mode<kAttnPrefix>(k, v, p, groups, ctas, stream);
+    case kAttnPart: return launch_decode_mode<kAttnPart>(k, v, p, groups, ctas, stream);
     case kAttnOwn: return launch_decode_mode<kAttnOwn>(k, v, p, groups, ctas, stream);
     default: return launch_decode_mode<kAttnWhole>(k, v, p, groups, ctas, stream);
   }

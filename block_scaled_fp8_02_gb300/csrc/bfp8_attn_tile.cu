@@ -1146,7 +1146,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       // columns 32 g .. of the row, from its fp32 ones
       auto store32 = [&](int g, const float* x) {
-        if constexpr (MODE == kAttnPrefix) {
+        if constexpr (MODE == kAttnPart) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(part_dst + 32 * g + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
@@ -1173,7 +1173,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       };
       auto store_lse = [&](float v) {
-        if constexpr (MODE == kAttnPrefix) a.part_lse2[prow] = v;
+        if constexpr (MODE == kAttnPart) a.part_lse2[prow] = v;
         else if (a.lse != nullptr) a.lse[(c.w.row0 + i) * a.heads + head] = v * 0.6931471805599453f;
       };
 #pragma unroll 1
@@ -1314,7 +1314,7 @@ cudaError_t launch_attn_tile(const CUtensorMap& k, const CUtensorMap& v, const A
                           : launch_tile<64, decltype(m)::value>(k, v, p, ctas, stream);
   };
   switch (mode) {
-    case kAttnPrefix: return go(std::integral_constant<int, kAttnPrefix>{});
+    case kAttnPart: return go(std::integral_constant<int, kAttnPart>{});
     case kAttnOwn: return go(std::integral_constant<int, kAttnOwn>{});
     default: return go(std::integral_constant<int, kAttnWhole>{});
   }

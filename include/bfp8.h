@@ -604,7 +604,8 @@ bfp8_status bfp8_paged_attention_workspace_size(int num_heads, int num_kv_heads,
  *            lens [prefixes] are device int32; max_q_len bounds the rows of one
  *            prefix (cu_q[f+1] - cu_q[f]), max_len the lens.  prefixes == 0: bfp8_paged_attention.
  *   workspace  as for bfp8_paged_attention, bfp8_shared_prefix_attention_workspace_size
- *            bytes: its part over the prefix is held there in fp32 for every row.
+ *            bytes: the part over the prefix (and in some calls that over the own tokens) is held
+ *            there in fp32 for every row.
  * The output is rounded once.  Page numbers and lengths as for bfp8_paged_attention; rows of
  * a prefix past its bound max_q_len have unspecified outputs.  Results are deterministic.
  */
