@@ -108,11 +108,15 @@ __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_gro
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Where a warp is in the line.
+// Where a warp is in the line: an item, and what does not change within it.
 struct Cursor {
   int b, h;
   int64_t item0;          // line position of the item's first unit
   int32_t units, t0, kv_len, pos0;
+  int32_t k, end;         // the warp's next unit of it; those of it in the share
+  const uint8_t* keys;    // of this lane, in page 0
+  const float* scales;
+  const float* sums;
 };
 // A unit: its first token and its page; b < 0: none.
 struct Unit {
@@ -175,7 +179,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
   }
   __syncthreads();
 
+  // the token whose sum this lane writes: g, or g + 8 (lanes t = 0 and 1)
+  const int out = g + 8 * t;
   Cursor c;
+  auto enter_head = [&]() {
+    c.end = static_cast<int32_t>(c.item0 + c.units < u1 ? c.units : u1 - c.item0);
+    c.keys = a.c.k + c.h * a.c.st_head + g * a.c.st_tok + 16 * t;
+    c.scales = a.c.ks + c.h * a.c.ss_head + g;
+    c.sums = p.w + c.h * p.ws_head + out;
+  };
   auto enter = [&](int b) {
     const SeqWork w = seq_work(p, b, kRows);
     c.b = b;
@@ -187,44 +199,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
   enter(s_b);
   c.h = static_cast<int>((u0 - s_before) / line_cost(c.units));
   c.item0 = s_before + static_cast<int64_t>(c.h) * line_cost(c.units);
-  int64_t u = u0 + warp;
-  // the warp's next unit, its page's number asked for; bounds: of its tokens
-  int32_t t0 = 0, kv_len = 0, pos0 = 0;
+  c.k = static_cast<int32_t>(u0 - c.item0) + warp;
+  enter_head();
+  // the warp's next unit, its page's number asked for
   auto locate = [&]() {
     Unit n;
     n.b = -1;
     n.h = n.tok = n.page = 0;
-    while (u < u1) {
+    while (c.k >= c.end) {
       const int32_t cost = line_cost(c.units);
-      if (u >= c.item0 + cost) {
-        c.item0 += cost;
-        if (++c.h == H) {
-          c.h = 0;
-          do {
-            enter(c.b + 1);
-          } while (c.units == 0);
-        }
-        continue;
+      if (c.item0 + cost >= u1) return n;
+      while (c.k < cost) c.k += kWarps;                              // the places behind the item
+      c.k -= cost;
+      c.item0 += cost;
+      if (++c.h == H) {
+        c.h = 0;
+        do {
+          enter(c.b + 1);
+        } while (c.units == 0);
       }
-      const int32_t k = static_cast<int32_t>(u - c.item0);
-      u += kWarps;
-      if (k >= c.units) continue;                                    // the places behind an item
-      n.b = c.b;
-      n.h = c.h;
-      n.tok = (c.t0 / kUnit + k) * kUnit;
-      n.page = __ldg(a.table + c.b * a.ld_table + (n.tok >> a.c.page_shift));
-      t0 = c.t0;
-      kv_len = c.kv_len;
-      pos0 = c.pos0;
-      break;
+      enter_head();
     }
+    n.b = c.b;
+    n.h = c.h;
+    n.tok = (c.t0 / kUnit + c.k) * kUnit;
+    n.page = __ldg(a.table + c.b * a.ld_table + (n.tok >> a.c.page_shift));
+    c.k += kWarps;
     return n;
   };
   uint8_t* const ring = few_smem + warp * (C::kStages * C::kStage);
   const uint32_t ring_at = smem_addr(ring);
-  // the token whose sum this lane writes: g, or g + 8 (lanes t = 0 and 1)
-  const int out = g + 8 * t;
-  // starts the copies of a unit located last: keys, their scales, the sum to be added to
+  // starts the copies of the unit located last: keys, their scales, the sum to be added to
   auto fetch = [&](Unit& n, int slot) {
     if (n.b >= 0) {
       if (n.page < 0 || n.page >= a.c.num_pages) {
@@ -234,20 +239,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
       const bool there = n.page >= 0;
       const int64_t page = there ? n.page : 0;
       const int off = n.tok & (a.c.page_size - 1);
-      const uint8_t* keys = a.c.k + page * a.c.st_page + n.h * a.c.st_head + (off + g) * a.c.st_tok + 16 * t;
-      const float* scales = a.c.ks + page * a.c.ss_page + n.h * a.c.ss_head + off + g;
+      const uint8_t* keys = c.keys + page * a.c.st_page + off * a.c.st_tok;
+      const float* scales = c.scales + page * a.c.ss_page + off;
       const uint32_t at = ring_at + slot * C::kStage;
+      // (a whole unit, which most are, needs none of the comparisons)
+      const bool all = there && n.tok + kUnit <= c.kv_len;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const bool live = there && n.tok + 8 * r + g < kv_len;
+        const bool live = all || (there && n.tok + 8 * r + g < c.kv_len);
 #pragma unroll
         for (int h = 0; h < KC; ++h) copy16(at + ((r * KC + h) * 32 + lane) * 16, keys + 8 * r * a.c.st_tok + 64 * h, live);
         copy4(at + C::kOffKs + (r * 32 + lane) * 4, scales + 8 * r, live);
       }
       const int32_t j = n.tok + out;
       if (t < 2)
-        copy4(at + C::kOffOld + lane * 4, p.w + page * p.ws_page + n.h * p.ws_head + off + out,
-              there && j < kv_len && !begins_here(p, j, pos0));
+        copy4(at + C::kOffOld + lane * 4, c.sums + page * p.ws_page + off, there && j < c.kv_len && !begins_here(p, j, c.pos0));
     }
     if (lane == 0) units[warp][slot] = n;
     copies_end();
@@ -259,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
   int32_t lo[NG][2], hi[NG][2];            // tokens that they see
   int q_b = -1, q_h = -1;
   int32_t q_t0 = 0, q_end = 0;             // the tokens of the sequence whose sums are written
+  int32_t all_lo = 0, all_hi = 0;          // those that all kRows rows see
   auto queries = [&](const Unit& n) {
     q_b = n.b;
     q_h = n.h;
@@ -266,6 +273,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
     q_t0 = w.t0;
     q_end = w.kv_len;
     const int rows = w.q_len * a.group;
+    {
+      int32_t x;
+      seen_range(a, w.kv_len, w.pos0 + w.q_len - 1, all_lo, x);
+      seen_range(a, w.kv_len, w.pos0, x, all_hi);
+      if (rows < kRows) all_hi = 0;
+    }
 #pragma unroll
     for (int grp = 0; grp < NG; ++grp) {
       const int r = grp * 8 + g, i = r / a.group;
@@ -347,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
       }
     }
     float sum[2] = {0.f, 0.f};
+    const bool all = n.tok >= all_lo && n.tok + kUnit <= all_hi;
 #pragma unroll
     for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
@@ -354,10 +368,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
         const int r = i >> 1, x = i & 1;
         float v = s[grp][0][i];
         if constexpr (KC == 2) v += s[grp][1][i];
-        const int32_t j = n.tok + 8 * r + g;
-        v = ex2(fmaf(v, ks[r] * cq[grp][x], bias[grp][x]));
-        if (j >= lo[grp][x] && j < hi[grp][x]) sum[r] += v;
+        s[grp][0][i] = ex2(fmaf(v, ks[r] * cq[grp][x], bias[grp][x]));
       }
+    if (!all) {
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t j = n.tok + 8 * (i >> 1) + g;
+          if (j < lo[grp][i & 1] || j >= hi[grp][i & 1]) s[grp][0][i] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i >> 1] += s[grp][0][i];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
