@@ -48,21 +48,17 @@ size_t workspace_bytes_for(int group, int dim, int max_q, int sms) {
          (has_many(group, max_q) ? attn_tile_partial_bytes(dim, sms) : 0);
 }
 
-// A call over shared prefixes: its parts may run beside each other, so the partial rows of the kernel for few rows (of either)
-// and those of the other have places of their own.
-size_t shared_few_bytes(int group, int dim, int max_prefix_q, int max_q, int sms) {
-  const size_t a = few_bytes(group, dim, max_prefix_q, sms), b = few_bytes(group, dim, max_q, sms);
-  return a > b ? a : b;
-}
+// Are both parts of a call over shared prefixes computed apart, beside each other, and joined in a launch of their own?  Where the
+// prefixes' takes the tile kernel and the own one the kernel for few rows: many sequences' single tokens.  64 of them, own contexts up
+// to 1000 behind a prefix of 8192, 64 / 8 heads of 128: 98 us with the own part's rows waiting for the prefix's, 76 apart.  (With more
+// new tokens the parts' fp32 rows would take longer to write and read than the wait; with fewer the third launch would.)
+bool parts_apart(int group, int max_prefix_q, int max_q) { return has_many(group, max_prefix_q) && !has_many(group, max_q); }
+// Scratch of such a call: each part's partial rows of the kernel for few rows, and those of the other, which only one takes at a time.
 size_t shared_scratch_bytes(int group, int dim, int max_prefix_q, int max_q, int sms) {
   const bool tile = has_many(group, max_prefix_q) || has_many(group, max_q);
-  return kCounterHeaderBytes + shared_few_bytes(group, dim, max_prefix_q, max_q, sms) + (tile ? attn_tile_partial_bytes(dim, sms) : 0);
+  return kCounterHeaderBytes + few_bytes(group, dim, max_prefix_q, sms) + few_bytes(group, dim, max_q, sms) +
+         (tile ? attn_tile_partial_bytes(dim, sms) : 0);
 }
-// Are both parts computed apart, beside each other, and joined in a launch of their own?  Where the prefixes' takes the tile kernel and
-// the own one the kernel for few rows: many sequences' single tokens.  64 of them, own contexts up to 1000 behind a prefix of
-// 8192, 64 / 8 heads of 128: 98 us with the own part's rows waiting for the prefix's.  (With more new tokens the parts' fp32 rows
-// would take longer to write and read than the wait.)
-bool parts_apart(int group, int max_prefix_q, int max_q) { return has_many(group, max_prefix_q) && !has_many(group, max_q); }
 // Behind all that: a part's rows in fp32 and their log2 sums, for each part that is not joined at once.
 size_t shared_rows_bytes(int64_t total_q, int heads, int dim, bool apart) {
   return static_cast<size_t>(total_q) * heads * (dim + 1) * sizeof(float) * (apart ? 2 : 1);
@@ -119,15 +115,17 @@ bool few_launched(const AttnArgs& a) {
                                  a.total_q <= static_cast<int64_t>(a.batch - 1) * a.max_q + 8 * few_groups(a.group, a.max_q) / a.group);
 }
 
-// SMs that the tile kernel gets for the prefixes' part `b` where the kernel for few rows takes the own part `a` beside it: by the
-// cycles that each needs at its bounds (own contexts at three quarters of theirs), a block's and an item's own among them.  64 sequences,
-// own contexts up to 1000 behind 8192 tokens, 64 / 8 heads of 128, by the tile kernel's SMs: 48 81 us, 64 69, 80 71, 96 78, 112 104; 79
+// SMs that the prefixes' part `b` gets where the own part `a` (by the kernel for few rows) runs beside it: by the cycles that each needs
+// at its bounds (contexts of the kernel for few rows at three quarters of theirs), a block's and an item's own among them.  64 sequences, own
+// contexts up to 1000 behind 8192 tokens, 64 / 8 heads of 128, by the tile kernel's SMs: 48 81 us, 64 69, 80 71, 96 78, 112 104; 79
 // with the kernel for few rows behind the other, on the SMs that it leaves.
-int tile_sms(const AttnArgs& a, const AttnArgs& b, int sms) {
+int prefix_sms(const AttnArgs& a, const AttnArgs& b, int sms) {
+  auto few = [](const AttnArgs& x) {
+    return static_cast<double>(x.batch) * x.c.heads * (0.75 * static_cast<double>(x.max_kv) / 128 + 4) * 1340;
+  };
   const double blocks = static_cast<double>(b.batch) * b.c.heads * ((static_cast<int64_t>(b.max_q) * b.group + 255) / 256);
-  const double tile = blocks * (static_cast<double>(b.max_kv) / 128 + 8) * 4500;
-  const double few = static_cast<double>(a.batch) * a.c.heads * (0.75 * static_cast<double>(a.max_kv) / 128 + 4) * 1340;
-  const int n = static_cast<int>(sms * (tile / (tile + few)));
+  const double prefix = has_many(b.group, b.max_q) ? blocks * (static_cast<double>(b.max_kv) / 128 + 8) * 4500 : few(b);
+  const int n = static_cast<int>(sms * (prefix / (prefix + few(a))));
   return n < sms / 4 ? sms / 4 : n > sms * 3 / 4 ? sms * 3 / 4 : n;
 }
 
@@ -176,24 +174,25 @@ cudaError_t launch_join(const JoinArgs& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, p.a.c.dim == 128 ? join_parts_kernel<128> : join_parts_kernel<64>, p);
 }
 
-// Launches what one part (or all) takes: the kernel for many rows, that for few, or both.  few_space: bytes of the partial rows
-// of the kernel for few rows, before the other's; ctas: SMs that it takes.  beside: the launch before is the tile kernel's, of
-// another part, and this one takes the kernel for few rows alone, which needs nothing of it.
-bfp8_status launch_part(const CacheMaps& m, AttnArgs a, AttnMode mode, int sms, int ctas, void* workspace, size_t few_space,
-                        bool beside, cudaStream_t cs) {
+// What the kernels of one part (or all) have to themselves: counters (zero) and partial rows.
+struct Scratch {
+  int32_t* few_counters;
+  float* few;
+  int32_t* tile_counters;
+  float* tile;
+};
+
+// Launches what one part (or all) takes: the kernel for many rows, that for few, or both, on `ctas` SMs.  beside: the launch before is
+// of another part, and this one takes the kernel for few rows alone, which needs nothing of it (kAttnOwn: before it joins rows).
+bfp8_status launch_part(const CacheMaps& m, AttnArgs a, AttnMode mode, int ctas, const Scratch& w, bool beside, cudaStream_t cs) {
   const int groups = few_groups(a.group, a.max_q);
   a.few_rows = groups * 8;
-  int32_t* counters = static_cast<int32_t*>(workspace);
-  char* partials = static_cast<char*>(workspace) + kCounterHeaderBytes;
-  cudaError_t e = cudaSuccess;
   const bool many = has_many(a.group, a.max_q), few = few_launched(a);
   if (!few) a.few_rows = 0;
-  if (many)
-    e = launch_attn_tile(m.k, m.v, a, mode, ctas, counters + sms,
-                         reinterpret_cast<float*>(partials + few_space), cs);
+  cudaError_t e = cudaSuccess;
+  if (many) e = launch_attn_tile(m.k, m.v, a, mode, ctas, w.tile_counters, w.tile, cs);
   if (e == cudaSuccess && few)
-    e = launch_attn_decode(m.k, m.v, a, mode, groups, ctas, counters, reinterpret_cast<float*>(partials),
-                           many || beside, cs);
+    e = launch_attn_decode(m.k, m.v, a, mode, groups, ctas, w.few_counters, w.few, many ? 1 : beside ? 2 : 0, cs);
   if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
   return BFP8_OK;
 }
@@ -295,9 +294,11 @@ extern "C" bfp8_status bfp8_paged_attention(const bfp8_attention_args* p, const 
   if (st != BFP8_OK) return st;
   CacheMaps m;
   if ((st = encode_maps(a.c, &m)) != BFP8_OK) return st;
-  if ((st = launch_part(m, a, kAttnWhole, sms, sms, workspace, few_bytes(a.group, a.c.dim, a.max_q, sms), false,
-                        static_cast<cudaStream_t>(stream))) != BFP8_OK)
-    return st;
+  int32_t* counters = static_cast<int32_t*>(workspace);
+  char* partials = static_cast<char*>(workspace) + kCounterHeaderBytes;
+  const Scratch w{counters, reinterpret_cast<float*>(partials), counters + sms,
+                  reinterpret_cast<float*>(partials + few_bytes(a.group, a.c.dim, a.max_q, sms))};
+  if ((st = launch_part(m, a, kAttnWhole, sms, w, false, static_cast<cudaStream_t>(stream))) != BFP8_OK) return st;
   return set_last_error(BFP8_OK, "");
 }
 
@@ -346,11 +347,17 @@ extern "C" bfp8_status bfp8_shared_prefix_attention(const bfp8_attention_args* p
                        [&](int n) { return shared_scratch_bytes(a.group, a.c.dim, pq, a.max_q, n) + rows; });
   if (st != BFP8_OK) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const size_t few_space = shared_few_bytes(a.group, a.c.dim, pq, a.max_q, sms);
+  // counters: one a CTA of either kernel for few rows, two of the other (4 * sms fit the header)
+  int32_t* counters = static_cast<int32_t*>(workspace);
+  char* partials = static_cast<char*>(workspace) + kCounterHeaderBytes;
+  const size_t few_prefix = few_bytes(a.group, a.c.dim, pq, sms), few_own = few_bytes(a.group, a.c.dim, a.max_q, sms);
+  float* const tile = reinterpret_cast<float*>(partials + few_prefix + few_own);
+  const Scratch w_prefix{counters, reinterpret_cast<float*>(partials), counters + sms, tile},
+      w_own{counters + 3 * sms, reinterpret_cast<float*>(partials + few_prefix), counters + sms, tile};
   CacheMaps m;
   if ((st = encode_maps(a.c, &m)) != BFP8_OK) return st;
   if (none) {
-    if ((st = launch_part(m, a, kAttnWhole, sms, sms, workspace, few_space, false, cs)) != BFP8_OK) return st;
+    if ((st = launch_part(m, a, kAttnWhole, sms, w_own, false, cs)) != BFP8_OK) return st;
     return set_last_error(BFP8_OK, "");
   }
   // rows of one part or both (whole rows: read and written in vectors), then their sums
@@ -369,18 +376,19 @@ extern "C" bfp8_status bfp8_shared_prefix_attention(const bfp8_attention_args* p
   b.max_q = f->max_q_len;
   b.causal = 0;
   b.window = 0;
-  // (beside only the tile kernel: one for few rows before it has the same partial rows and counters)
-  const bool beside = apart && !few_launched(b);
-  const int ctas = beside ? tile_sms(a, b, sms) : sms;
-  if ((st = launch_part(m, b, kAttnPart, sms, ctas, workspace, few_space, false, cs)) != BFP8_OK) return st;
-  if (!apart) {
-    if ((st = launch_part(m, a, kAttnOwn, sms, sms, workspace, few_space, false, cs)) != BFP8_OK) return st;
+  // The own part runs beside the prefixes' where each is one launch, that of the own part for few rows: apart, or joining its rows itself
+  // where the prefixes' are few too (4 sequences, up to 40 own tokens behind 500: 28.9 us one behind the other, 25.7 so).
+  const bool beside = !has_many(a.group, a.max_q) && !(has_many(b.group, b.max_q) && few_launched(b));
+  const int ctas = beside ? prefix_sms(a, b, sms) : sms;
+  if ((st = launch_part(m, b, kAttnPart, ctas, w_prefix, false, cs)) != BFP8_OK) return st;
+  if (!(beside && apart)) {
+    if ((st = launch_part(m, a, kAttnOwn, beside ? sms - ctas : sms, w_own, beside, cs)) != BFP8_OK) return st;
     return set_last_error(BFP8_OK, "");
   }
   AttnArgs own = a;
   own.part_o = a.part_o + row_floats;
   own.part_lse2 = a.part_lse2 + a.total_q * a.heads;
-  if ((st = launch_part(m, own, kAttnPart, sms, beside ? sms - ctas : sms, workspace, few_space, beside, cs)) != BFP8_OK) return st;
+  if ((st = launch_part(m, own, kAttnPart, sms - ctas, w_own, true, cs)) != BFP8_OK) return st;
   const cudaError_t e = launch_join(JoinArgs{a, own.part_o, own.part_lse2}, cs);
   if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
   return set_last_error(BFP8_OK, "");

@@ -179,7 +179,7 @@ struct DecodeArgs {
   int32_t* counters;          // one a CTA, zero between calls
   float* partials;            // two slots a CTA: NG * 8 rows of D floats, then their log2 sums
   unsigned long long wait_limit;
-  int32_t behind;             // launched right behind the other kernel, for the same call
+  int32_t behind;             // launched right behind the launch that it runs beside: 1 of the same part, 2 of the other
 };
 
 template <int D, int NG, int RT, int MODE>
@@ -208,10 +208,12 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
     }
     fence_barrier_init();
   }
-  griddep_launch_dependents();
   // Behind the other kernel this one starts once all of its CTAs have passed their wait, on what SMs it leaves,
-  // needs nothing of it and only must not be done before it.
-  if (!p.behind) griddep_wait();
+  // needs nothing of it and only must not be done before it.  (One part may have the other's launch behind it: that needs this
+  // wait to be over.)
+  if (MODE == kAttnPart && !p.behind) griddep_wait();
+  griddep_launch_dependents();
+  if (MODE != kAttnPart && !p.behind) griddep_wait();
 
   // ---- this CTA's share [u0, u1) of the line of units, and where it starts
   __shared__ int64_t part[C::kThreads / 32];
@@ -692,6 +694,8 @@ __global__ void __launch_bounds__((DecCfg<D, NG, RT>::kThreads), 1)
     more = next(nx);
     if (more) fetch(nx);
 
+    if constexpr (MODE == kAttnOwn)
+      if (p.behind == 2) griddep_wait();                     // rows are joined from here on
     // row r of the item as lane's elements of it, and its log2 sum
     auto finish = [&](int r, float (&o)[D / 32], float lse2) {
       const int i = r / a.group, head = c.h * a.group + r - i * a.group;
@@ -899,7 +903,7 @@ size_t attn_decode_partial_bytes(int groups, int dim, int ctas) {
 }
 
 cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, AttnMode mode, int groups, int ctas,
-                               int32_t* counters, float* partials, bool behind, cudaStream_t stream) {
+                               int32_t* counters, float* partials, int behind, cudaStream_t stream) {
   DecodeArgs p;
   p.a = a;
   p.counters = counters;
