@@ -89,8 +89,9 @@ def test_head_layouts(dev, Hq, H, D, page, q_lens, kv_lens):
 @pytest.mark.parametrize("window", [1, 5, 64, 100, 1000])
 @pytest.mark.parametrize("q_lens,kv_lens", [([1, 2], [300, 77]), ([50, 130], [50, 400])])
 @pytest.mark.parametrize("accumulate", [True, False])
-def test_windows(dev, window, q_lens, kv_lens, accumulate):
-    check(dev, make(q_lens, kv_lens, window=window), accumulate)
+@pytest.mark.parametrize("causal", [True, False])
+def test_windows(dev, window, q_lens, kv_lens, accumulate, causal):
+    check(dev, make(q_lens, kv_lens, window=window, causal=causal), accumulate)
 
 
 @pytest.mark.parametrize("accumulate", [True, False])
