@@ -28,9 +28,9 @@ namespace {
 
 constexpr int kBins = 2048;
 // Threads of a CTA that looks for the kept positions, and keys that each holds (a longer stretch is read anew each time).
-// Many (sequence, head)s: small CTAs, four a SM (64 x 8 heads of 8000 tokens 28 us, 41 with clusters of two).  Few long ones: large
-// ones, in clusters (the measured cost of a cluster's barriers is about a microsecond each, so no more CTAs than the
-// keys need).
+// Many (sequence, head)s: small CTAs, four a SM (64 x 8 heads of 8000 tokens 28 us, 36 in clusters of two).  Few: large
+// ones (16 x 8 heads 11 us, 19 with small ones), in clusters where their keys are too many for one (a cluster's barriers cost about
+// a microsecond each, so no more CTAs than the keys need).
 template <int T>
 struct Find {
   static constexpr int kWarps = T / 32, kHold = T == 256 ? 32 : 16, kChunk = kHold * T, kCtasPerSm = T == 256 ? 4 : 1;
@@ -281,12 +281,16 @@ __global__ void __launch_bounds__(kThreads, Find<kThreads>::kCtasPerSm) evict_se
   if (n > a.budget) find_kept<kThreads>(a, C, rank, h, n, a.table + b * a.ld_table, a.kept + item * a.cap);
 }
 
-template <int D, bool kInPlace>
+// S blocks (blockIdx.z) take a share of every row's pieces each, and S times the ranks at a time: in place, where only a cluster's
+// CTAs work on a (sequence, head) and each round waits for all of them, few items leave most SMs idle and take many rounds.
+template <int D, bool kInPlace, int S>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
   constexpr int kPieces = D / 16;                           // 16-byte pieces of a row's keys, and of its values
-  constexpr int kStep = kMoveThreads / (2 * kPieces);       // rows that the block holds a piece a thread of
-  constexpr int kUnroll = kMoveTokens / kStep;
-  __shared__ int64_t s_src[kMoveTokens][3], s_dst[kMoveTokens][3];    // offsets of codes, scales and sums; -1: none
+  constexpr int kMine = 2 * kPieces / S, kTokens = kMoveTokens * S;
+  constexpr int kStep = kMoveThreads / kMine;               // rows that the block holds a piece a thread of
+  constexpr int kUnroll = kTokens / kStep;
+  static_assert(S == 1 ? kMoveThreads >= 3 * kTokens : kMoveThreads == kTokens && S >= 3, "a thread a scale or sum");
+  __shared__ int64_t s_src[kTokens][3], s_dst[kTokens][3];    // offsets of codes, scales and sums; -1: none
   const int item = static_cast<int>(blockIdx.y), b = item / a.c.heads, h = item - b * a.c.heads;
   const int tid = threadIdx.x;
   griddep_launch_dependents();
@@ -296,14 +300,14 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   if (kInPlace && whole) return;                            // (all of a cluster)
   const int32_t m = whole ? n : a.budget;
   const int32_t* kept = a.kept + item * a.cap;
-  const int32_t step = static_cast<int32_t>(gridDim.x) * kMoveTokens;
-  const int piece = tid % (2 * kPieces), r0 = tid / (2 * kPieces);
+  const int32_t step = static_cast<int32_t>(gridDim.x) * kTokens;
+  const int piece = static_cast<int>(blockIdx.z) * kMine + tid % kMine, r0 = tid / kMine;
   uint8_t* const codes = (piece < kPieces ? a.c.k : a.c.v) + (piece % kPieces) * 16;
   // in place every CTA of the cluster takes part in each round's barrier
   for (int32_t i0 = 0; i0 < m; i0 += step) {
-    const int32_t base = i0 + static_cast<int32_t>(blockIdx.x) * kMoveTokens;
+    const int32_t base = i0 + static_cast<int32_t>(blockIdx.x) * kTokens;
     if (!kInPlace && base >= m) break;
-    if (tid < kMoveTokens) {
+    if (tid < kTokens) {
       const int32_t i = base + tid;
       s_src[tid][0] = s_dst[tid][0] = -1;
       if (i < m) {
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
       if (at >= 0) x[u] = *reinterpret_cast<const uint4*>(codes + at);
     }
     float f = 0.f;
-    const int what = tid / kMoveTokens, ri = tid % kMoveTokens;       // key scales, value scales, sums
+    const int what = S == 1 ? tid / kTokens : static_cast<int>(blockIdx.z), ri = tid % kTokens;      // key scales, value scales, sums
     const bool scalar = what < 3 && s_src[ri][0] >= 0;
     if (scalar) f = what == 0 ? a.c.ks[s_src[ri][1]] : what == 1 ? a.c.vs[s_src[ri][1]] : a.w[s_src[ri][2]];
     if (kInPlace) cluster_sync();
@@ -353,11 +357,11 @@ bfp8_status bad(const char* fmt, V... v) {
   return set_last_errorf(BFP8_ERR_INVALID_ARG, fmt, v...);
 }
 
-// x blocks for each (sequence, head), as a cluster or not.
+// x (and z times) blocks for each (sequence, head), the x as a cluster or not.
 template <typename F>
-cudaError_t launch(F* f, int x, int items, bool cluster, int threads, const EvictArgs& a, cudaStream_t stream) {
+cudaError_t launch(F* f, int x, int items, int z, bool cluster, int threads, const EvictArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(x, items);
+  cfg.gridDim = dim3(x, items, z);
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -445,20 +449,30 @@ extern "C" bfp8_status bfp8_kv_cache_evict(const bfp8_evict_args* p, const bfp8_
   a.first = static_cast<int32_t>(p->first < a.budget ? p->first : a.budget);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int items = p->batch * a.c.heads;
-  // (8 heads of a sequence of 60000 tokens: see Find)
+  // Small CTAs where there are more (sequence, head)s than SMs, or few keys; else large ones, in clusters where the keys are more
+  // than one holds and SMs are left (see Find).
   cudaError_t e;
-  if (items * 4 > sms || p->max_kv_len <= 4 * Find<256>::kChunk / 8) {
-    e = launch(evict_select_kernel<256>, 1, items, false, 256, a, cs);
+  if (items > sms || p->max_kv_len <= 2048) {
+    e = launch(evict_select_kernel<256>, 1, items, 1, false, 256, a, cs);
   } else {
     int cluster = 1;
-    while (cluster < kMaxCluster && p->max_kv_len > static_cast<int64_t>(cluster) * Find<1024>::kChunk) cluster *= 2;
-    e = launch(evict_select_kernel<1024>, cluster, items, true, 1024, a, cs);
+    while (cluster < kMaxCluster && 2 * items * cluster <= sms && p->max_kv_len > static_cast<int64_t>(cluster) * Find<1024>::kChunk)
+      cluster *= 2;
+    e = launch(evict_select_kernel<1024>, cluster, items, 1, true, 1024, a, cs);
   }
   if (e == cudaSuccess && most > 0 && (!in_place || a.cap > 0)) {
-    auto f = a.c.dim == 128 ? (in_place ? evict_move_kernel<128, true> : evict_move_kernel<128, false>)
-                            : (in_place ? evict_move_kernel<64, true> : evict_move_kernel<64, false>);
-    const int64_t blocks = (most + kMoveTokens - 1) / kMoveTokens;
-    e = launch(f, in_place ? kMoveCluster : static_cast<int>(blocks), items, in_place, kMoveThreads, a, cs);
+    const int blocks = static_cast<int>((most + kMoveTokens - 1) / kMoveTokens);
+    // (8 heads of 60000 tokens to 8192 in place, with the search: 53 us with one share, 32 with four; 512 items of up to 8000 to 2048: 103
+    // and 136)
+    const bool few = items * kMoveCluster < 2 * sms;
+    if (!in_place) {
+      auto f = a.c.dim == 128 ? evict_move_kernel<128, false, 1> : evict_move_kernel<64, false, 1>;
+      e = launch(f, blocks, items, 1, false, kMoveThreads, a, cs);
+    } else {
+      auto f = a.c.dim == 128 ? (few ? evict_move_kernel<128, true, 4> : evict_move_kernel<128, true, 1>)
+                              : (few ? evict_move_kernel<64, true, 4> : evict_move_kernel<64, true, 1>);
+      e = launch(f, kMoveCluster, items, few ? 4 : 1, true, kMoveThreads, a, cs);
+    }
   }
   if (e != cudaSuccess) return set_last_errorf(BFP8_ERR_CUDA, "cache evict launch: %s", cudaGetErrorString(e));
   return set_last_error(BFP8_OK, "");
