@@ -167,3 +167,52 @@ def test_a_decoding_step_in_one_graph(dev):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(eager[i], (*lse_out, lens, x.weights))), i
     assert bf.bfp8_device_status() == 0
+
+
+def test_calls_of_every_kind_in_turn_on_one_workspace(dev):
+    """Nothing waits between them: each finds the counters at zero and leaves the others' partial rows alone."""
+    g = torch.Generator().manual_seed(7)
+    pages = 400
+    codes = [torch.randint(0, 120, (pages, H, PAGE, D), generator=g, dtype=torch.uint8).to(dev) for _ in range(2)]
+    scales = [(torch.rand(pages, H, PAGE, generator=g) * 0.01 + 1e-3).to(dev) for _ in range(2)]
+    w0 = torch.rand(pages, H, PAGE, generator=g).to(dev)
+
+    def ints(v):
+        return torch.tensor(v, dtype=torch.int32, device=dev)
+
+    def case(plens, pcu, q_lens, kv_lens):
+        order = torch.randperm(pages, generator=g).int().to(dev)
+        width = (max(kv_lens) + PAGE - 1) // PAGE
+        ahead = (max(plens) + PAGE - 1) // PAGE
+        cu = [0]
+        for m in q_lens:
+            cu.append(cu[-1] + m)
+        q = torch.randn(cu[-1], HQ, D, generator=g).bfloat16().to(dev)
+        table, ptable = order[:len(q_lens) * width].view(len(q_lens), width), order[-len(plens) * ahead:].view(len(plens), ahead)
+        pq = max(b - a for a, b in zip(pcu, pcu[1:]))
+        i = [ints(v) for v in (pcu, plens, cu, kv_lens)]
+
+        def run():
+            cache = bf.KVCache(*(c.clone().view(torch.float8_e4m3fn) for c in codes), *(s.clone() for s in scales))
+            w = w0.clone()
+            o, lse = bf.bfp8_shared_prefix_attention(q, cache, ptable, i[0], i[1], pq, max(plens), table, i[2], i[3], max(q_lens),
+                                                     max(kv_lens), return_lse=True)
+            o2, l2 = bf.bfp8_paged_attention(q, cache, table, i[2], i[3], max(q_lens), max(kv_lens), return_lse=True)
+            bf.bfp8_kv_cache_weigh(q, lse, cache, w, table, i[2], i[3], max(q_lens), max(kv_lens))
+            lens = bf.bfp8_kv_cache_evict(cache, w, table, i[3], max(kv_lens), 20, recent=3)
+            return [o, lse, o2, l2, w, lens, cache.k.view(torch.uint8), cache.v_scale]
+        return run
+
+    calls = [case([300], [0, 3], [1] * 3, [5, 64, 129]), case([1500], [0, 20], [1] * 20, [3 * i + 1 for i in range(20)]),
+             case([700, 33], [0, 30, 33], [1] * 33, [i + 1 for i in range(33)]), case([260], [0, 150], [100, 50], [100, 400]),
+             case([515], [0, 88], [1, 40, 1, 45, 1], [300, 40, 1, 200, 77]), case([90, 2000], [0, 2, 60], [2] * 30, [17 + i for i in range(30)])]
+    alone = []
+    for call in calls:
+        alone.append(call())
+        torch.cuda.synchronize()
+    order = [i for _ in range(6) for i in torch.randperm(len(calls), generator=g).tolist()]
+    got = [calls[i]() for i in order]
+    torch.cuda.synchronize()
+    assert bf.bfp8_device_status() == 0
+    for i, r in zip(order, got):
+        assert all(torch.equal(a, b) for a, b in zip(r, alone[i])), i
