@@ -5,7 +5,7 @@
 //   a[h, j] = sum over query heads of kv head h, over new tokens i that see j, of exp(scale q_i . k_j - lse_i)
 //
 // With at most 16 rows (new tokens x heads of a kv head) it is bound by reading
-// the keys once.  The units (16 tokens of a sequence and kv head) of all
+// the keys once.  The units (32 tokens of a sequence and kv head, 16 where a page has no more) of all
 // sequences form one line; CTAs take equal shares of it and their warps turns in
 // it, each by itself: a token's sum is one warp's, so that nothing is joined.
 // The tokens are the 16-row operand of mma.sync.m16n8k16 (f16, fp32 sums), the
@@ -31,7 +31,6 @@ namespace bfp8 {
 
 namespace {
 
-constexpr int kUnit = 16;                  // tokens of a unit: never more than a page
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kItemCost = 8;               // places of a (sequence, head) in the line besides its units
 constexpr int kCtasPerSm = 2;
@@ -44,6 +43,7 @@ struct SeqWork {
   int32_t units;                           // of each kv head; 0: not this kernel's
 };
 
+template <int U>
 __device__ __forceinline__ SeqWork seq_work(const WeighArgs& p, int b, int max_rows) {
   const SeqLens s = seq_lens(p.a, b);
   SeqWork w;
@@ -57,7 +57,7 @@ __device__ __forceinline__ SeqWork seq_work(const WeighArgs& p, int b, int max_r
   w.t0 = p.add != 0 ? lo : 0;
   w.units = 0;
   if (s.q_len > 0 && static_cast<int64_t>(s.q_len) * p.a.group <= max_rows)
-    w.units = (s.kv_len + kUnit - 1) / kUnit - w.t0 / kUnit;
+    w.units = (s.kv_len + U - 1) / U - w.t0 / U;
   return w;
 }
 __device__ __forceinline__ int32_t line_cost(int32_t units) { return units > 0 ? units + kItemCost : 0; }
@@ -86,15 +86,16 @@ __device__ __forceinline__ void mma_f16_16x8x16(float (&d)[4], uint32_t a0, uint
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int D>
+template <int D, int U>
 struct FewCfg {
-  static constexpr int kKeys = kUnit * D;
-  static constexpr int kStages = D == 128 ? 5 : 8;                 // units of a warp on their way
-  static constexpr int kOffKs = kKeys;                             // scales of tokens g and g + 8 of each lane
-  static constexpr int kOffOld = kOffKs + 2 * 32 * 4;              // the sum so far of the token that the lane writes
+  static constexpr int kHalves = U / 16;                           // a unit's 16 tokens, of an MMA
+  static constexpr int kKeys = U * D;
+  static constexpr int kStages = D == 128 ? (U == 32 ? 3 : 5) : (U == 32 ? 5 : 8);      // units of a warp on their way
+  static constexpr int kOffKs = kKeys;                             // scales of tokens g and g + 8 of each half and lane
+  static constexpr int kOffOld = kOffKs + kHalves * 2 * 32 * 4;    // the sum so far of the token that the lane writes
   static constexpr int kStage = kOffOld + 32 * 4;
   static constexpr int kSmem = kWarps * kStages * kStage;
-  static_assert(kCtasPerSm * (kSmem + 4096) <= 227 * 1024, "shared memory of the CTAs of a SM");
+  static_assert(kCtasPerSm * (kSmem + 2560) <= 228 * 1024, "shared memory of the CTAs of a SM");
 };
 
 // 16 or 4 bytes into shared memory, zeros in place of a source that is not there.
@@ -124,9 +125,10 @@ struct Unit {
   int32_t tok, page;
 };
 
-template <int D, int NG>
+template <int D, int NG, int U>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const __grid_constant__ WeighArgs p) {
-  using C = FewCfg<D>;
+  using C = FewCfg<D, U>;
+  constexpr int NH = C::kHalves;
   constexpr int kRows = NG * 8;
   constexpr int KC = D / 64;               // 16-byte key chunks a lane reads of a token
   const AttnArgs& a = p.a;
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
   int32_t n0 = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     const int b = b0 + tid;
-    n0 = b < a.batch ? line_cost(seq_work(p, b, kRows).units) : 0;
+    n0 = b < a.batch ? line_cost(seq_work<U>(p, b, kRows).units) : 0;
     incl0 = block_scan(n0, part);
     if (tid == kThreads - 1) part[0] = incl0;
     __syncthreads();
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
     run = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
       const int b = b0 + tid;
-      const int32_t n = b < a.batch ? line_cost(seq_work(p, b, kRows).units) : 0;
+      const int32_t n = b < a.batch ? line_cost(seq_work<U>(p, b, kRows).units) : 0;
       const int64_t incl = run + block_scan(n, part);
       find(b, incl, n);
       if (tid == kThreads - 1) part[0] = incl;
@@ -179,9 +181,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
   }
   __syncthreads();
 
-  // the token whose sum this lane writes: g, or g + 8 (lanes t = 0 and 1)
+  // the token whose sum this lane writes (units of 16: lanes t = 0 and 1)
   const int out = g + 8 * t;
-  Cursor c;
+  Cursor c{};
   auto enter_head = [&]() {
     c.end = static_cast<int32_t>(c.item0 + c.units < u1 ? c.units : u1 - c.item0);
     c.keys = a.c.k + c.h * a.c.st_head + g * a.c.st_tok + 16 * t;
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
     c.sums = p.w + c.h * p.ws_head + out;
   };
   auto enter = [&](int b) {
-    const SeqWork w = seq_work(p, b, kRows);
+    const SeqWork w = seq_work<U>(p, b, kRows);
     c.b = b;
     c.units = w.units;
     c.t0 = w.t0;
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
     }
     n.b = c.b;
     n.h = c.h;
-    n.tok = (c.t0 / kUnit + c.k) * kUnit;
+    n.tok = (c.t0 / U + c.k) * U;
     n.page = __ldg(a.table + c.b * a.ld_table + (n.tok >> a.c.page_shift));
     c.k += kWarps;
     return n;
@@ -243,16 +245,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
       const float* scales = c.scales + page * a.c.ss_page + off;
       const uint32_t at = ring_at + slot * C::kStage;
       // (a whole unit, which most are, needs none of the comparisons)
-      const bool all = there && n.tok + kUnit <= c.kv_len;
+      const bool all = there && n.tok + U <= c.kv_len;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < 2 * NH; ++r) {                             // tokens 8 r + g
         const bool live = all || (there && n.tok + 8 * r + g < c.kv_len);
 #pragma unroll
         for (int h = 0; h < KC; ++h) copy16(at + ((r * KC + h) * 32 + lane) * 16, keys + 8 * r * a.c.st_tok + 64 * h, live);
         copy4(at + C::kOffKs + (r * 32 + lane) * 4, scales + 8 * r, live);
       }
       const int32_t j = n.tok + out;
-      if (t < 2)
+      if (t < 2 * NH)
         copy4(at + C::kOffOld + lane * 4, c.sums + page * p.ws_page + off, there && j < c.kv_len && !begins_here(p, j, c.pos0));
     }
     if (lane == 0) units[warp][slot] = n;
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
   auto queries = [&](const Unit& n) {
     q_b = n.b;
     q_h = n.h;
-    const SeqWork w = seq_work(p, n.b, kRows);
+    const SeqWork w = seq_work<U>(p, n.b, kRows);
     q_t0 = w.t0;
     q_end = w.kv_len;
     const int rows = w.q_len * a.group;
@@ -337,61 +339,57 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_few_kernel(const _
     if (n.b != q_b || n.h != q_h) queries(n);
     const uint8_t* at = ring + slot * C::kStage;
     const float* sc = reinterpret_cast<const float*>(at + C::kOffKs) + lane;
-    const float ks[2] = {sc[0], sc[32]};
-    float s[NG][KC][4];
+    float s[NH][NG][KC][4];
 #pragma unroll
-    for (int grp = 0; grp < NG; ++grp)
-#pragma unroll
-      for (int h = 0; h < KC; ++h) s[grp][h][0] = s[grp][h][1] = s[grp][h][2] = s[grp][h][3] = 0.f;
-#pragma unroll
-    for (int h = 0; h < KC; ++h) {
-      const uint4 ka = *reinterpret_cast<const uint4*>(at + (h * 32 + lane) * 16),
-                  kb = *reinterpret_cast<const uint4*>(at + ((KC + h) * 32 + lane) * 16);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t wa = x == 0 ? ka.x : x == 1 ? ka.y : x == 2 ? ka.z : ka.w;
-        const uint32_t wb = x == 0 ? kb.x : x == 1 ? kb.y : x == 2 ? kb.z : kb.w;
-        uint32_t a0, a1, a2, a3;
-        e4m3x4_to_f16(wa, a0, a2);
-        e4m3x4_to_f16(wb, a1, a3);
-#pragma unroll
-        for (int grp = 0; grp < NG; ++grp)
-          mma_f16_16x8x16(s[grp][h], a0, a1, a2, a3, qf[grp][h * 4 + x][0], qf[grp][h * 4 + x][1]);
-      }
-    }
-    float sum[2] = {0.f, 0.f};
-    const bool all = n.tok >= all_lo && n.tok + kUnit <= all_hi;
-#pragma unroll
-    for (int grp = 0; grp < NG; ++grp)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i >> 1, x = i & 1;
-        float v = s[grp][0][i];
-        if constexpr (KC == 2) v += s[grp][1][i];
-        s[grp][0][i] = ex2(fmaf(v, ks[r] * cq[grp][x], bias[grp][x]));
-      }
-    if (!all) {
+    for (int e = 0; e < NH; ++e)
 #pragma unroll
       for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int32_t j = n.tok + 8 * (i >> 1) + g;
-          if (j < lo[grp][i & 1] || j >= hi[grp][i & 1]) s[grp][0][i] = 0.f;
+        for (int h = 0; h < KC; ++h) s[e][grp][h][0] = s[e][grp][h][1] = s[e][grp][h][2] = s[e][grp][h][3] = 0.f;
+#pragma unroll
+    for (int h = 0; h < KC; ++h)
+#pragma unroll
+      for (int e = 0; e < NH; ++e) {
+        const uint4 ka = *reinterpret_cast<const uint4*>(at + ((2 * e * KC + h) * 32 + lane) * 16),
+                    kb = *reinterpret_cast<const uint4*>(at + (((2 * e + 1) * KC + h) * 32 + lane) * 16);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t wa = x == 0 ? ka.x : x == 1 ? ka.y : x == 2 ? ka.z : ka.w;
+          const uint32_t wb = x == 0 ? kb.x : x == 1 ? kb.y : x == 2 ? kb.z : kb.w;
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16(wa, a0, a2);
+          e4m3x4_to_f16(wb, a1, a3);
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp)
+            mma_f16_16x8x16(s[e][grp][h], a0, a1, a2, a3, qf[grp][h * 4 + x][0], qf[grp][h * 4 + x][1]);
         }
-    }
+      }
+    const bool all = n.tok >= all_lo && n.tok + U <= all_hi;
+    float sum[2 * NH];                                               // of tokens 8 r + g
 #pragma unroll
-    for (int grp = 0; grp < NG; ++grp)
+    for (int r = 0; r < 2 * NH; ++r) {
+      const float ks = sc[32 * r];
+      const int32_t j = n.tok + 8 * r + g;
+      sum[r] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[i >> 1] += s[grp][0][i];
+      for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+        for (int x = 0; x < 2; ++x) {
+          const int i = 2 * (r & 1) + x;
+          float v = s[r >> 1][grp][0][i];
+          if constexpr (KC == 2) v += s[r >> 1][grp][1][i];
+          v = ex2(fmaf(v, ks * cq[grp][x], bias[grp][x]));
+          if (!all && (j < lo[grp][x] || j >= hi[grp][x])) v = 0.f;
+          sum[r] += v;
+        }
       sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
       sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
     }
     const int32_t j = n.tok + out;
-    if (t < 2 && n.page >= 0 && j >= q_t0 && j < q_end)
-      p.w[n.page * p.ws_page + n.h * p.ws_head + (j & (a.c.page_size - 1))] =
-          reinterpret_cast<const float*>(at + C::kOffOld)[lane] + (t == 0 ? sum[0] : sum[1]);
+    float mine = t == 0 ? sum[0] : sum[1];
+    if constexpr (NH == 2) mine = t < 2 ? mine : t == 2 ? sum[2] : sum[3];
+    if (t < 2 * NH && n.page >= 0 && j >= q_t0 && j < q_end)
+      p.w[n.page * p.ws_page + n.h * p.ws_head + (j & (a.c.page_size - 1))] = reinterpret_cast<const float*>(at + C::kOffOld)[lane] + mine;
   };
 
   // a unit's page number is asked for a turn before its copies start
@@ -439,10 +437,10 @@ size_t workspace_bytes_for(int group, int max_q, int sms) {
 
 namespace {
 
-template <int D, int NG>
+template <int D, int NG, int U>
 cudaError_t launch_few(const WeighArgs& p, int ctas, cudaStream_t stream) {
-  using C = FewCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(weigh_few_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  using C = FewCfg<D, U>;
+  cudaError_t e = cudaFuncSetAttribute(weigh_few_kernel<D, NG, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas * kCtasPerSm));
@@ -454,14 +452,20 @@ cudaError_t launch_few(const WeighArgs& p, int ctas, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weigh_few_kernel<D, NG>, p);
+  return cudaLaunchKernelEx(&cfg, weigh_few_kernel<D, NG, U>, p);
+}
+
+template <int U>
+cudaError_t launch_few_of(const WeighArgs& p, int groups, int ctas, cudaStream_t stream) {
+  if (p.a.c.dim == 128) return groups == 1 ? launch_few<128, 1, U>(p, ctas, stream) : launch_few<128, 2, U>(p, ctas, stream);
+  return groups == 1 ? launch_few<64, 1, U>(p, ctas, stream) : launch_few<64, 2, U>(p, ctas, stream);
 }
 
 }  // namespace
 
+// (64 sequences of up to 8000 tokens on pages of 64, 64 / 8 heads of 128: 67.8 us in units of 16, 64.6 in units of 32)
 cudaError_t launch_weigh_few(const WeighArgs& p, int groups, int ctas, cudaStream_t stream) {
-  if (p.a.c.dim == 128) return groups == 1 ? launch_few<128, 1>(p, ctas, stream) : launch_few<128, 2>(p, ctas, stream);
-  return groups == 1 ? launch_few<64, 1>(p, ctas, stream) : launch_few<64, 2>(p, ctas, stream);
+  return p.a.c.page_size >= 32 ? launch_few_of<32>(p, groups, ctas, stream) : launch_few_of<16>(p, groups, ctas, stream);
 }
 
 }  // namespace bfp8
