@@ -998,7 +998,7 @@ def bfp8_kv_cache_evict(cache: KVCache, weights: torch.Tensor, block_table: torc
     the heaviest by weights [pages, kv_heads, page_size] (fp32, as bfp8_kv_cache_weigh sums them), in their order.
     They move with codes, scales and weights to the pages out_table (int32 [batch, max_pages], none of them among
     those of block_table; shorter sequences are copied whole), or, without one, to the first pages of block_table
-    (so too where out_table is block_table, or its first columns).
+    (so too where out_table is block_table or a view of its first columns; a copy of them is not, and not allowed).
     Returns the new lengths min(kv_lens, budget) (int32 [batch], into new_lens if given; not kv_lens itself)."""
     _, H, page, _ = cache.k.shape
     wp, wh = _weight_strides(weights, cache)

@@ -436,7 +436,9 @@ extern "C" bfp8_status bfp8_kv_cache_evict(const bfp8_evict_args* p, const bfp8_
   a.ws_head = p->weights_stride_head;
   a.table = p->block_table;
   a.ld_table = p->ld_table;
-  const bool in_place = p->out_table == nullptr || (p->out_table == p->block_table && p->ld_out == p->ld_table);
+  // (one sequence's table may come with any stride, whose rows nobody looks for)
+  const bool in_place =
+      p->out_table == nullptr || (p->out_table == p->block_table && (p->batch == 1 || p->ld_out == p->ld_table));
   a.out_table = in_place ? p->block_table : p->out_table;
   a.ld_out = in_place ? p->ld_table : p->ld_out;
   a.lens = p->kv_lens;

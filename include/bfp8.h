@@ -679,9 +679,9 @@ bfp8_status bfp8_kv_cache_weigh_workspace_size(int num_heads, int num_kv_heads, 
  *            tokens move to, max_out_pages * page_size >= min(budget, max_kv_len).  None of them is among the
  *            pages that block_table holds for the call's sequences.  A sequence of at
  *            most budget tokens is copied whole.  The pages that it came from are left as they were.
- *            NULL, or block_table itself with the same stride: in place, to the first pages of
- *            block_table (a sequence of at most budget tokens stays as it is); places behind the
- *            budget are left as they were.
+ *            NULL, or block_table itself (the same address, and the same stride unless batch == 1): in place,
+ *            to the first pages of block_table (a sequence of at most budget tokens stays as it is);
+ *            places behind the budget are left as they were.
  *   weights  as for bfp8_kv_cache_weigh.
  *   kv_lens, new_lens   device int32 [batch], not overlapping.
  *   max_kv_len   host upper bound of the lengths.

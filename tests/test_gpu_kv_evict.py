@@ -170,6 +170,25 @@ def test_block_table_as_its_own_destination(dev):
         assert torch.equal(d["k"].view(torch.uint8).cpu(), want[0]) and torch.equal(d["w"].cpu(), want[1])
 
 
+@pytest.mark.parametrize("H,D,page", [(1, 128, 64), (8, 128, 16), (2, 64, 64)])
+@pytest.mark.parametrize("n,budget", [(1300, 600), (9000, 2500)])
+def test_one_sequence_onto_the_first_columns_of_its_table(dev, n, budget, H, D, page):
+    """In place too, although a single row's stride says nothing: many more rows than a block moves at a time."""
+    c = make([n], budget, H, D, page)
+    parts = [c["k"].view(torch.uint8), c["v"].view(torch.uint8), c["ks"], c["vs"], c["w"]]
+    want, lens = evict_ref(parts, c["w"], c["table"], c["kv"], budget, 7, 1)
+    wide = torch.full((1, c["table"].shape[1] + 3), -9, dtype=torch.int32)
+    wide[:, :-3] = c["table"]
+    for columns in ((budget + page - 1) // page, (n + page - 1) // page, wide.shape[1]):
+        d = [x.to(dev) for x in parts]
+        table = wide.to(dev)
+        got = bf.bfp8_kv_cache_evict(bf.KVCache(*(x.view(torch.float8_e4m3fn) for x in d[:2]), *d[2:4]), d[4], table, ints(c["kv"], dev), n,
+                                     budget, recent=7, first=1, out_table=table[:, :columns])
+        assert got.tolist() == lens
+        assert all(torch.equal(x.cpu(), y) for x, y in zip(d, want)), columns
+    assert bf.bfp8_device_status() == 0
+
+
 def test_lengths_for_the_caller(dev):
     c = make([300, 80], 64)
     lens = torch.empty(2, dtype=torch.int32, device=dev)
