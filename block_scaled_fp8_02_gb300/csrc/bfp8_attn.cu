@@ -63,6 +63,12 @@ size_t shared_scratch_bytes(int group, int dim, int max_prefix_q, int max_q, int
 size_t shared_rows_bytes(int64_t total_q, int heads, int dim, bool apart) {
   return static_cast<size_t>(total_q) * heads * (dim + 1) * sizeof(float) * (apart ? 2 : 1);
 }
+// The new tokens, up to max_q, with which a call has the most partial rows of the kernel for few rows: those of all sequences at
+// once, where more tokens leave it single ones.
+int most_few_q(int group, int max_q) {
+  const int q = group < kFewRows ? kFewRows / group : 1;
+  return max_q < q ? max_q : q;
+}
 
 // Sequences (or prefixes), rows and context of a call, checked apart from the pointers.
 bfp8_status check_context(const char* what, int batch, int max_q, int max_pages, int64_t ld_table, int64_t max_kv, int page,
@@ -313,8 +319,13 @@ extern "C" bfp8_status bfp8_shared_prefix_attention_workspace_size(int num_heads
   int sms = 0;
   int* err = nullptr;
   if ((st = device_for_call(&sms, &err)) != BFP8_OK) return st;
-  *bytes = shared_scratch_bytes(num_heads / num_kv_heads, head_dim, max_prefix_q_len, max_q_len, sms) +
-           shared_rows_bytes(total_q, num_heads, head_dim, parts_apart(num_heads / num_kv_heads, max_prefix_q_len, max_q_len));
+  // what calls below the bounds need too
+  const int group = num_heads / num_kv_heads;
+  const int pq = most_few_q(group, max_prefix_q_len), q = most_few_q(group, max_q_len);
+  const bool tile = has_many(group, max_prefix_q_len) || has_many(group, max_q_len);
+  *bytes = kCounterHeaderBytes + few_bytes(group, head_dim, pq, sms) + few_bytes(group, head_dim, q, sms) +
+           (tile ? attn_tile_partial_bytes(head_dim, sms) : 0) +
+           shared_rows_bytes(total_q, num_heads, head_dim, parts_apart(group, max_prefix_q_len, max_q_len));
   return set_last_error(BFP8_OK, "");
 }
 
@@ -340,17 +351,21 @@ extern "C" bfp8_status bfp8_shared_prefix_attention(const bfp8_attention_args* p
       return set_last_errorf(BFP8_ERR_ALIGNMENT, "prefix: pointers must be 4-byte aligned");
   }
   int sms = 0;
-  const int pq = none ? a.max_q : f->max_q_len;
-  const bool apart = !none && parts_apart(a.group, pq, a.max_q);
-  const size_t rows = none ? 0 : shared_rows_bytes(a.total_q, a.heads, a.c.dim, apart);
-  st = check_workspace(workspace, workspace_bytes, &sms, &a.err,
-                       [&](int n) { return shared_scratch_bytes(a.group, a.c.dim, pq, a.max_q, n) + rows; });
+  auto scratch = [&](int n) {
+    return none ? workspace_bytes_for(a.group, a.c.dim, a.max_q, n)
+                : shared_scratch_bytes(a.group, a.c.dim, f->max_q_len, a.max_q, n);
+  };
+  const size_t rows = none ? 0 : shared_rows_bytes(a.total_q, a.heads, a.c.dim, false);
+  st = check_workspace(workspace, workspace_bytes, &sms, &a.err, [&](int n) { return scratch(n) + rows; });
   if (st != BFP8_OK) return st;
+  // (a workspace for more new tokens a sequence, whose parts are joined at once, need not hold both parts' rows)
+  const bool apart =
+      !none && parts_apart(a.group, f->max_q_len, a.max_q) && workspace_bytes >= scratch(sms) + 2 * rows;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   // counters: one a CTA of either kernel for few rows, two of the other (4 * sms fit the header)
   int32_t* counters = static_cast<int32_t*>(workspace);
   char* partials = static_cast<char*>(workspace) + kCounterHeaderBytes;
-  const size_t few_prefix = few_bytes(a.group, a.c.dim, pq, sms), few_own = few_bytes(a.group, a.c.dim, a.max_q, sms);
+  const size_t few_prefix = none ? 0 : few_bytes(a.group, a.c.dim, f->max_q_len, sms), few_own = few_bytes(a.group, a.c.dim, a.max_q, sms);
   float* const tile = reinterpret_cast<float*>(partials + few_prefix + few_own);
   const Scratch w_prefix{counters, reinterpret_cast<float*>(partials), counters + sms, tile},
       w_own{counters + 3 * sms, reinterpret_cast<float*>(partials + few_prefix), counters + sms, tile};
@@ -362,7 +377,7 @@ extern "C" bfp8_status bfp8_shared_prefix_attention(const bfp8_attention_args* p
   }
   // rows of one part or both (whole rows: read and written in vectors), then their sums
   const int64_t row_floats = a.total_q * a.heads * a.c.dim;
-  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + shared_scratch_bytes(a.group, a.c.dim, pq, a.max_q, sms));
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + scratch(sms));
   a.part_lse2 = a.part_o + (apart ? 2 : 1) * row_floats;
   a.part_cu = f->cu_q;
   a.prefixes = f->prefixes;
@@ -378,7 +393,7 @@ extern "C" bfp8_status bfp8_shared_prefix_attention(const bfp8_attention_args* p
   b.window = 0;
   // The own part runs beside the prefixes' where each is one launch, that of the own part for few rows: apart, or joining its rows itself
   // where the prefixes' are few too (4 sequences, up to 40 own tokens behind 500: 28.9 us one behind the other, 25.7 so).
-  const bool beside = !has_many(a.group, a.max_q) && !(has_many(b.group, b.max_q) && few_launched(b));
+  const bool beside = !has_many(a.group, a.max_q) && (!has_many(b.group, b.max_q) || (apart && !few_launched(b)));
   const int ctas = beside ? prefix_sms(a, b, sms) : sms;
   if ((st = launch_part(m, b, kAttnPart, ctas, w_prefix, false, cs)) != BFP8_OK) return st;
   if (!(beside && apart)) {

@@ -626,7 +626,9 @@ bfp8_status bfp8_shared_prefix_attention(const bfp8_attention_args* args, const 
                                          size_t workspace_bytes, void* stream);
 
 /* Workspace bytes bfp8_shared_prefix_attention needs on the current device for up
- * to max_prefix_q_len rows a prefix, max_q_len new tokens a sequence and total_q rows. */
+ * to max_prefix_q_len rows a prefix, max_q_len new tokens a sequence and total_q rows.  (A
+ * call with fewer new tokens than the bound may compute its parts one after the other where the
+ * bytes of its own bounds would have let them run beside each other.) */
 bfp8_status bfp8_shared_prefix_attention_workspace_size(int num_heads, int num_kv_heads, int head_dim,
                                                         int max_prefix_q_len, int max_q_len,
                                                         int64_t total_q, size_t* bytes);

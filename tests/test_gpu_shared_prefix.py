@@ -183,6 +183,33 @@ def test_captured_with_other_lengths(dev):
     assert bf.bfp8_device_status() == 0
 
 
+# bounds of the workspace (rows a prefix, new tokens a sequence), and prefixes, rows, new and own tokens of calls within them
+WITHIN = [
+    ((200, 100), ([700], [0, 200], [1] * 200, [3 * i % 90 + 1 for i in range(200)])),
+    ((200, 100), ([700], [0, 200], [4] * 50, [3 * i + 4 for i in range(50)])),
+    ((200, 100), ([300, 90], [0, 2, 200], [8] * 25, [3 * i + 8 for i in range(25)])),
+    ((200, 100), ([300], [0, 8], [8], [100])),
+    ((200, 100), ([300], [0, 190], [90, 100], [100, 300])),
+    ((200, 1), ([300], [0, 7], [1] * 7, [40] * 7)),
+    ((1, 8), ([], [0], [8, 1], [50, 300])),
+    ((1, 100), ([], [0], [8, 7], [50, 300])),
+]
+
+
+@pytest.mark.parametrize("i", range(len(WITHIN)))
+def test_a_workspace_for_larger_bounds(dev, i):
+    """A workspace of the size for some bounds serves every call within them, and no byte behind it is touched."""
+    (pq, mq), lens = WITHIN[i]
+    Hq, H, D = 8, 2, 128
+    host, args = make(dev, *lens, Hq=Hq, H=H, D=D)
+    n = bf.bfp8_shared_prefix_attention_workspace_size(Hq, H, D, pq, mq, args[0].shape[0])
+    assert n >= bf.bfp8_shared_prefix_attention_workspace_size(Hq, H, D, args[5], args[10], 0)
+    buf = torch.zeros(n + 4096, dtype=torch.uint8, device=dev)
+    buf[n:] = 0x5A
+    check(host, args, workspace=buf[:n])
+    assert (buf[n:] == 0x5A).all()
+
+
 def test_pages_outside_the_cache(dev):
     host, args = make(dev, [300], [0, 12], [1] * 12, [40] * 12)
     bad = args[2].clone()
