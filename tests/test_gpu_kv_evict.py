@@ -127,6 +127,16 @@ def test_longer_than_a_cluster_holds(dev):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
+def test_many_sequences_longer_than_a_small_block_holds(dev, in_place):
+    """More (sequence, head)s than SMs, so small blocks, some of whose keys do not fit them: those are read anew."""
+    lens = [50 + i for i in range(200)]
+    lens[3], lens[77], lens[199] = 8192, 8193, 21000
+    c = make(lens, 300, H=1, D=64, page=256)
+    check(dev, c, recent=20, first=3, in_place=in_place)
+    check(dev, make(lens, 60, H=1, D=64, page=256, coarse=True), in_place=in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
 def test_orders_and_strides(dev, in_place):
     c = make([300, 80, 64], 64, H=3)
     check(dev, c, recent=9, in_place=in_place, order="pthd")
