@@ -892,7 +892,8 @@ def bfp8_shared_prefix_attention(q: torch.Tensor, cache: KVCache, prefix_table: 
     are seen by the rows prefix_cu_q[f] .. prefix_cu_q[f+1] of q (int32 [prefixes + 1]; max_prefix_q_len bounds how many
     they are, max_prefix_len the lengths).  block_table, cu_q, kv_lens and their bounds are those of the sequences' own
     tokens behind the prefix.  Returns out or (out, lse), of one softmax over both parts.  (The workspace holds the
-    prefixes' part in fp32, and in some calls the own one: up to 8 (head_dim + 1) bytes a row and head.)"""
+    prefixes' part in fp32, and in some calls the own one: 4 or 8 (head_dim + 1) bytes a row and head, 1.1 GB for 32768
+    rows of 64 heads of 128.  A stream's own workspace keeps the largest call's size until drop_workspaces.)"""
     _check_query(q, cache)
     _, H, _, D = cache.k.shape
     qs, dev = q.shape, q.device
@@ -955,7 +956,8 @@ def bfp8_kv_cache_weigh(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, weig
     the new tokens q, summed over them and over the query heads of a kv head.  lse [total_q, heads] (fp32) is what
     bfp8_paged_attention or bfp8_shared_prefix_attention returned for the same q; the other arguments are as
     there.  With accumulate the sums of the new tokens begin here (causal) and those of the earlier ones go on; without
-    it all sums of the context begin here."""
+    it all sums of the context begin here.  Unlike in attention, no page may stand in two sequences' tables of one
+    call (their sums would overwrite each other's): what sequences share is weighed once, as a prefix."""
     _check_query(q, cache)
     _, H, _, D = cache.k.shape
     T, Hq, _ = q.shape
@@ -999,6 +1001,7 @@ def bfp8_kv_cache_evict(cache: KVCache, weights: torch.Tensor, block_table: torc
     They move with codes, scales and weights to the pages out_table (int32 [batch, max_pages], none of them among
     those of block_table; shorter sequences are copied whole), or, without one, to the first pages of block_table
     (so too where out_table is block_table or a view of its first columns; a copy of them is not, and not allowed).
+    No page may stand in two sequences' tables of one call.
     Returns the new lengths min(kv_lens, budget) (int32 [batch], into new_lens if given; not kv_lens itself)."""
     _, H, page, _ = cache.k.shape
     wp, wh = _weight_strides(weights, cache)

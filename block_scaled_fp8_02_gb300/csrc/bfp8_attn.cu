@@ -50,7 +50,7 @@ size_t workspace_bytes_for(int group, int dim, int max_q, int sms) {
 
 // Are both parts of a call over shared prefixes computed apart, beside each other, and joined in a launch of their own?  Where the
 // prefixes' takes the tile kernel and the own one the kernel for few rows: many sequences' single tokens.  64 of them, own contexts up
-// to 1000 behind a prefix of 8192, 64 / 8 heads of 128: 98 us with the own part's rows waiting for the prefix's, 76 apart.  (With more
+// to 1000 behind a prefix of 8192, 64 / 8 heads of 128: 98 us with the own part's rows waiting for the prefix's, 75 apart.  (With more
 // new tokens the parts' fp32 rows would take longer to write and read than the wait; with fewer the third launch would.)
 bool parts_apart(int group, int max_prefix_q, int max_q) { return has_many(group, max_prefix_q) && !has_many(group, max_q); }
 // Scratch of such a call: each part's partial rows of the kernel for few rows, and those of the other, which only one takes at a time.
@@ -124,7 +124,8 @@ bool few_launched(const AttnArgs& a) {
 // SMs that the prefixes' part `b` gets where the own part `a` (by the kernel for few rows) runs beside it: by the cycles that each needs
 // at its bounds (contexts of the kernel for few rows at three quarters of theirs), a block's and an item's own among them.  64 sequences, own
 // contexts up to 1000 behind 8192 tokens, 64 / 8 heads of 128, by the tile kernel's SMs: 48 81 us, 64 69, 80 71, 96 78, 112 104; 79
-// with the kernel for few rows behind the other, on the SMs that it leaves.
+// with the kernel for few rows behind the other, on the SMs that it leaves.  (The cycles are those of that shape, for heads of 64 too, and the
+// bounds are the caller's: loose ones move the split towards its ends.)
 int prefix_sms(const AttnArgs& a, const AttnArgs& b, int sms) {
   auto few = [](const AttnArgs& x) {
     return static_cast<double>(x.batch) * x.c.heads * (0.75 * static_cast<double>(x.max_kv) / 128 + 4) * 1340;

@@ -121,6 +121,10 @@ bfp8_status check_attention(const bfp8_attention_args* p, AttnArgs* a, bool* emp
 // k, v: tensor maps [dim, token, head, page] of bytes, boxes of min(page_size, 128) tokens.
 // behind 1: the launch before it in the stream is launch_attn_tile's of the same part; the two run beside each other.
 // behind 2: it is that of the prefixes' part, by either kernel; they run beside each other (kAttnOwn: until rows are joined).
+// A launch with `behind` touches memory without having waited.  That is sound for two reasons, which any launch put between the two
+// or any earlier signal would break: the one before it lets it begin only after its own wait (the tile kernel always, this one as
+// kAttnPart with behind 0), so that all before that is done; and it waits in its turn before it ends, so that what follows it finds both done.
+// Every other kernel of the attention and the cache waits before it touches memory, and may let the next begin at any time.
 int attn_decode_groups(int64_t rows);
 size_t attn_decode_partial_bytes(int groups, int dim, int ctas);
 cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, AttnMode mode, int groups, int ctas,

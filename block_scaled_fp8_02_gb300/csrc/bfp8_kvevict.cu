@@ -30,7 +30,9 @@ constexpr int kBins = 2048;
 // Threads of a CTA that looks for the kept positions, and keys that each holds (a longer stretch is read anew each time).
 // Many (sequence, head)s: small CTAs, four a SM (64 x 8 heads of 8000 tokens 28 us, 36 in clusters of two).  Few: large
 // ones (16 x 8 heads 11 us, 19 with small ones), in clusters where their keys are too many for one (a cluster's barriers cost about
-// a microsecond each, so no more CTAs than the keys need).
+// a microsecond each, so no more CTAs than the keys need).  The choice goes by the number of (sequence, head)s alone: small CTAs read what is
+// past their 8192 keys anew in each pass (64 x 8 heads to 2048 tokens, the whole call: 110 us from up to 8000, 170 from 16384, 255 from
+// 32768, where the moving is much the same).
 template <int T>
 struct Find {
   static constexpr int kWarps = T / 32, kHold = T == 256 ? 32 : 16, kChunk = kHold * T, kCtasPerSm = T == 256 ? 4 : 1;
