@@ -193,6 +193,9 @@ WITHIN = [
     ((200, 1), ([300], [0, 7], [1] * 7, [40] * 7)),
     ((1, 8), ([], [0], [8, 1], [50, 300])),
     ((1, 100), ([], [0], [8, 7], [50, 300])),
+    # (9.9 MB of rows: more than the size has over what this call's partial rows take, so that both parts' do not fit)
+    ((2400, 100), ([130], [0, 2400], [4] * 600, [4 + i % 9 for i in range(600)])),
+    ((2400, 100), ([130, 5], [0, 2396, 2400], [4] * 600, [4 + i % 9 for i in range(600)])),
 ]
 
 
